@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -8,3 +9,10 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a B200 (sm_100a) GPU and the built CUDA library")
+
+
+def pytest_runtest_setup(item):
+    # The device tensors of earlier tests that sit in reference cycles (the traceback of an expected error holds
+    # its frame) are freed here, not by a collection in the middle of a test that compares allocated bytes.
+    if item.get_closest_marker("gpu"):
+        gc.collect()
