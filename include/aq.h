@@ -403,6 +403,131 @@ int aq_linear_group(int phase, const aq_packed* const* w, int G, const uint16_t*
 size_t aq_group_workspace_bytes(int phase, int M, const aq_packed* const* w, int G);
 
 /*
+ * Low-rank adapters beside a shared projection: L adapters of one N x K
+ * projection, adapter l adding scale[l] B_l A_l to the projection's weights.
+ * The tables hold the adapters' rows one after another; adapter l owns rows
+ * off[l] .. off[l+1]-1, its rank (0 .. max_rank; 0: it leaves this projection
+ * alone).
+ *  a      bf16 [R][K] (bits as uint16), row off[l] + i = row i of A_l (r_l x K)
+ *  bt     bf16 [R][N], row off[l] + i = column i of B_l (N x r_l)
+ *  off    int32 [L+1] non-decreasing, off[0] = 0, off[L] = R
+ *  scale  fp32 [L]
+ *  max_rank  largest rank, 1 .. 256
+ * All device pointers; a and bt 16-byte aligned, off and scale 4-byte.
+ * N and K multiples of 8 up to 1048576; 1 <= L <= 16383.
+ */
+typedef struct aq_lora {
+  int32_t N, K, L, R, max_rank;
+  const uint16_t* a;
+  const uint16_t* bt;
+  const int32_t* off;
+  const float* scale;
+} aq_lora;
+
+/*
+ * Adapters of many requests at once.  With l = ids[m], the adapter of token m:
+ *   S[m][i]   = scale[l] * sum_k x[m][k] A_l[i][k]
+ *   out[m][n] = y[m][n] + sum_i S[m][i] B_l[n][i]
+ * in fp32, out rounded once.  A token whose id is outside [0, L) (-1 by
+ * convention) or whose adapter has rank 0 gets out = y.  Tokens may carry ids
+ * in any order; tokens of one request next to one another are the fast case
+ * (each run of 64 tokens costs one pass per adapter that occurs in it).  A
+ * token's result depends on its own activations and adapter alone, also where
+ * others hold infinities or NaN.
+ *  x     bf16 [M][ldx], ldx % 8 == 0, ldx >= K
+ *  ids   int32 [M]
+ *  y     the projection's output [M][ldy], fp32 or bf16 (ydtype), or NULL (out = the
+ *        adapters' part alone)
+ *  out   [M][ldo], same dtype; may be y itself, otherwise must not overlap an input
+ *  s     fp32 [M][max_rank] or NULL: receives S (zeros behind a token's rank), which
+ *        aq_lora_backward takes
+ *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned; its contents
+ *        need no initialization, and calls that share it must not run concurrently
+ * Rows are 16-byte aligned: x, y, out on 16 bytes, ld % 8 == 0 (bf16) or
+ * ld % 4 == 0 (fp32).  1 <= M <= 4194240.  Asynchronous.
+ * Errors: AQ_ERR_ARG, AQ_ERR_SHAPE (N, K, L, R, max_rank), AQ_ERR_WORKSPACE, AQ_ERR_CUDA.
+ */
+int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y, int ldy,
+                  void* out, int ldo, int ydtype, float* s, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of aq_lora_apply, from the output's gradient dy and the products S
+ * that the forward pass kept.  The activations come as the 8-bit checkpoint the
+ * shared projection was given (codes and token scales of aq_quant_act: x =
+ * sx[m] xq[m][k]) or, with sx NULL, as bf16.  With T[m][i] = scale[l] * sum_n
+ * dy[m][n] B_l[n][i]:
+ *   da[off[l]+i][k]  = sum over tokens m of adapter l of T[m][i] x[m][k]
+ *   dbt[off[l]+i][n] = sum over tokens m of adapter l of S[m][i] dy[m][n]
+ *   dx[m][k]         = add[m][k] + sum_i T[m][i] A_l[i][k]
+ * in fp32; an adapter that no token has gets zeros.  Sums are formed in a fixed
+ * order: results are bitwise reproducible on a given GPU.
+ *  dy    bf16 [M][ldd], ldd % 8 == 0, ldd >= N
+ *  s     fp32 [M][max_rank], from aq_lora_apply
+ *  x     int8 [M][ldx] (ldx % 16 == 0, K % 16 == 0) with sx fp32 [M], or bf16 [M][ldx] (ldx % 8 == 0)
+ *  da    fp32 [R][K], dbt fp32 [R][N], 16-byte aligned, written
+ *  add   [M][ldadd] of dxdtype or NULL (zero), e.g. aq_linear_backward's result
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype), or NULL (not wanted); may be add itself
+ *  ws    >= aq_lora_workspace_bytes(ad, M, 1) bytes, as for aq_lora_apply
+ * Alignment, M and errors as for aq_lora_apply.
+ */
+int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M, const float* s,
+                     const void* x, int ldx, const float* sx, float* da, float* dbt, const void* add, int ldadd,
+                     void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Host only.  Workspace bytes of aq_lora_apply (backward 0) or aq_lora_backward (1); 0 when invalid. */
+size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward);
+
+/*
+ * Gated activation between the gate/up and the down projection, straight to the
+ * down projection's input codes: h = gate / (1 + exp(-gate)) * up, and for every
+ * token its codes and scale,
+ *   s = max(max_f |h[m][f]| * R, 1e-12), R = fl64(1 / 127);  hq = clamp(rint(h / s), -127, 127);  sh[m] = (float)s
+ * with h, s and the quotient in fp64 (h is not rounded to bf16 in between).  It is
+ * aq_quant_act's rule up to the last fp64 bit of s.
+ * gq, gs, uq, us (all or none): 8-bit checkpoints of gate and up for the backward
+ * pass, the same rule with one scale per 128 features of a row (the last group
+ * may be shorter).
+ *  gate, up  bf16 [M][ldg], [M][ldu], 16-byte aligned, ld % 8 == 0
+ *  hq, gq, uq  int8 [M][F], 16-byte aligned;  sh fp32 [M];  gs, us fp32 [M][ceil(F/128)]
+ * 1 <= M, 16 <= F <= 65536 with F % 16 == 0.  A row that holds an infinity or NaN
+ * gets unspecified codes; other rows are not touched by it.  Asynchronous, no
+ * workspace.  Errors: AQ_ERR_ARG, AQ_ERR_CUDA.
+ */
+int aq_silu_mul_quant(const uint16_t* gate, int ldg, const uint16_t* up, int ldu, int M, int F, int8_t* hq, float* sh,
+                      int8_t* gq, float* gs, int8_t* uq, float* us, void* stream);
+
+/*
+ * Backward of the gated activation from its checkpoints: with g = gs gq,
+ * u = us uq, p = 1 / (1 + exp(-g)),
+ *   dgate = dh u p (1 + g (1 - p)),   dup = dh g p        (fp32, rounded once to bf16)
+ *  dh  bf16 [M][ldd];  dgate, dup bf16 [M][ldg], [M][ldu]; 16-byte aligned, ld % 8 == 0
+ * The rounding of h to its codes is passed through.  Limits and errors as for
+ * aq_silu_mul_quant.
+ */
+int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const float* gs, const int8_t* uq,
+                         const float* us, int M, int F, uint16_t* dgate, int ldg, uint16_t* dup, int ldu,
+                         void* stream);
+
+/*
+ * Input gradient of a packed projection (its weights are frozen):
+ *   dx[m][k] = add[m][k] + sum_n dy[m][n] sw[n][k / 128] q[n][k]
+ *  w     as for aq_linear_prefill
+ *  dy    bf16 [M][ldd], 16-byte aligned, ldd % 8 == 0, ldd >= N
+ *  add   [M][ldadd] of dxdtype or NULL (zero): e.g. the gradient through another
+ *        projection of the same input
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself
+ *  ws    >= aq_linear_backward_workspace_bytes(M, w) bytes, 16-byte aligned,
+ *        zero-filled once as for the linear calls; errors by aq_workspace_status
+ * 1 <= M <= 2097152.  Asynchronous.
+ * Errors: AQ_ERR_ARG, AQ_ERR_SHAPE, AQ_ERR_WORKSPACE, AQ_ERR_CUDA.
+ */
+int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd, void* dx,
+                       int lddx, int dxdtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Host only.  Workspace bytes of aq_linear_backward; 0 when invalid. */
+size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w);
+
+/*
  * Decode-phase linear layer for callers that cannot allocate device memory
  * (code running inside an allocator or memory-pool callback, runtimes that
  * forbid allocation after start-up to keep a fixed footprint, plug-ins handed

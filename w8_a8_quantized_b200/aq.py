@@ -26,7 +26,8 @@ EXPORTED = ("aq_status_str", "aq_packed_sizes", "aq_pack_metadata", "aq_pack", "
             "aq_quantize_weights", "aq_paper_packed_bytes", "aq_expanded_bytes", "aq_expand_int8",
             "aq_linear_prefill_expanded", "aq_act_group_rows", "aq_quant_act_groups", "aq_measure_i8_peak",
             "aq_debug_linear_stalled", "aq_pack_tiles", "aq_paper_quant_act", "aq_paper_linear",
-            "aq_debug_paper_partials")
+            "aq_debug_paper_partials", "aq_lora_apply", "aq_lora_backward", "aq_lora_workspace_bytes",
+            "aq_silu_mul_quant", "aq_silu_mul_backward", "aq_linear_backward", "aq_linear_backward_workspace_bytes")
 
 
 class AqError(RuntimeError):
@@ -41,6 +42,11 @@ AQ_SCALES_ROW_FP16, AQ_SCALES_TILE_FP32 = 0, 1
 class AqPackedStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "bN", "bK", "R", "C", "T4", "T8")] + \
                [(n, ctypes.c_void_p) for n in BUF_NAMES] + [("scale_kind", ctypes.c_int32)]
+
+
+class AqLoraStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "L", "R", "max_rank")] + \
+               [(n, ctypes.c_void_p) for n in ("a", "bt", "off", "scale")]
 
 
 _lib = None
@@ -115,6 +121,25 @@ def lib():
     L.aq_measure_i8_peak.argtypes = [c_int, ctypes.POINTER(ctypes.c_double), c_void_p]
     L.aq_workspace_status.restype = c_int
     L.aq_workspace_status.argtypes = [c_void_p, c_void_p, ctypes.POINTER(c_int)]
+    A = ctypes.POINTER(AqLoraStruct)
+    L.aq_lora_apply.restype = c_int
+    L.aq_lora_apply.argtypes = [A, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_void_p,
+                                c_void_p, c_size_t, c_void_p]
+    L.aq_lora_backward.restype = c_int
+    L.aq_lora_backward.argtypes = [A, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_void_p, c_size_t, c_void_p]
+    L.aq_lora_workspace_bytes.restype = c_size_t
+    L.aq_lora_workspace_bytes.argtypes = [A, c_int, c_int]
+    L.aq_silu_mul_quant.restype = c_int
+    L.aq_silu_mul_quant.argtypes = [c_void_p, c_int, c_void_p, c_int, c_int, c_int] + [c_void_p] * 7
+    L.aq_silu_mul_backward.restype = c_int
+    L.aq_silu_mul_backward.argtypes = [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p,
+                                       c_int, c_void_p, c_int, c_void_p]
+    L.aq_linear_backward.restype = c_int
+    L.aq_linear_backward.argtypes = [P, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_void_p,
+                                     c_size_t, c_void_p]
+    L.aq_linear_backward_workspace_bytes.restype = c_size_t
+    L.aq_linear_backward_workspace_bytes.argtypes = [c_int, P]
     _lib = L
     return L
 
@@ -294,7 +319,8 @@ def aq_debug_paper_partials(w: PackedWeights, xq: torch.Tensor, M: int) -> torch
     P = torch.zeros((M, w.N, w.C), dtype=torch.int32, device=dev)
     with torch.cuda.device(dev):
         _check(lib().aq_debug_paper_partials(ctypes.byref(w.struct), xq.data_ptr(), M, P.data_ptr(), _stream(dev)),
-               "aq_debug_paper_partials")
+               "aq_debug_paper_partials", "aq_lora_apply", "aq_lora_backward", "aq_lora_workspace_bytes",
+            "aq_silu_mul_quant", "aq_silu_mul_backward", "aq_linear_backward", "aq_linear_backward_workspace_bytes")
     return P
 
 
@@ -567,6 +593,279 @@ class Group:
             _check(lib().aq_linear_group(self.phase, self._w, G, x.data_ptr(), x.stride(0), self.M, bs, ys, lds,
                                          ydt, ws.data_ptr(), ws.numel(), _stream(dev)), "aq_linear_group")
         return outs
+
+
+# ------------------------------------------------------------------ adapters, gated activation, gradients
+
+AQ_LORA_MAX_RANK = 256
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int):
+    """A 2-D [>= M][>= width] tensor with unit inner stride whose rows the kernels
+    read or write through a leading dimension."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must live on {device if device is not None else 'a CUDA device'}")
+    if t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < M or t.shape[1] < width or \
+            (t.shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{name} must be [>= {M}][>= {width}] with unit inner stride and rows that do not overlap")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension; a single row's stride says nothing, so its width stands in."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+
+
+class Adapters:
+    """Low-rank adapters of one N x K projection, laid out for aq_lora_apply.
+
+    a bf16 [R][K] and bt bf16 [R][N] hold the adapters' rows one after another
+    (adapter l: ranks[l] rows of A_l, and as many columns of B_l); they are used in
+    place, so an optimizer may update them.  scales: one factor per adapter."""
+
+    def __init__(self, a: torch.Tensor, bt: torch.Tensor, ranks, scales):
+        _need(a, "a", torch.bfloat16)
+        _need(bt, "bt", torch.bfloat16, a.device)
+        self.ranks, self.scales = [int(r) for r in ranks], [float(s) for s in scales]
+        if a.dim() != 2 or bt.dim() != 2 or a.shape[0] != bt.shape[0] or a.shape[0] != sum(self.ranks):
+            raise ValueError("a [R][K] and bt [R][N] must hold sum(ranks) rows")
+        if len(self.ranks) != len(self.scales) or min(self.ranks, default=-1) < 0 or max(self.ranks, default=0) < 1:
+            raise ValueError("one rank >= 0 and one scale per adapter, not all ranks 0")
+        if max(self.ranks) > AQ_LORA_MAX_RANK:
+            raise ValueError(f"ranks above {AQ_LORA_MAX_RANK} are not supported")
+        self.a, self.bt, self.device = a, bt, a.device
+        off = np.concatenate([[0], np.cumsum(self.ranks)]).astype(np.int32)
+        self.off = torch.from_numpy(off).to(self.device)
+        self.scale = torch.tensor(self.scales, dtype=torch.float32, device=self.device)
+        self.struct = AqLoraStruct(N=bt.shape[1], K=a.shape[1], L=len(self.ranks), R=a.shape[0],
+                                   max_rank=max(self.ranks), a=a.data_ptr(), bt=bt.data_ptr(),
+                                   off=self.off.data_ptr(), scale=self.scale.data_ptr())
+
+    @classmethod
+    def from_pairs(cls, pairs, scales) -> "Adapters":
+        """From (A [r][K], B [N][r]) bf16 pairs on one CUDA device."""
+        return cls(torch.cat([a for a, _ in pairs]).contiguous(), torch.cat([b.t() for _, b in pairs]).contiguous(),
+                   [a.shape[0] for a, _ in pairs], scales)
+
+    N = property(lambda s: s.struct.N)
+    K = property(lambda s: s.struct.K)
+    L = property(lambda s: s.struct.L)
+    R = property(lambda s: s.struct.R)
+    max_rank = property(lambda s: s.struct.max_rank)
+
+    def split(self, da: torch.Tensor, dbt: torch.Tensor):
+        """Views of aq_lora_backward's gradients per adapter: (dA [r][K], dB [N][r]) pairs."""
+        return [(x, y.t()) for x, y in zip(da.split(self.ranks), dbt.split(self.ranks))]
+
+
+def aq_lora_workspace_bytes(ad: Adapters, M: int, backward: bool) -> int:
+    return int(lib().aq_lora_workspace_bytes(ctypes.byref(ad.struct), M, int(bool(backward))))
+
+
+def _lora_ws(ad: Adapters, M: int, backward: bool, ws):
+    """The call's workspace: the caller's, or a fresh one from torch's allocator (it
+    needs no initialization, so nothing is shared between calls, streams or graphs)."""
+    need = aq_lora_workspace_bytes(ad, M, backward)
+    if need == 0:
+        raise ValueError("invalid adapters or token count")
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=ad.device)
+    _need(ws, "ws", torch.uint8, ad.device)
+    return ws
+
+
+def _lora_ids(ad: Adapters, ids: torch.Tensor, M: int):
+    _need(ids, "ids", torch.int32, ad.device)
+    if ids.dim() != 1 or ids.shape[0] != M:
+        raise ValueError(f"ids must be int32 [{M}], one adapter index per token")
+
+
+def aq_lora_apply(ad: Adapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Tensor = None, s: torch.Tensor = None,
+                  out: torch.Tensor = None, out_dtype=torch.float32, ws: torch.Tensor = None) -> torch.Tensor:
+    """y + scale_l B_l A_l x per token, l = ids[m] (none outside [0, L)): x bf16 [M][K],
+    ids int32 [M], y float32 or bfloat16 [M][N] (None: the adapters' part alone, in
+    out_dtype).  out may be y.  s float32 [M][max_rank] receives the products that
+    aq_lora_backward takes."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a 2-D torch.bfloat16 tensor")
+    M, dev = x.shape[0], ad.device
+    _rows(x, "x", (torch.bfloat16,), dev, M, ad.K)
+    _lora_ids(ad, ids, M)
+    dtypes = (torch.float32, torch.bfloat16)
+    if y is not None:
+        _rows(y, "y", dtypes, dev, M, ad.N)
+        out_dtype = y.dtype
+    if out is None:
+        out = torch.empty((M, ad.N), dtype=out_dtype, device=dev)
+    _rows(out, "out", dtypes if y is None else (y.dtype,), dev, M, ad.N)
+    if s is not None:
+        _need(s, "s", torch.float32, dev)
+        if tuple(s.shape) != (M, ad.max_rank):
+            raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
+    ws = _lora_ws(ad, M, False, ws)
+    with torch.cuda.device(dev):
+        _check(lib().aq_lora_apply(ctypes.byref(ad.struct), x.data_ptr(), _ld(x), ids.data_ptr(), M,
+                                   y.data_ptr() if y is not None else None, _ld(y) if y is not None else 0,
+                                   out.data_ptr(), _ld(out), AQ_F32 if out.dtype == torch.float32 else AQ_BF16,
+                                   s.data_ptr() if s is not None else None, ws.data_ptr(), ws.numel(), _stream(dev)),
+               "aq_lora_apply")
+    return out
+
+
+def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch.Tensor, x: torch.Tensor,
+                     sx: torch.Tensor = None, add: torch.Tensor = None, dx: torch.Tensor = None, want_dx: bool = True,
+                     dx_dtype=torch.bfloat16, da: torch.Tensor = None, dbt: torch.Tensor = None,
+                     ws: torch.Tensor = None):
+    """Gradients of aq_lora_apply -> (da float32 [R][K], dbt float32 [R][N], dx [M][K] or
+    None).  dy bf16 [M][N]; s as the forward call wrote it; x the activations'
+    8-bit checkpoint (int8 codes with token scales sx, as aq_quant_act made them)
+    or bf16 (sx None).  dx = add + the adapters' part, in add's dtype (dx_dtype
+    without add); dx may be add."""
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise TypeError("dy must be a 2-D torch.bfloat16 tensor")
+    M, dev = dy.shape[0], ad.device
+    _rows(dy, "dy", (torch.bfloat16,), dev, M, ad.N)
+    _lora_ids(ad, ids, M)
+    _need(s, "s", torch.float32, dev)
+    if tuple(s.shape) != (M, ad.max_rank):
+        raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
+    _rows(x, "x", (torch.bfloat16,) if sx is None else (torch.int8,), dev, M, ad.K)
+    if sx is not None:
+        _need(sx, "sx", torch.float32, dev)
+        if sx.numel() < M:
+            raise ValueError(f"sx must hold M = {M} token scales")
+    dtypes = (torch.float32, torch.bfloat16)
+    if add is not None:
+        _rows(add, "add", dtypes, dev, M, ad.K)
+        dx_dtype = add.dtype
+    if dx is None and (want_dx or add is not None):
+        dx = torch.empty((M, ad.K), dtype=dx_dtype, device=dev)
+    if dx is not None:
+        _rows(dx, "dx", dtypes if add is None else (add.dtype,), dev, M, ad.K)
+    if da is None:
+        da = torch.empty((ad.R, ad.K), dtype=torch.float32, device=dev)
+    if dbt is None:
+        dbt = torch.empty((ad.R, ad.N), dtype=torch.float32, device=dev)
+    for t, name, width in ((da, "da", ad.K), (dbt, "dbt", ad.N)):
+        _need(t, name, torch.float32, dev)
+        if tuple(t.shape) != (ad.R, width):
+            raise ValueError(f"{name} must be float32 [{ad.R}][{width}]")
+    ws = _lora_ws(ad, M, True, ws)
+    with torch.cuda.device(dev):
+        _check(lib().aq_lora_backward(ctypes.byref(ad.struct), dy.data_ptr(), _ld(dy), ids.data_ptr(), M, s.data_ptr(),
+                                      x.data_ptr(), _ld(x), sx.data_ptr() if sx is not None else None, da.data_ptr(),
+                                      dbt.data_ptr(), add.data_ptr() if add is not None else None,
+                                      _ld(add) if add is not None else 0, dx.data_ptr() if dx is not None else None,
+                                      _ld(dx) if dx is not None else 0,
+                                      AQ_BF16 if dx is None or dx.dtype == torch.bfloat16 else AQ_F32, ws.data_ptr(),
+                                      ws.numel(), _stream(dev)), "aq_lora_backward")
+    return da, dbt, dx
+
+
+AQ_GATED_GROUP = 128  # features per scale of a gated checkpoint
+
+
+def aq_silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, keep: bool = False, hq: torch.Tensor = None,
+                      sh: torch.Tensor = None):
+    """silu(gate) * up, quantized per token to INT8: gate, up bf16 [M][F]
+    -> (hq int8 [M][F], sh float32 [M]), the down projection's input.  keep=True
+    appends the 8-bit checkpoints of gate and up for aq_silu_mul_backward: (..., gq
+    int8 [M][F], gs float32 [M][ceil(F/128)], uq, us)."""
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+        raise TypeError("gate must be a 2-D torch.bfloat16 tensor")
+    (M, F), dev = gate.shape, gate.device
+    _rows(gate, "gate", (torch.bfloat16,), None, M, F)
+    _rows(up, "up", (torch.bfloat16,), dev, M, F)
+    if tuple(up.shape) != (M, F):
+        raise ValueError("gate and up must have one shape")
+    codes = [hq if hq is not None else torch.empty((M, F), dtype=torch.int8, device=dev)]
+    sh = torch.empty((M,), dtype=torch.float32, device=dev) if sh is None else sh
+    _need(codes[0], "hq", torch.int8, dev)
+    _need(sh, "sh", torch.float32, dev)
+    if tuple(codes[0].shape) != (M, F) or sh.numel() < M:
+        raise ValueError("hq must be int8 [M][F] and sh hold M scales")
+    groups = -(-F // AQ_GATED_GROUP)
+    kept = ()
+    if keep:
+        kept = tuple(t for _ in range(2) for t in (torch.empty((M, F), dtype=torch.int8, device=dev),
+                                                   torch.empty((M, groups), dtype=torch.float32, device=dev)))
+    ptrs = [t.data_ptr() for t in kept] if keep else [None] * 4
+    with torch.cuda.device(dev):
+        _check(lib().aq_silu_mul_quant(gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), M, F, codes[0].data_ptr(),
+                                       sh.data_ptr(), *ptrs, _stream(dev)), "aq_silu_mul_quant")
+    return (codes[0], sh) + kept
+
+
+def aq_silu_mul_backward(dh: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, uq: torch.Tensor, us: torch.Tensor,
+                         dgate: torch.Tensor = None, dup: torch.Tensor = None):
+    """Gradients of silu(gate) * up from its 8-bit checkpoints: dh bf16 [M][F] ->
+    (dgate, dup) bf16 [M][F]."""
+    if not isinstance(dh, torch.Tensor) or dh.dim() != 2:
+        raise TypeError("dh must be a 2-D torch.bfloat16 tensor")
+    (M, F), dev = dh.shape, dh.device
+    _rows(dh, "dh", (torch.bfloat16,), None, M, F)
+    for q, s, name in ((gq, gs, "g"), (uq, us, "u")):
+        _need(q, name + "q", torch.int8, dev)
+        _need(s, name + "s", torch.float32, dev)
+        if tuple(q.shape) != (M, F) or tuple(s.shape) != (M, -(-F // AQ_GATED_GROUP)):
+            raise ValueError(f"{name}q must be int8 [M][F] and {name}s float32 [M][ceil(F/{AQ_GATED_GROUP})]")
+    dgate = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if dgate is None else dgate
+    dup = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if dup is None else dup
+    _rows(dgate, "dgate", (torch.bfloat16,), dev, M, F)
+    _rows(dup, "dup", (torch.bfloat16,), dev, M, F)
+    with torch.cuda.device(dev):
+        _check(lib().aq_silu_mul_backward(dh.data_ptr(), _ld(dh), gq.data_ptr(), gs.data_ptr(), uq.data_ptr(),
+                                          us.data_ptr(), M, F, dgate.data_ptr(), _ld(dgate), dup.data_ptr(), _ld(dup),
+                                          _stream(dev)), "aq_silu_mul_backward")
+    return dgate, dup
+
+
+def aq_linear_backward_workspace_bytes(M: int, w: PackedWeights) -> int:
+    return int(lib().aq_linear_backward_workspace_bytes(M, ctypes.byref(w.struct)))
+
+
+def _backward_workspace(M: int, w: PackedWeights) -> torch.Tensor:
+    """A zero-filled workspace: cached per device and stream, or the call's own while
+    a graph is captured (so that graphs share none)."""
+    need = aq_linear_backward_workspace_bytes(M, w)
+    if need == 0:
+        raise ValueError("invalid arguments for a workspace")
+    with torch.cuda.device(w.device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(need, dtype=torch.uint8, device=w.device)
+        key = (w.device, "backward", _stream(w.device))
+        ws = _ws_cache.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=w.device)
+        return ws
+
+
+def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = None, out: torch.Tensor = None,
+                       out_dtype=torch.bfloat16, ws: torch.Tensor = None) -> torch.Tensor:
+    """Input gradient of a packed projection: dx = add + dy W (W dequantized), dy bf16
+    [M][N] -> [M][K] in add's dtype (out_dtype without add).  out may be add."""
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise TypeError("dy must be a 2-D torch.bfloat16 tensor")
+    M, dev = dy.shape[0], w.device
+    _rows(dy, "dy", (torch.bfloat16,), dev, M, w.N)
+    dtypes = (torch.float32, torch.bfloat16)
+    if add is not None:
+        _rows(add, "add", dtypes, dev, M, w.K)
+        out_dtype = add.dtype
+    if out is None:
+        out = torch.empty((M, w.K), dtype=out_dtype, device=dev)
+    _rows(out, "out", dtypes if add is None else (add.dtype,), dev, M, w.K)
+    if ws is None:
+        ws = _backward_workspace(M, w)
+    _need(ws, "ws", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        _check(lib().aq_linear_backward(ctypes.byref(w.struct), dy.data_ptr(), _ld(dy), M,
+                                        add.data_ptr() if add is not None else None,
+                                        _ld(add) if add is not None else 0, out.data_ptr(), _ld(out),
+                                        AQ_F32 if out.dtype == torch.float32 else AQ_BF16, ws.data_ptr(), ws.numel(),
+                                        _stream(dev)), "aq_linear_backward")
+    return out
 
 
 def aq_debug_tile_partials(w: PackedWeights, xq: torch.Tensor, phase: int, ws=None) -> torch.Tensor:

@@ -1,0 +1,729 @@
+// Low-rank adapters of many requests beside a shared projection, and their
+// gradients.
+//
+// Token m has the adapter l = ids[m] (none when ids[m] is outside [0, L)) of
+// rank r_l, with A_l [r_l][K] and B_l^T [r_l][N] stored as rows
+// off[l] .. off[l+1]-1 of two bf16 tables:
+//   forward   S[m][r] = c_l sum_k x[m][k] A_l[r][k]
+//             out[m][n] = y[m][n] + sum_r S[m][r] B_l^T[r][n]
+//   backward  T[m][r] = c_l sum_n dy[m][n] B_l^T[r][n]
+//             dx[m][k] = add[m][k] + sum_r T[m][r] A_l[r][k]
+//             dA_l[r][k] = sum_m T[m][r] x[m][k];  dB_l^T[r][n] = sum_m S[m][r] dy[m][n]
+// so three kernels serve both: contract a long axis to the rank (shrink),
+// the rank to a long axis (expand), and the tokens (outer).
+//
+// Products run on mma.sync (bf16 in, fp32 out): the tables and x, dy are bf16
+// (8-bit codes are exact in bf16), and S and T, fp32, enter as three bf16 terms
+// (24 significant bits), so that no operand loses bits.  Sums are fp32.
+//
+// A tile is 64 consecutive tokens.  A kernel lists the adapters that occur in
+// its tile and runs them one after another on the same activations: requests
+// are contiguous in a batch, so a tile has one or two; a decode batch has up to
+// 64 in its one tile, which `kz` CTAs share out.  Rows of other adapters are
+// never added in but selected out, so that an infinity or NaN in one request's
+// adapter or activations stays with that request.
+#include <algorithm>
+
+#include "aq_internal.cuh"
+
+namespace aq {
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kTok = 64;       // tokens of a tile
+constexpr int kRank = 64;      // ranks of a block
+constexpr int kMaxRank = 256;  // largest rank of an adapter
+constexpr int kThreads = 256;  // 8 warps
+constexpr int kDC = 128;       // columns of a chunk of the long axis
+constexpr int kLd = kDC + 8;   // row pitch in shared memory: 17 x 16 bytes, conflict-free for ldmatrix
+constexpr int kLdR = kRank + 8;
+
+struct Table {  // one of the two tables of an adapter set
+  const uint16_t* w;   // [R][D]
+  const int32_t* off;  // [L + 1]
+  const float* scale;  // [L]
+  int D, L, R, max_rank;
+};
+
+// Rows of adapter l, kept inside the table whatever `off` holds.
+__device__ __forceinline__ void rows_of(const Table& t, int l, int& row0, int& rank) {
+  const int a = min(max(__ldg(t.off + l), 0), t.R), b = min(max(__ldg(t.off + l + 1), a), t.R);
+  row0 = a;
+  rank = min(b - a, t.max_rank);
+}
+
+// The adapters of a tile that this CTA handles.
+struct TileList {
+  int n;             // adapters
+  int row0[kTok];    // first table row of the rank block
+  int rank[kTok];    // ranks of the block
+  float scale[kTok];
+  u64 mask[kTok];    // tokens of the tile that have it
+  int slot[kTok];    // of each token: list index, -1 another CTA's, -2 no adapter (or none in this rank block)
+  int id[kTok];
+  int first[kTok];
+  int count[2];
+};
+
+// Ranks from rb0 on; of the adapters that have some, those with index = zi mod kz.
+__device__ void list_tile(const Table& t, const int32_t* ids, int m0, int M, int rb0, int zi, int kz, TileList& q) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  int v = -1, row0 = 0, rank = 0;
+  if (tid < kTok) {
+    if (m0 + tid < M) v = __ldg(ids + m0 + tid);
+    if (v < 0 || v >= t.L) v = -1;
+    if (v >= 0) {
+      rows_of(t, v, row0, rank);
+      rank -= rb0;
+      if (rank <= 0) v = -1;
+    }
+    q.id[tid] = v;
+  }
+  __syncthreads();
+  u64 mk = 0;
+  bool first = false;
+  unsigned vote = 0;
+  if (tid < kTok) {
+#pragma unroll 8
+    for (int j = 0; j < kTok; ++j) mk |= (u64)(q.id[j] == v) << j;
+    first = v >= 0 && __ffsll((long long)mk) - 1 == tid;
+    vote = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) q.count[tid >> 5] = __popc(vote);
+  }
+  __syncthreads();
+  if (tid < kTok) {
+    const int idx = (tid >= 32 ? q.count[0] : 0) + __popc(vote & ((1u << lane) - 1));
+    if (first) {
+      q.first[tid] = idx;
+      if (idx % kz == zi) {
+        const int a = idx / kz;
+        q.row0[a] = row0 + rb0;
+        q.rank[a] = rank;
+        q.scale[a] = __ldg(t.scale + v);
+        q.mask[a] = mk;
+      }
+    }
+    if (tid == 0) {
+      const int all = q.count[0] + q.count[1];
+      q.n = all > zi ? (all - zi + kz - 1) / kz : 0;
+    }
+  }
+  __syncthreads();
+  if (tid < kTok) {
+    int s = -2;
+    if (v >= 0) {
+      const int idx = q.first[__ffsll((long long)mk) - 1];
+      s = idx % kz == zi ? idx / kz : -1;
+    }
+    q.slot[tid] = s;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// v as three bf16 terms: hi + mid + lo = v to 24 bits.  A non-finite v stays in hi.
+__device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  float r = v - __bfloat162float(h);
+  if (!(fabsf(r) < 3e38f)) r = 0.f;
+  const __nv_bfloat16 m = __float2bfloat16_rn(r);
+  const __nv_bfloat16 l = __float2bfloat16_rn(r - __bfloat162float(m));
+  hi = __bfloat16_as_ushort(h);
+  mid = __bfloat16_as_ushort(m);
+  lo = __bfloat16_as_ushort(l);
+}
+
+// ---------------------------------------------------------------- shrink
+struct ShrinkArgs {
+  Table t;
+  const uint16_t* x;
+  int ldx, M;
+  const int32_t* ids;
+  float* p;  // [splits][M][max_rank]
+  int splits, kz;
+};
+
+struct ShrinkSmem {
+  uint16_t x[3][kTok][kLd];
+  uint16_t w[3][kRank][kLd];
+  float s[2][kTok][kRank];
+  TileList q;
+};
+
+__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  ShrinkSmem& sm = *reinterpret_cast<ShrinkSmem*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int m0 = blockIdx.x * kTok, split = blockIdx.y, zi = blockIdx.z % a.kz, rb0 = blockIdx.z / a.kz * kRank;
+  const Table& t = a.t;
+  pdl_launch_dependents();
+  pdl_wait();
+  list_tile(t, a.ids, m0, a.M, rb0, zi, a.kz, sm.q);
+  const int na = sm.q.n;
+  if (na == 0) return;
+  const int chunks = (t.D + kDC - 1) / kDC;
+  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
+  for (int i = tid; i < 2 * kTok * kRank; i += kThreads) (&sm.s[0][0][0])[i] = 0.f;
+
+  // items: (chunk, adapter), adapters inside
+  const int items = (c1 - c0) * na;
+  int ic = c0, ia = 0, is = 0, ix = 2;  // next item to issue: its chunk, adapter, table slot, activation slot
+  auto issue = [&]() {
+    if (ic < c1) {
+      const int d0 = ic * kDC;
+      if (ia == 0) {
+        ix = ix == 2 ? 0 : ix + 1;
+        for (int i = tid; i < kTok * (kDC / 8); i += kThreads) {
+          const int r = i / (kDC / 8), c = i % (kDC / 8) * 8;
+          const bool in = m0 + r < a.M && d0 + c < t.D;
+          cp16(&sm.x[ix][r][c], in ? a.x + (size_t)(m0 + r) * a.ldx + d0 + c : a.x, in);
+        }
+      }
+      const int nr = min(sm.q.rank[ia], kRank), row0 = sm.q.row0[ia];
+      const int rows = (nr + 15) & ~15;
+      for (int i = tid; i < rows * (kDC / 8); i += kThreads) {
+        const int r = i / (kDC / 8), c = i % (kDC / 8) * 8;
+        const bool in = r < nr && d0 + c < t.D;
+        cp16(&sm.w[is][r][c], in ? t.w + (size_t)(row0 + r) * t.D + d0 + c : t.w, in);
+      }
+      is = is == 2 ? 0 : is + 1;
+      if (++ia == na) {
+        ia = 0;
+        ++ic;
+      }
+    }
+    cp_commit();
+  };
+  issue();
+  issue();
+  const int sub = warp & 3, kh = warp >> 2;
+  float acc[kRank / 8][4];
+#pragma unroll
+  for (int j = 0; j < kRank / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  int al = 0, ws = 0, xs = 0, run = 0;
+  for (int it = 0; it < items; ++it) {
+    cp_wait<1>();
+    __syncthreads();
+    issue();
+    const u64 mask = sm.q.mask[al];
+    const uint32_t mine = (uint32_t)(mask >> (16 * sub)) & 0xFFFFu;
+    if (mine) {
+      const int nt = (min(sm.q.rank[al], kRank) + 15) / 16;  // pairs of 8-rank tiles
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int k0 = 64 * kh + 16 * ks;
+        uint32_t fa[4];
+        ldsm4(fa, &sm.x[xs][16 * sub + (lane & 7) + 8 * ((lane >> 3) & 1)][k0 + 8 * (lane >> 4)]);
+#pragma unroll
+        for (int j = 0; j < kRank / 16; ++j) {
+          if (j < nt) {
+            uint32_t fb[4];
+            ldsm4(fb, &sm.w[ws][16 * j + (lane & 7) + 8 * (lane >> 4)][k0 + 8 * ((lane >> 3) & 1)]);
+            mma16816(acc[2 * j], fa, fb[0], fb[1]);
+            mma16816(acc[2 * j + 1], fa, fb[2], fb[3]);
+          }
+        }
+      }
+      // the tokens of this adapter take the products over (a run of 8 chunks
+      // where the tile has one adapter)
+      if (na > 1 || ++run == 8 || it + 1 == items) {
+        run = 0;
+#pragma unroll
+        for (int j = 0; j < kRank / 8; ++j) {
+          if (j < 2 * nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = (lane >> 2) + 8 * (e >> 1);
+              if ((mine >> r) & 1u) sm.s[kh][16 * sub + r][8 * j + 2 * (lane & 3) + (e & 1)] += acc[j][e];
+              acc[j][e] = 0.f;
+            }
+          }
+        }
+      }
+    }
+    ws = ws == 2 ? 0 : ws + 1;
+    if (++al == na) {
+      al = 0;
+      xs = xs == 2 ? 0 : xs + 1;
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  for (int i = tid; i < kTok * kRank; i += kThreads) {
+    const int r = i / kRank, c = i % kRank, s = sm.q.slot[r];
+    if (s >= 0 && c < sm.q.rank[s])
+      a.p[((size_t)split * a.M + m0 + r) * t.max_rank + rb0 + c] = sm.q.scale[s] * (sm.s[0][r][c] + sm.s[1][r][c]);
+  }
+}
+
+// ---------------------------------------------------------------- expand
+struct ExpandArgs {
+  Table t;
+  const int32_t* ids;
+  int M;
+  const float* p;  // [splits][M][max_rank]
+  int splits, kz;
+  const void* y;   // or null
+  void* out;
+  int ldy, ldo, f32;
+  float* s;        // [M][max_rank] or null: the summed products
+};
+
+struct ExpandSmem {
+  TileList q;
+  uint16_t w[2][kRank][kLd];
+  // then three terms of S: [3][kTok][ranks + 8]
+};
+
+__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const ExpandArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  ExpandSmem& sm = *reinterpret_cast<ExpandSmem*>(raw);
+  uint16_t* terms = reinterpret_cast<uint16_t*>(raw + sizeof(ExpandSmem));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int m0 = blockIdx.y * kTok, n0 = blockIdx.x * kDC, zi = blockIdx.z;
+  const Table& t = a.t;
+  const int rp = (t.max_rank + 15) / 16 * 16, lds = rp + 8, plane = kTok * lds;
+  pdl_launch_dependents();
+  pdl_wait();
+  list_tile(t, a.ids, m0, a.M, 0, zi, a.kz, sm.q);
+  const int na = sm.q.n;
+
+  // S of this tile, as three bf16 terms; zero behind the token's rank
+  for (int i = tid; i < kTok * rp; i += kThreads) {
+    const int r = i / rp, c = i % rp, s = sm.q.slot[r];
+    if (s == -1 || m0 + r >= a.M) continue;
+    float v = 0.f;
+    if (s >= 0 && c < sm.q.rank[s])
+      for (int k = 0; k < a.splits; ++k) v += __ldg(a.p + ((size_t)k * a.M + m0 + r) * t.max_rank + c);
+    if (a.s && blockIdx.x == 0 && c < t.max_rank && (s >= 0 || zi == 0))
+      a.s[(size_t)(m0 + r) * t.max_rank + c] = v;
+    uint16_t* d = terms + r * lds + c;
+    split3(v, d[0], d[plane], d[2 * plane]);
+  }
+
+  // items: (adapter, block of 64 ranks)
+  int ia = 0, ir = 0, ib = 0;
+  auto issue = [&]() {
+    if (ia < na) {
+      const int nr = min(sm.q.rank[ia] - ir, kRank), row0 = sm.q.row0[ia] + ir;
+      const int rows = (nr + 15) & ~15;
+      for (int i = tid; i < rows * (kDC / 8); i += kThreads) {
+        const int r = i / (kDC / 8), c = i % (kDC / 8) * 8;
+        const bool in = r < nr && n0 + c < t.D;
+        cp16(&sm.w[ib][r][c], in ? t.w + (size_t)(row0 + r) * t.D + n0 + c : t.w, in);
+      }
+      ib ^= 1;
+      ir += kRank;
+      if (ir >= sm.q.rank[ia]) {
+        ir = 0;
+        ++ia;
+      }
+    }
+    cp_commit();
+  };
+  issue();
+  const int sub = warp & 3, nh = warp >> 2;
+  float delta[8][4], acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) delta[j][e] = acc[j][e] = 0.f;
+  int wb = 0;
+  for (int al = 0; al < na; ++al) {
+    const int rank = sm.q.rank[al];
+    const uint32_t mine = (uint32_t)(sm.q.mask[al] >> (16 * sub)) & 0xFFFFu;
+    for (int r0 = 0; r0 < rank; r0 += kRank) {
+      cp_wait<0>();
+      __syncthreads();
+      issue();
+      if (mine) {
+        const int ksteps = (min(rank - r0, kRank) + 15) / 16;
+        for (int ks = 0; ks < ksteps; ++ks) {
+          uint32_t fb[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ldsm4t(fb[j], &sm.w[wb][16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1)][64 * nh + 16 * j + 8 * (lane >> 4)]);
+#pragma unroll
+          for (int sp = 2; sp >= 0; --sp) {
+            uint32_t fa[4];
+            ldsm4(fa, terms + sp * plane + (16 * sub + (lane & 7) + 8 * ((lane >> 3) & 1)) * lds + r0 + 16 * ks +
+                          8 * (lane >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma16816(acc[2 * j], fa, fb[j][0], fb[j][1]);
+              mma16816(acc[2 * j + 1], fa, fb[j][2], fb[j][3]);
+            }
+          }
+        }
+      }
+      wb ^= 1;
+    }
+    if (mine) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((mine >> ((lane >> 2) + 8 * (e >> 1))) & 1u) delta[j][e] = acc[j][e];
+          acc[j][e] = 0.f;
+        }
+    }
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 16 * sub + (lane >> 2) + 8 * h, m = m0 + r, s = sm.q.slot[r];
+    if (m >= a.M || s == -1 || (s == -2 && zi != 0)) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = n0 + 64 * nh + 8 * j + 2 * (lane & 3);
+      if (n >= t.D) continue;
+      float v0 = delta[j][2 * h], v1 = delta[j][2 * h + 1];
+      if (a.f32) {
+        if (a.y) {
+          const float2 y = *reinterpret_cast<const float2*>(static_cast<const float*>(a.y) + (size_t)m * a.ldy + n);
+          v0 += y.x;
+          v1 += y.y;
+        }
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + (size_t)m * a.ldo + n) = make_float2(v0, v1);
+      } else {
+        if (a.y) {
+          const uint32_t y =
+              *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.y) + (size_t)m * a.ldy + n);
+          v0 += bf16_bits_to_float(y & 0xFFFFu);
+          v1 += bf16_bits_to_float(y >> 16);
+        }
+        const __nv_bfloat162 o = __floats2bfloat162_rn(v0, v1);
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.ldo + n) = o;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- outer
+struct OuterArgs {
+  Table t;              // rows and ranks (the table itself is not read)
+  const int32_t* ids;
+  int M;
+  const float* p;       // [psplits][M][max_rank]
+  int psplits;
+  const void* x;        // bf16 [M][ldx], or int8 codes with sx [M]
+  const float* sx;
+  int ldx;
+  float* g;             // [splits][R][D]
+  int splits;
+};
+
+struct OuterSmem {
+  uint16_t x[kTok][kLd];
+  uint16_t t[3][kTok][kLdR];
+  int in[kTok];
+};
+
+template <bool CODES>
+__global__ void __launch_bounds__(kThreads) lora_outer_kernel(const OuterArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  OuterSmem& sm = *reinterpret_cast<OuterSmem*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rblocks = (a.t.max_rank + kRank - 1) / kRank;
+  const int d0 = blockIdx.x * kDC, l = blockIdx.y / rblocks, rb0 = blockIdx.y % rblocks * kRank, split = blockIdx.z;
+  const Table& t = a.t;
+  pdl_launch_dependents();
+  pdl_wait();
+  int row0, rank;
+  rows_of(t, l, row0, rank);
+  const int nr = min(rank - rb0, kRank);
+  if (nr <= 0) return;
+  const int chunks = (a.M + kTok - 1) / kTok;
+  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
+  const int mt = (nr + 15) / 16;
+  float tot[4][2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tot[i][j][e] = 0.f;
+  for (int c = c0; c < c1; ++c) {
+    const int m0 = c * kTok;
+    bool in = false;
+    if (tid < kTok) {
+      in = m0 + tid < a.M && __ldg(a.ids + m0 + tid) == l;
+      sm.in[tid] = in;
+    }
+    if (!__syncthreads_or(in)) continue;
+    // activations: rows of other adapters as zeros
+    if (CODES) {
+      for (int i = tid; i < kTok * (kDC / 16); i += kThreads) {
+        const int r = i / (kDC / 16), cc = i % (kDC / 16) * 16;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (sm.in[r] && d0 + cc < t.D)
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.x) + (size_t)(m0 + r) * a.ldx + d0 + cc));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int b0 = static_cast<int8_t>(w[e >> 1] >> (16 * (e & 1)));
+          const int b1 = static_cast<int8_t>(w[e >> 1] >> (16 * (e & 1) + 8));
+          const __nv_bfloat162 p = __floats2bfloat162_rn((float)b0, (float)b1);
+          o[e] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(&sm.x[r][cc]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(&sm.x[r][cc + 8]) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    } else {
+      for (int i = tid; i < kTok * (kDC / 8); i += kThreads) {
+        const int r = i / (kDC / 8), cc = i % (kDC / 8) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (sm.in[r] && d0 + cc < t.D)
+          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (size_t)(m0 + r) * a.ldx + d0 + cc));
+        *reinterpret_cast<uint4*>(&sm.x[r][cc]) = v;
+      }
+    }
+    for (int i = tid; i < kTok * 16 * mt; i += kThreads) {
+      const int r = i / (16 * mt), cc = i % (16 * mt);
+      float v = 0.f;
+      if (sm.in[r] && cc < nr) {
+        for (int k = 0; k < a.psplits; ++k) v += __ldg(a.p + ((size_t)k * a.M + m0 + r) * t.max_rank + rb0 + cc);
+        if (CODES) v *= __ldg(a.sx + m0 + r);
+      }
+      split3(v, sm.t[0][r][cc], sm.t[1][r][cc], sm.t[2][r][cc]);
+    }
+    __syncthreads();
+    float acc[4][2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t fb[4];
+      ldsm4t(fb, &sm.x[16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1)][16 * warp + 8 * (lane >> 4)]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < mt) {
+#pragma unroll
+          for (int sp = 2; sp >= 0; --sp) {
+            uint32_t fa[4];
+            ldsm4t(fa, &sm.t[sp][16 * ks + (lane & 7) + 8 * (lane >> 4)][16 * i + 8 * ((lane >> 3) & 1)]);
+            mma16816(acc[i][0], fa, fb[0], fb[1]);
+            mma16816(acc[i][1], fa, fb[2], fb[3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tot[i][j][e] += acc[i][j][e];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = 16 * i + (lane >> 2) + 8 * h;
+      if (r >= nr) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int d = d0 + 16 * warp + 8 * j + 2 * (lane & 3);
+        if (d < t.D)
+          *reinterpret_cast<float2*>(a.g + ((size_t)split * t.R + row0 + rb0 + r) * t.D + d) =
+              make_float2(tot[i][j][2 * h], tot[i][j][2 * h + 1]);
+      }
+    }
+}
+
+// g[i] = sum of the splits' values, splits in increasing order.
+__global__ void __launch_bounds__(256) lora_sum_kernel(const float4* __restrict__ p, int splits, size_t n,
+                                                       float4* __restrict__ g) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+    float4 v = p[i];
+    for (int k = 1; k < splits; ++k) {
+      const float4 w = p[(size_t)k * n + i];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    g[i] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+Table table_a(const aq_lora* ad) { return {ad->a, ad->off, ad->scale, ad->K, ad->L, ad->R, ad->max_rank}; }
+Table table_b(const aq_lora* ad) { return {ad->bt, ad->off, ad->scale, ad->N, ad->L, ad->R, ad->max_rank}; }
+
+// CTAs that share the adapters of one tile: a single tile may hold 64.
+int share(int M, const Table& t) { return M <= kTok && t.L > 1 ? std::min(4, t.L) : 1; }
+
+int shrink_splits(int M, const Table& t) {
+  const int tiles = ceil_div(M, kTok), chunks = ceil_div(t.D, kDC);
+  return std::max(1, std::min(chunks, ceil_div(2 * num_sms(), tiles)));
+}
+
+int outer_splits(int M, const Table& t) {
+  const int tiles = ceil_div(M, kTok), blocks = ceil_div(t.D, kDC);
+  return std::max(1, std::min(std::min(tiles, 16), ceil_div(2 * num_sms(), blocks)));
+}
+
+size_t p_bytes(int M, const Table& t) {
+  return align256((size_t)shrink_splits(M, t) * M * t.max_rank * sizeof(float));
+}
+size_t g_bytes(int M, const Table& t) {
+  const int s = outer_splits(M, t);
+  return s > 1 ? align256((size_t)s * t.R * t.D * sizeof(float)) : 0;
+}
+
+cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p, cudaStream_t st) {
+  ShrinkArgs a{t, x, ldx, M, ids, p, shrink_splits(M, t), share(M, t)};
+  cudaError_t e = ensure_smem_attr<lora_shrink_kernel>(sizeof(ShrinkSmem));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(ceil_div(M, kTok), a.splits, a.kz * ceil_div(t.max_rank, kRank));
+  return launch_pdl(lora_shrink_kernel, grid, dim3(kThreads), sizeof(ShrinkSmem), st, a);
+}
+
+cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, int splits, const void* y, int ldy,
+                   void* out, int ldo, int dtype, float* s, cudaStream_t st) {
+  ExpandArgs a{t, ids, M, p, splits, share(M, t), y, out, ldy, ldo, dtype == AQ_F32, s};
+  const size_t most = sizeof(ExpandSmem) + 3 * kTok * (kMaxRank + 8) * 2;
+  const size_t smem = sizeof(ExpandSmem) + 3 * kTok * ((t.max_rank + 15) / 16 * 16 + 8) * 2;
+  cudaError_t e = ensure_smem_attr<lora_expand_kernel>((int)most);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(ceil_div(t.D, kDC), ceil_div(M, kTok), a.kz);
+  return launch_pdl(lora_expand_kernel, grid, dim3(kThreads), smem, st, a);
+}
+
+cudaError_t outer(const Table& t, const int32_t* ids, int M, const float* p, int psplits, const void* x,
+                  const float* sx, int ldx, float* g, float* part, cudaStream_t st) {
+  const int splits = outer_splits(M, t);
+  OuterArgs a{t, ids, M, p, psplits, x, sx, ldx, splits > 1 ? part : g, splits};
+  const dim3 grid(ceil_div(t.D, kDC), t.L * ceil_div(t.max_rank, kRank), splits);
+  cudaError_t e = sx ? ensure_smem_attr<lora_outer_kernel<true>>(sizeof(OuterSmem))
+                     : ensure_smem_attr<lora_outer_kernel<false>>(sizeof(OuterSmem));
+  if (e == cudaSuccess)
+    e = sx ? launch_pdl(lora_outer_kernel<true>, grid, dim3(kThreads), sizeof(OuterSmem), st, a)
+           : launch_pdl(lora_outer_kernel<false>, grid, dim3(kThreads), sizeof(OuterSmem), st, a);
+  if (e == cudaSuccess && splits > 1) {
+    const size_t n = (size_t)t.R * t.D / 4;
+    const int blocks = (int)std::min<size_t>((n + 255) / 256, 8 * (size_t)num_sms());
+    e = launch_pdl(lora_sum_kernel, dim3(blocks), dim3(256), 0, st, reinterpret_cast<const float4*>(part), splits, n,
+                   reinterpret_cast<float4*>(g));
+  }
+  return e;
+}
+
+int check_lora(const aq_lora* ad) {
+  if (!ad || !ad->a || !ad->bt || !ad->off || !ad->scale) return AQ_ERR_ARG;
+  if (ad->N < 8 || ad->K < 8 || ad->N % 8 || ad->K % 8 || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
+  if (ad->L < 1 || ad->R < 1 || ad->max_rank < 1 || ad->max_rank > kMaxRank || ad->max_rank > ad->R) return AQ_ERR_SHAPE;
+  if (ad->L > 16383) return AQ_ERR_SHAPE;  // grid rows: up to four rank blocks per adapter
+  if (((uintptr_t)ad->a | (uintptr_t)ad->bt) & 15) return AQ_ERR_ARG;
+  if (((uintptr_t)ad->off | (uintptr_t)ad->scale) & 3) return AQ_ERR_ARG;
+  return AQ_OK;
+}
+
+constexpr int kMaxTokens = 65535 * kTok;  // grid rows of the expand kernel
+
+// Rows read or written as 16-byte vectors.
+bool bad_rows(const void* p, int ld, int width, int per16) { return !p || ((uintptr_t)p & 15) || ld < width || ld % per16; }
+
+}  // namespace
+}  // namespace aq
+
+using namespace aq;
+
+extern "C" size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward) {
+  if (check_lora(ad) != AQ_OK || M < 1 || M > kMaxTokens) return 0;
+  const Table ta = table_a(ad), tb = table_b(ad);
+  if (!backward) return p_bytes(M, ta);
+  return p_bytes(M, tb) + std::max(g_bytes(M, ta), g_bytes(M, tb)) + 256;
+}
+
+extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
+                             int ldy, void* out, int ldo, int ydtype, float* s, void* ws, size_t ws_bytes,
+                             void* stream) {
+  int rc = check_lora(ad);
+  if (rc != AQ_OK) return rc;
+  if (M < 1 || M > kMaxTokens || !ids || ((uintptr_t)ids & 3) || ((uintptr_t)s & 3)) return AQ_ERR_ARG;
+  if (ydtype != AQ_F32 && ydtype != AQ_BF16) return AQ_ERR_ARG;
+  const int per16 = ydtype == AQ_F32 ? 4 : 8;
+  if (bad_rows(x, ldx, ad->K, 8) || bad_rows(out, ldo, ad->N, per16) || (y && bad_rows(y, ldy, ad->N, per16)))
+    return AQ_ERR_ARG;
+  if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 0)) return AQ_ERR_WORKSPACE;
+  if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Table ta = table_a(ad);
+  float* p = static_cast<float*>(ws);
+  cudaError_t e = shrink(ta, x, ldx, ids, M, p, st);
+  if (e == cudaSuccess)
+    e = expand(table_b(ad), ids, M, p, shrink_splits(M, ta), y, ldy, out, ldo, ydtype, s, st);
+  return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M,
+                                const float* s, const void* x, int ldx, const float* sx, float* da, float* dbt,
+                                const void* add, int ldadd, void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes,
+                                void* stream) {
+  int rc = check_lora(ad);
+  if (rc != AQ_OK) return rc;
+  if (M < 1 || M > kMaxTokens || !ids || !da || !dbt || !s) return AQ_ERR_ARG;
+  if (((uintptr_t)ids | (uintptr_t)s | (uintptr_t)sx) & 3 || ((uintptr_t)da | (uintptr_t)dbt) & 15) return AQ_ERR_ARG;
+  if (bad_rows(dy, ldd, ad->N, 8) || bad_rows(x, ldx, ad->K, sx ? 16 : 8)) return AQ_ERR_ARG;
+  if (sx && ad->K % 16) return AQ_ERR_SHAPE;  // codes are read 16 at a time
+  if (!dx && add) return AQ_ERR_ARG;
+  if (dx) {
+    if (dxdtype != AQ_F32 && dxdtype != AQ_BF16) return AQ_ERR_ARG;
+    const int per16 = dxdtype == AQ_F32 ? 4 : 8;
+    if (bad_rows(dx, lddx, ad->K, per16) || (add && bad_rows(add, ldadd, ad->K, per16))) return AQ_ERR_ARG;
+  }
+  if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 1)) return AQ_ERR_WORKSPACE;
+  if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Table ta = table_a(ad), tb = table_b(ad);
+  float* p = static_cast<float*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p_bytes(M, tb));
+  const int splits = shrink_splits(M, tb);
+  cudaError_t e = shrink(tb, dy, ldd, ids, M, p, st);
+  if (e == cudaSuccess && dx) e = expand(ta, ids, M, p, splits, add, ldadd, dx, lddx, dxdtype, nullptr, st);
+  if (e == cudaSuccess) e = outer(ta, ids, M, p, splits, x, sx, ldx, da, part, st);
+  if (e == cudaSuccess) e = outer(tb, ids, M, s, 1, dy, nullptr, ldd, dbt, part, st);
+  return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
