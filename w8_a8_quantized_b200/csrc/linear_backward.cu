@@ -1,63 +1,391 @@
-// Input gradient of a packed projection:
-//   dx[m][k] = add[m][k] + sum_n dy[m][n] sw[n][j(k)] q[n][k],   j(k) = k / 128.
-// One CTA per 64 tokens x 64 columns; 16 x 64 slices of dy and of the
-// dequantized weights pass through shared memory, sums in fp32.
+// Input gradient of a packed projection on the 5th-generation tensor cores:
+//   dx[m][k] = add[m][k] + sum_n dy[m][n] w[n][k],   w[n][k] = sw[n][k / 128] q[n][k].
+//
+// The contraction runs over the output features n, whose scales differ from row
+// to row, so a scale cannot be taken out of the sum: the packed codes are
+// dequantized on chip and the products run in bf16 with fp32 accumulation.
+// w is rounded to bf16 once (q is exact in bf16, sw q is not): 2^-8 relative per
+// product at most, independent from row to row, so about the error that the
+// rounding of a bf16 dx adds; dy is bf16 already.
+//
+// A work unit is (128 columns k: one tile column; NT tokens; a range of n).  Per
+// step of 64 rows n:
+//   D[128 k][NT tokens] += W'[64 n][128 k]^T dY[NT tokens][64 n]^T
+// with W' as the A operand, MN-major, so that the codes keep the packed order
+// (k contiguous) and no transposition is needed, and dY as the B operand,
+// K-major as it lies in memory.
+//
+// Roles in one CTA (persistent over work units, every role walks the same
+// sequence of steps g = 0, 1, 2, ...):
+//   warp 0       weight producer: labels and tile indices of 32 steps at a time,
+//                one step per lane, the next 32 in flight; codes (TMA) and the 64
+//                row scales (bulk copy) into the raw ring
+//   warp 1       allocates tensor memory; one lane issues tcgen05.mma (kind::f16,
+//                M = 128, N = NT, K = 16) four times per step
+//   warp 3       dY producer (TMA, 128-byte swizzle), after the previous kernel
+//   warps 4-11   transform: codes -> sw q in bf16 -> the swizzled A stage
+//   warps 12-15  epilogue: tensor memory -> add -> dx, while the next unit runs in
+//                the other accumulator buffer
+// The weights are read before the previous kernel has finished; dY, add, dx and
+// the workspace are not touched before.
+//
+// Few units (short sequences): the range of n is split, partial sums go to the
+// workspace, and the CTA that finishes a unit last adds them in split order.
+// Every wait is bounded, as in tc_linear_kernel.
+#include <algorithm>
+#include <cstring>
+
 #include "aq_internal.cuh"
 
 namespace aq {
 namespace {
 
-constexpr int kT = 64, kN = 16;
+constexpr int kStep = 64;       // rows n per step
+constexpr int kRawSlots = 3;    // ring of packed codes and scales
+constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 scales
+constexpr int kXfWarp0 = 4, kXfWarps = 8, kXfThreads = 32 * kXfWarps;
+constexpr int kEpiWarp0 = kXfWarp0 + kXfWarps, kEpiWarps = 4;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kMaxBwdSplits = 16;
+constexpr unsigned long long kGraceNs = 200000;
+
+template <int NT>
+struct BwdShape {
+  static constexpr int kA = kStep * kTileK * 2;  // W' stage: two 64-column halves of 64 rows x 128 bytes
+  static constexpr int kB = NT * kStep * 2;      // dY stage: NT rows x 128 bytes
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 196608 / kStage < 6 ? 196608 / kStage : 6;
+  static constexpr int kTmemCols = 2 * NT <= 32 ? 32 : 2 * NT <= 64 ? 64 : 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
+  static constexpr int kCtrl = 512;
+  static constexpr int kSmem = 1024 + kStages * kStage + kRawSlots * kRawBytes + kCtrl;
+  // D fp32; A, B bf16; A MN-major, B K-major
+  static constexpr uint32_t kIdesc =
+      (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
+  static_assert(kStages >= 3 && kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
+  static_assert((2 * kRawSlots + 3 * kStages + 4 + 2) * 8 + kRawSlots * 4 + 4 * 4 <= kCtrl, "control area");
+};
+
+struct BwdMaps {
+  CUtensorMap w8, w4, dy;
+};
 
 struct BwdArgs {
-  aq_packed w;
-  const uint16_t* dy;
-  int ldd, M;
+  const uint8_t* bitmap;
+  const int32_t* tile_idx;
+  const uint16_t* scales;
+  int N, K, bN, C, T4, T8;
+  int M, ntb, S, units, steps;  // steps of the whole range: N / 64
   const void* add;
   void* dx;
   int ldadd, lddx, f32;
+  void* ws;
+  float* partial;  // [S][M][K]
+  int* counters;   // [C * ntb]
+  int ws_clear;
 };
 
-__global__ void __launch_bounds__(256) linear_backward_kernel(const BwdArgs a) {
-  __shared__ float sd[kN][kT + 1], sw[kN][kT + 1];
-  const int tid = threadIdx.x, m0 = blockIdx.y * kT, k0 = blockIdx.x * kT, j = k0 / kTileK;
-  const aq_packed& w = a.w;
-  pdl_launch_dependents();
-  pdl_wait();
-  float acc[4][4] = {};
-  for (int n0 = 0; n0 < w.N; n0 += kN) {
-    const int r = n0 / w.bN, tile = r * w.C + j;
-    const bool is4 = (w.bitmap[tile >> 3] >> (tile & 7)) & 1;
-    const size_t base = (size_t)w.tile_idx[tile] * w.bN * kTileK;
-    for (int i = tid; i < kN * kT; i += 256) {
-      const int n = i / kT, k = i % kT, in_row = n0 + n - r * w.bN, in_col = k0 + k - j * kTileK;
-      const size_t e = base + (size_t)in_row * kTileK + in_col;
-      int q;
-      if (is4) {
-        const int b = w.w4[e >> 1];
-        q = (int)(int8_t)((e & 1) ? (b & 0xF0) : (b << 4)) >> 4;
-      } else {
-        q = w.w8[e];
-      }
-      sw[n][k] = __half2float(__ushort_as_half(w.scales[(size_t)tile * w.bN + in_row])) * (float)q;
-      const int m = i / kN, c = i % kN;
-      sd[c][m] = m0 + m < a.M ? bf16_bits_to_float(a.dy[(size_t)(m0 + m) * a.ldd + n0 + c]) : 0.f;
+struct BwdUnit {
+  int kb, tb, s, i0, i1;
+};
+
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
+  BwdUnit x;
+  x.s = u % a.S;
+  const int rest = u / a.S;
+  x.tb = rest % a.ntb;
+  x.kb = rest / a.ntb;
+  x.i0 = (int)((long long)a.steps * x.s / a.S);
+  x.i1 = (int)((long long)a.steps * (x.s + 1) / a.S);
+  return x;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, one CTA.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: groups of 8 rows
+// (contraction) 1024 bytes apart, halves of 64 columns 64 x 128 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
+  d |= (uint64_t)((kStep * 128) >> 4) << 16;  // leading: the next 64 columns
+  d |= (uint64_t)(1024 >> 4) << 32;           // stride: the next 8 rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+struct Ring {
+  uint32_t i, ph;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1u;
     }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) acc[y][x] = fmaf(sd[n][(tid / 16) * 4 + y], sw[n][(tid % 16) + 16 * x], acc[y][x]);
-    __syncthreads();
   }
-  for (int y = 0; y < 4; ++y) {
-    const int m = m0 + (tid / 16) * 4 + y;
-    if (m >= a.M) continue;
-    for (int x = 0; x < 4; ++x) {
-      const int k = k0 + tid % 16 + 16 * x;
-      float v = acc[y][x];
+};
+
+// Four codes (two's-complement bytes) times sw, as two bf16 pairs.
+// A byte b = q + 128 in the low mantissa bits of 2^23 is 8388608 + b exactly.
+__device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw) {
+  const uint32_t x = w ^ 0x80808080u;
+  const float2 bias = make_float2(-8388736.f, -8388736.f);
+  float2 p = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440)),
+                         __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441)));
+  float2 q = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442)),
+                         __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443)));
+  p = __fmul2_rn(__fadd2_rn(p, bias), sw);
+  q = __fmul2_rn(__fadd2_rn(q, bias), sw);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(p.x, p.y), b = __floats2bfloat162_rn(q.x, q.y);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ void grace() {
+  const unsigned long long t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kGraceNs) __nanosleep(1000);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_backward_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
+  using Sh = BwdShape<NT>;
+  constexpr int S_ = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  auto stage_a = [&](int st) { return smem + st * Sh::kStage; };
+  auto stage_b = [&](int st) { return smem + st * Sh::kStage + Sh::kA; };
+  auto raw_slot = [&](int sl) { return smem + S_ * Sh::kStage + sl * kRawBytes; };
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S_ * Sh::kStage + kRawSlots * kRawBytes);
+  uint64_t* raw_empty = raw_full + kRawSlots;
+  uint64_t* a_full = raw_empty + kRawSlots;  // transform warps done with the stage
+  uint64_t* b_full = a_full + S_;            // dY landed
+  uint64_t* done = b_full + S_;              // the stage's MMAs are complete
+  uint64_t* acc_full = done + S_;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* epi_sync = acc_empty + 2;
+  uint64_t* drain = epi_sync + 1;
+  volatile uint32_t* raw_int4 = reinterpret_cast<volatile uint32_t*>(drain + 1);
+  uint32_t* tmem_slot = const_cast<uint32_t*>(raw_int4 + kRawSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* last_flag = abort_flag + 1;
+  volatile int* never_flag = abort_flag + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kXfWarps);
+    }
+    for (int i = 0; i < S_; ++i) {
+      mbar_init(&a_full[i], kXfWarps);
+      mbar_init(&b_full[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps);
+    }
+    mbar_init(epi_sync, 32 * kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never_flag = 0;
+    fence_mbar_init();
+    if (a.T8 > 0) prefetch_tmap(&maps.w8);
+    if (a.T4 > 0) prefetch_tmap(&maps.w4);
+    prefetch_tmap(&maps.dy);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, Sh::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_launch_dependents();
+
+  auto fail = [&](int info) {
+    *abort_flag = 1;
+    record_error(a.ws, AQ_ERR_TIMEOUT, info, a.ws_clear);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ weight producer
+    int u = blockIdx.x;  // unit that holds this lane's next step, and the step it starts at
+    uint32_t base = 0, g = lane;
+    BwdUnit x = bwd_unit(a, u);
+    // first row in its precision's buffer, offset of the scales, INT4 label: 2 = past the end
+    auto fetch = [&](uint32_t& row, uint32_t& sc, uint32_t& kind) {
+      while (u < a.units && g >= base + (uint32_t)(x.i1 - x.i0)) {
+        base += x.i1 - x.i0;
+        u += gridDim.x;
+        if (u < a.units) x = bwd_unit(a, u);
+      }
+      kind = 2;
+      row = sc = 0;
+      if (u < a.units) {
+        const int n0 = (x.i0 + (int)(g - base)) * kStep, r = n0 / a.bN, in = n0 - r * a.bN;
+        const int t = r * a.C + x.kb;
+        kind = __ldg(a.bitmap + (t >> 3)) >> (t & 7) & 1;
+        row = (uint32_t)__ldg(a.tile_idx + t) * a.bN + in;
+        sc = (uint32_t)t * a.bN + in;
+      }
+      g += 32;
+    };
+    uint32_t row[2], sc[2], kind[2];
+    fetch(row[0], sc[0], kind[0]);
+    Ring rr{0, 0};
+    bool more = true, ok = true;
+    while (more && ok) {
+      fetch(row[1], sc[1], kind[1]);
+      for (int i = 0; i < 32 && ok; ++i) {
+        const uint32_t k = __shfl_sync(0xffffffffu, kind[0], i), r = __shfl_sync(0xffffffffu, row[0], i),
+                       s = __shfl_sync(0xffffffffu, sc[0], i);
+        if (k == 2) {
+          more = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, lane != 0 || mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag))) {
+          fail(1);
+          ok = false;
+        } else if (lane == 0) {
+          raw_int4[rr.i] = k;
+          uint8_t* dst = raw_slot(rr.i);
+          mbar_arrive_expect_tx(&raw_full[rr.i], (k ? kStep * kTileK / 2 : kStep * kTileK) + kStep * 2);
+          tma_load_2d(dst, k ? &maps.w4 : &maps.w8, 0, (int)r, &raw_full[rr.i]);
+          bulk_load(dst + kStep * kTileK, a.scales + s, kStep * 2, &raw_full[rr.i]);
+        }
+        rr.next<kRawSlots>();
+      }
+      row[0] = row[1];
+      sc[0] = sc[1];
+      kind[0] = kind[1];
+    }
+    if (lane == 0 && (!ok || *abort_flag)) grace();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0))), bdesc0 = sw128_desc(smem_u32(stage_b(0)));
+      Ring sr{0, 0};
+      bool ok = true, any = false;
+      int ui = 0;
+      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++ui) {
+        const BwdUnit x = bwd_unit(a, u);
+        const int buf = ui & 1;
+        if (!mbar_wait(&acc_empty[buf], ((ui >> 1) & 1) ^ 1, abort_flag)) {
+          fail(2);
+          break;
+        }
+        const uint32_t d = tmem_base + buf * NT;
+        for (int i = x.i0; i < x.i1; ++i) {
+          if (!mbar_wait(&b_full[sr.i], sr.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
+            fail(3);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t off = (uint64_t)((sr.i * Sh::kStage) >> 4);
+#pragma unroll
+          for (int k = 0; k < kStep / 16; ++k)  // 16 rows: two groups of A, 32 bytes of B
+            mma_bf16(d, adesc0 + off + 128 * k, bdesc0 + off + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
+          mma_commit(&done[sr.i]);
+          any = true;
+          sr.template next<S_>();
+        }
+        if (ok) mma_commit(&acc_full[buf]);
+      }
+      if (any) {  // every MMA issued is complete before tensor memory is freed
+        mma_commit(drain);
+        mbar_wait(drain, 0, never_flag);
+      }
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ dY producer
+    if (lane == 0) {
+      pdl_wait();
+      Ring sr{0, 0};
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+        const BwdUnit x = bwd_unit(a, u);
+        for (int i = x.i0; i < x.i1; ++i) {
+          if (!mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag)) {
+            fail(4);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&b_full[sr.i], Sh::kB);
+          tma_load_2d(stage_b(sr.i), &maps.dy, i * kStep, x.tb * NT, &b_full[sr.i]);
+          sr.template next<S_>();
+        }
+      }
+      if (!ok || *abort_flag) grace();
+    }
+  } else if (warp >= kXfWarp0 && warp < kEpiWarp0) {
+    // ------------------------------------------------------------ transform
+    // 8 codes of one row per thread and round: 16 threads cover a row, so that
+    // a quarter warp writes the eight 16-byte chunks of one 128-byte row.
+    const int t = threadIdx.x - 32 * kXfWarp0, c = t & 15, r0 = t >> 4;
+    Ring sr{0, 0}, rr{0, 0};
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+      const BwdUnit x = bwd_unit(a, u);
+      for (int i = x.i0; i < x.i1; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag) &&
+                                         mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag))) {
+          fail(5);
+          ok = false;
+          break;
+        }
+        const uint8_t* src = raw_slot(rr.i);
+        const uint16_t* scl = reinterpret_cast<const uint16_t*>(src + kStep * kTileK);
+        uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kStep * 128);
+        const bool is4 = raw_int4[rr.i];
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k) {
+          const int r = r0 + 16 * k;
+          float s = __half2float(__ushort_as_half(scl[r]));
+          uint2 v;
+          if (is4) {  // nibbles as 16 q: see tc_linear.cu
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * (kTileK / 2) + c * 4);
+            const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
+            v = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+            s *= 0.0625f;
+          } else {
+            v = *reinterpret_cast<const uint2*>(src + r * kTileK + c * 8);
+          }
+          const float2 s2 = make_float2(s, s);
+          const uint2 e0 = codes4(v.x, s2), e1 = codes4(v.y, s2);
+          *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&a_full[sr.i]);
+          mbar_arrive(&raw_empty[rr.i]);
+        }
+        sr.template next<S_>();
+        rr.template next<kRawSlots>();
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    const size_t kcol = 32 * quad + lane;
+    pdl_wait();
+    uint32_t sync_phase = 0;
+    int ui = 0;
+    bool ok = true;
+    auto put = [&](int m, size_t k, float v) {
       if (a.f32) {
         if (a.add) v += static_cast<const float*>(a.add)[(size_t)m * a.ldadd + k];
         static_cast<float*>(a.dx)[(size_t)m * a.lddx + k] = v;
@@ -65,20 +393,155 @@ __global__ void __launch_bounds__(256) linear_backward_kernel(const BwdArgs a) {
         if (a.add) v += bf16_bits_to_float(static_cast<const uint16_t*>(a.add)[(size_t)m * a.ldadd + k]);
         static_cast<__nv_bfloat16*>(a.dx)[(size_t)m * a.lddx + k] = __float2bfloat16_rn(v);
       }
+    };
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++ui) {
+      const BwdUnit x = bwd_unit(a, u);
+      const int buf = ui & 1, m0 = x.tb * NT;
+      const size_t k = (size_t)x.kb * kTileK + kcol;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (ui >> 1) & 1, abort_flag))) {
+        fail(6);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT;
+      for (int c0 = 0; c0 < NT; c0 += 16) {
+        if (m0 + c0 >= a.M) break;
+        uint32_t v[16];
+        tmem_ld16(taddr + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          asm volatile("" : "+r"(v[e]));
+          const int m = m0 + c0 + e;
+          if (m < a.M) {
+            if (a.S > 1) __stcg(a.partial + ((size_t)x.s * a.M + m) * a.K + k, __uint_as_float(v[e]));
+            else put(m, k, __uint_as_float(v[e]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (a.S == 1) continue;
+      // the CTA that comes last adds the splits in increasing order
+      __threadfence();
+      mbar_arrive(epi_sync);
+      if (!__all_sync(0xffffffffu, mbar_wait(epi_sync, sync_phase, abort_flag))) {
+        fail(7);
+        break;
+      }
+      sync_phase ^= 1;
+      int* counter = a.counters + x.kb * a.ntb + x.tb;
+      if (quad == 0 && lane == 0) *last_flag = atomicAdd(counter, 1) == a.S - 1;
+      mbar_arrive(epi_sync);
+      if (!__all_sync(0xffffffffu, mbar_wait(epi_sync, sync_phase, abort_flag))) {
+        fail(8);
+        break;
+      }
+      sync_phase ^= 1;
+      if (*last_flag) {
+        __threadfence();
+        const int m1 = min(m0 + NT, a.M);
+        for (int m = m0; m < m1; ++m) {
+          float v = 0.f;
+          for (int s = 0; s < a.S; ++s) v += __ldcg(a.partial + ((size_t)s * a.M + m) * a.K + k);
+          put(m, k, v);
+        }
+        if (quad == 0 && lane == 0) *counter = 0;
+      }
     }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Sh::kTmemCols);
+  }
 }
+
+// ---------------------------------------------------------------- host side
+struct BwdPlan {
+  int nt, ntb, S;
+};
+
+// Token-block width and splits.  A step takes the longer of the MMAs (2 NT
+// cycles) and the dequantization; whole units go to the CTAs in waves.
+BwdPlan plan_bwd(int M, int N, int C) {
+  const int sms = num_sms(), steps = N / kStep;
+  BwdPlan best{0, 0, 1};
+  long long best_cost = 0;
+  for (int nt : {32, 64, 128, 192, 256}) {
+    const int ntb = (M + nt - 1) / nt;
+    const long long blocks = (long long)C * ntb;
+    const int S = (int)std::max<long long>(1, std::min<long long>({sms / blocks, (long long)steps / 4, kMaxBwdSplits}));
+    const long long waves = (blocks * S + sms - 1) / sms;
+    const long long cost = waves * ((steps + S - 1) / S + 4) * std::max(2 * nt, 400);
+    if (best.nt == 0 || cost < best_cost) {
+      best = {nt, ntb, S};
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+size_t bwd_counter_bytes(const BwdPlan& p, int C) { return ((size_t)C * p.ntb * sizeof(int) + 255) / 256 * 256; }
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch,
+            uint32_t box_cols, uint32_t box_rows, bool swizzle) {
+  EncodeFn fn = encode();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+cudaError_t launch_bwd(const aq_packed* w, const uint16_t* dy, int ldd, const BwdArgs& a, cudaStream_t st) {
+  using Sh = BwdShape<NT>;
+  cudaError_t e = ensure_smem_attr<linear_backward_kernel<NT>>(Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  BwdMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  bool ok = map_2d(&maps.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, a.N, a.M, (uint64_t)ldd * 2, kStep, NT, true);
+  if (ok && w->T8 > 0)
+    ok = map_2d(&maps.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->w8, kTileK, (uint64_t)w->T8 * w->bN, kTileK, kTileK, kStep, false);
+  if (ok && w->T4 > 0)
+    ok = map_2d(&maps.w4, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->w4, kTileK / 2, (uint64_t)w->T4 * w->bN, kTileK / 2,
+                kTileK / 2, kStep, false);
+  if (!ok) return cudaErrorInvalidValue;
+  return launch_pdl(linear_backward_kernel<NT>, dim3(std::min(a.units, num_sms())), dim3(kThreads), (size_t)Sh::kSmem,
+                    st, maps, a);
+}
+
+constexpr int kMaxBwdTokens = 1 << 21;
 
 }  // namespace
 }  // namespace aq
 
 using namespace aq;
 
-static constexpr int kMaxBwdTokens = 1 << 21;
-
 extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) {
   if (validate_packed(w) != AQ_OK || M < 1 || M > kMaxBwdTokens) return 0;
-  return kWsHeader;
+  const BwdPlan p = plan_bwd(M, w->N, w->C);
+  return kWsHeader + bwd_counter_bytes(p, w->C) + (p.S > 1 ? (size_t)p.S * M * w->K * sizeof(float) : 0);
 }
 
 extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
@@ -92,9 +555,28 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   if (add && (ldadd < w->K || ldadd % per16 || ((uintptr_t)add & 15))) return AQ_ERR_ARG;
   if (!ws || ws_bytes < aq_linear_backward_workspace_bytes(M, w)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
-  BwdArgs a{*w, dy, ldd, M, add, dx, ldadd, lddx, dxdtype == AQ_F32};
-  return launch_pdl(linear_backward_kernel, dim3(w->K / kT, (M + kT - 1) / kT), dim3(256), 0,
-                    static_cast<cudaStream_t>(stream), a) == cudaSuccess
-             ? AQ_OK
-             : AQ_ERR_CUDA;
+  const BwdPlan p = plan_bwd(M, w->N, w->C);
+  const size_t counters = bwd_counter_bytes(p, w->C);
+  BwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.bitmap = w->bitmap; a.tile_idx = w->tile_idx; a.scales = w->scales;
+  a.N = w->N; a.K = w->K; a.bN = w->bN; a.C = w->C; a.T4 = w->T4; a.T8 = w->T8;
+  a.M = M; a.ntb = p.ntb; a.S = p.S; a.steps = w->N / kStep;
+  if ((long long)w->C * p.ntb * p.S > 0x7FFFFFFFll) return AQ_ERR_ARG;
+  a.units = w->C * p.ntb * p.S;
+  a.add = add; a.dx = dx; a.ldadd = ldadd; a.lddx = lddx; a.f32 = dxdtype == AQ_F32;
+  a.ws = ws;
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader + counters);
+  a.ws_clear = p.S > 1 ? (int)counters : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (p.nt) {
+    case 32: e = launch_bwd<32>(w, dy, ldd, a, st); break;
+    case 64: e = launch_bwd<64>(w, dy, ldd, a, st); break;
+    case 128: e = launch_bwd<128>(w, dy, ldd, a, st); break;
+    case 192: e = launch_bwd<192>(w, dy, ldd, a, st); break;
+    case 256: e = launch_bwd<256>(w, dy, ldd, a, st); break;
+  }
+  return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }
