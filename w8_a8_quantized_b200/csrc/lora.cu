@@ -14,7 +14,7 @@
 //
 // Products run on mma.sync (bf16 in, fp32 out): the tables and x, dy are bf16
 // (8-bit codes are exact in bf16), and S and T, fp32, enter as three bf16 terms
-// (24 significant bits), so that no operand loses bits.  Sums are fp32.
+// (24 significant bits; two where the result is rounded to bf16).  Sums are fp32.
 //
 // A tile is 64 consecutive tokens.  A kernel lists the adapters that occur in
 // its tile and runs them one after another on the same activations: requests
@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "aq_internal.cuh"
+#include "lora.cuh"
 
 namespace aq {
 namespace {
@@ -294,138 +295,197 @@ struct ExpandArgs {
   int splits, kz;
   const void* y;   // or null
   void* out;
-  int ldy, ldo, f32;
+  int ldy, ldo;
   float* s;        // [M][max_rank] or null: the summed products
+  int rp;          // ranks of a tile's products in shared memory: max_rank rounded up to 16
+  int wrows;       // table rows per slot: min(rp, kRank)
 };
 
-struct ExpandSmem {
-  TileList q;
-  uint16_t w[2][kRank][kLd];
-  // then three terms of S: [3][kTok][ranks + 8]
+// A CTA takes one tile of tokens and a range of column blocks: the list of
+// adapters and the products' bf16 terms are made once, then the blocks stream
+// through two buffers of table rows and two of y (16-byte copies, one item
+// ahead); sums go into the y buffer and leave it as 16-byte stores.
+// F32: fp32 y and out, 64 columns a block and three terms of S; otherwise bf16,
+// 128 columns and two terms: 2^-17 of a product, far below the rounding of out.
+template <bool F32>
+struct ExpandShape {
+  static constexpr int kBN = F32 ? 64 : 128, kTerms = F32 ? 3 : 2;
+  static constexpr int kLdW = kBN + 8;                // bf16 elements
+  static constexpr int kElt = F32 ? 4 : 2, kPer16 = 16 / kElt;
+  static constexpr int kLdY = kBN + kPer16;           // elements of y: rows of 272 bytes
+  static constexpr int kYBytes = kTok * kLdY * kElt;
+  static constexpr int kNt = kBN / 16;                // 8-column tiles of a warp (half the block)
+  static size_t smem(int rp) {
+    return sizeof(TileList) + 2 * kYBytes + 2 * (size_t)std::min(rp, kRank) * kLdW * 2 +
+           (size_t)kTerms * kTok * (rp + 8) * 2;
+  }
 };
 
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const ExpandArgs a) {
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const ExpandArgs a) {
+  using Sh = ExpandShape<F32>;
+  constexpr int BN = Sh::kBN, NT = Sh::kNt;
   extern __shared__ __align__(16) uint8_t raw[];
-  ExpandSmem& sm = *reinterpret_cast<ExpandSmem*>(raw);
-  uint16_t* terms = reinterpret_cast<uint16_t*>(raw + sizeof(ExpandSmem));
+  TileList& q = *reinterpret_cast<TileList*>(raw);
+  uint8_t* ybuf = raw + sizeof(TileList);
+  uint16_t* wbuf = reinterpret_cast<uint16_t*>(ybuf + 2 * Sh::kYBytes);
+  uint16_t* terms = wbuf + 2 * a.wrows * Sh::kLdW;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int m0 = blockIdx.y * kTok, n0 = blockIdx.x * kDC, zi = blockIdx.z;
+  const int m0 = blockIdx.y * kTok, zi = blockIdx.z;
   const Table& t = a.t;
-  const int rp = (t.max_rank + 15) / 16 * 16, lds = rp + 8, plane = kTok * lds;
+  const int lds = a.rp + 8, plane = kTok * lds;
+  const int blocks = (t.D + BN - 1) / BN;
+  const int b0 = (int)((long long)blocks * blockIdx.x / gridDim.x);
+  const int b1 = (int)((long long)blocks * (blockIdx.x + 1) / gridDim.x);
   pdl_launch_dependents();
   pdl_wait();
-  list_tile(t, a.ids, m0, a.M, 0, zi, a.kz, sm.q);
-  const int na = sm.q.n;
+  list_tile(t, a.ids, m0, a.M, 0, zi, a.kz, q);
+  const int na = q.n;
 
-  // S of this tile, as three bf16 terms; zero behind the token's rank
-  for (int i = tid; i < kTok * rp; i += kThreads) {
-    const int r = i / rp, c = i % rp, s = sm.q.slot[r];
-    if (s == -1 || m0 + r >= a.M) continue;
-    float v = 0.f;
-    if (s >= 0 && c < sm.q.rank[s])
-      for (int k = 0; k < a.splits; ++k) v += __ldg(a.p + ((size_t)k * a.M + m0 + r) * t.max_rank + c);
-    if (a.s && blockIdx.x == 0 && c < t.max_rank && (s >= 0 || zi == 0))
-      a.s[(size_t)(m0 + r) * t.max_rank + c] = v;
-    uint16_t* d = terms + r * lds + c;
-    split3(v, d[0], d[plane], d[2 * plane]);
-  }
-
-  // items: (adapter, block of 64 ranks)
-  int ia = 0, ir = 0, ib = 0;
+  // items: (column block, adapter, block of 64 ranks); a block without an
+  // adapter has one empty item
+  int ib = b0, ia = 0, ir = 0, is = 0;  // next item to issue
   auto issue = [&]() {
-    if (ia < na) {
-      const int nr = min(sm.q.rank[ia] - ir, kRank), row0 = sm.q.row0[ia] + ir;
-      const int rows = (nr + 15) & ~15;
-      for (int i = tid; i < rows * (kDC / 8); i += kThreads) {
-        const int r = i / (kDC / 8), c = i % (kDC / 8) * 8;
-        const bool in = r < nr && n0 + c < t.D;
-        cp16(&sm.w[ib][r][c], in ? t.w + (size_t)(row0 + r) * t.D + n0 + c : t.w, in);
+    if (ib < b1) {
+      const int n0 = ib * BN;
+      if (ia == 0 && ir == 0 && a.y) {
+        uint8_t* dst = ybuf + (ib & 1) * Sh::kYBytes;
+        for (int i = tid; i < kTok * 16; i += kThreads) {
+          const int r = i >> 4, c = (i & 15) * Sh::kPer16, s = q.slot[r];
+          const bool in = m0 + r < a.M && n0 + c < t.D && (s >= 0 || (s == -2 && zi == 0));
+          const uint8_t* src = static_cast<const uint8_t*>(a.y);
+          cp16(dst + (r * Sh::kLdY + c) * Sh::kElt,
+               in ? src + ((size_t)(m0 + r) * a.ldy + n0 + c) * Sh::kElt : src, in);
+        }
       }
-      ib ^= 1;
+      if (ia < na) {
+        const int nr = min(q.rank[ia] - ir, kRank), row0 = q.row0[ia] + ir;
+        const int rows = (nr + 15) & ~15;
+        uint16_t* dst = wbuf + is * a.wrows * Sh::kLdW;
+        for (int i = tid; i < rows * (BN / 8); i += kThreads) {
+          const int r = i / (BN / 8), c = i % (BN / 8) * 8;
+          const bool in = r < nr && n0 + c < t.D;
+          cp16(dst + r * Sh::kLdW + c, in ? t.w + (size_t)(row0 + r) * t.D + n0 + c : t.w, in);
+        }
+      }
+      is ^= 1;
       ir += kRank;
-      if (ir >= sm.q.rank[ia]) {
+      if (ia >= na || ir >= q.rank[ia]) {
         ir = 0;
-        ++ia;
+        if (++ia >= na) {
+          ia = 0;
+          ++ib;
+        }
       }
     }
     cp_commit();
   };
   issue();
+
+  // S of this tile as bf16 terms, zero behind the token's rank
+  for (int r = tid >> 4; r < kTok; r += kThreads / 16) {
+    const int s = q.slot[r], m = m0 + r;
+    if (s == -1 || m >= a.M) continue;
+    const int rank = s >= 0 ? q.rank[s] : 0;
+    for (int c = tid & 15; c < a.rp; c += 16) {
+      float v = 0.f;
+      if (c < rank) {
+        const float* src = a.p + (size_t)m * t.max_rank + c;
+        const size_t step = (size_t)a.M * t.max_rank;
+#pragma unroll 8
+        for (int k = 0; k < a.splits; ++k) v += __ldg(src + k * step);
+      }
+      if (a.s && blockIdx.x == 0 && c < t.max_rank && (s >= 0 || zi == 0)) a.s[(size_t)m * t.max_rank + c] = v;
+      uint16_t hi, mid, lo;
+      split3(v, hi, mid, lo);
+      uint16_t* d = terms + r * lds + c;
+      d[0] = hi;
+      d[plane] = mid;
+      if (Sh::kTerms > 2) d[2 * plane] = lo;
+    }
+  }
+
   const int sub = warp & 3, nh = warp >> 2;
-  float delta[8][4], acc[8][4];
+  float delta[NT][4], acc[NT][4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) delta[j][e] = acc[j][e] = 0.f;
-  int wb = 0;
-  for (int al = 0; al < na; ++al) {
-    const int rank = sm.q.rank[al];
-    const uint32_t mine = (uint32_t)(sm.q.mask[al] >> (16 * sub)) & 0xFFFFu;
-    for (int r0 = 0; r0 < rank; r0 += kRank) {
-      cp_wait<0>();
-      __syncthreads();
-      issue();
-      if (mine) {
-        const int ksteps = (min(rank - r0, kRank) + 15) / 16;
-        for (int ks = 0; ks < ksteps; ++ks) {
-          uint32_t fb[4][4];
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  int ws = 0;
+  for (int b = b0; b < b1; ++b) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            ldsm4t(fb[j], &sm.w[wb][16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1)][64 * nh + 16 * j + 8 * (lane >> 4)]);
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int sp = 2; sp >= 0; --sp) {
-            uint32_t fa[4];
-            ldsm4(fa, terms + sp * plane + (16 * sub + (lane & 7) + 8 * ((lane >> 3) & 1)) * lds + r0 + 16 * ks +
-                          8 * (lane >> 4));
+      for (int e = 0; e < 4; ++e) delta[j][e] = 0.f;
+    for (int al = 0; al < max(na, 1); ++al) {
+      const int rank = al < na ? q.rank[al] : 1;
+      const uint32_t mine = al < na ? (uint32_t)(q.mask[al] >> (16 * sub)) & 0xFFFFu : 0u;
+      for (int r0 = 0; r0 < rank; r0 += kRank) {
+        cp_wait<0>();
+        __syncthreads();
+        issue();
+        if (mine) {
+          const uint16_t* w = wbuf + ws * a.wrows * Sh::kLdW;
+          const int ksteps = (min(rank - r0, kRank) + 15) / 16;
+          for (int ks = 0; ks < ksteps; ++ks) {
+            uint32_t fa[Sh::kTerms][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma16816(acc[2 * j], fa, fb[j][0], fb[j][1]);
-              mma16816(acc[2 * j + 1], fa, fb[j][2], fb[j][3]);
+            for (int sp = 0; sp < Sh::kTerms; ++sp)
+              ldsm4(fa[sp], terms + sp * plane + (16 * sub + (lane & 15)) * lds + r0 + 16 * ks + 8 * (lane >> 4));
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+              uint32_t fb[4];
+              ldsm4t(fb, w + (16 * ks + (lane & 15)) * Sh::kLdW + (BN / 2) * nh + 16 * j + 8 * (lane >> 4));
+#pragma unroll
+              for (int sp = Sh::kTerms - 1; sp >= 0; --sp) {
+                mma16816(acc[2 * j], fa[sp], fb[0], fb[1]);
+                mma16816(acc[2 * j + 1], fa[sp], fb[2], fb[3]);
+              }
             }
           }
         }
+        ws ^= 1;
       }
-      wb ^= 1;
+      if (mine) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((mine >> ((lane >> 2) + 8 * (e >> 1))) & 1u) delta[j][e] = acc[j][e];
+            acc[j][e] = 0.f;
+          }
+      }
     }
-    if (mine) {
+    uint8_t* yb = ybuf + (b & 1) * Sh::kYBytes;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+    for (int h = 0; h < 2; ++h) {
+      const int r = 16 * sub + (lane >> 2) + 8 * h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((mine >> ((lane >> 2) + 8 * (e >> 1))) & 1u) delta[j][e] = acc[j][e];
-          acc[j][e] = 0.f;
+      for (int j = 0; j < NT; ++j) {
+        const int c = (BN / 2) * nh + 8 * j + 2 * (lane & 3);
+        float v0 = delta[j][2 * h], v1 = delta[j][2 * h + 1];
+        if constexpr (F32) {
+          float2* d = reinterpret_cast<float2*>(yb + (r * Sh::kLdY + c) * 4);
+          const float2 y = a.y ? *d : make_float2(0.f, 0.f);
+          *d = make_float2(y.x + v0, y.y + v1);
+        } else {
+          uint32_t* d = reinterpret_cast<uint32_t*>(yb + (r * Sh::kLdY + c) * 2);
+          const uint32_t y = a.y ? *d : 0u;
+          const __nv_bfloat162 o =
+              __floats2bfloat162_rn(bf16_bits_to_float(y & 0xFFFFu) + v0, bf16_bits_to_float(y >> 16) + v1);
+          *d = *reinterpret_cast<const uint32_t*>(&o);
         }
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < kTok * 16; i += kThreads) {
+      const int r = i >> 4, c = (i & 15) * Sh::kPer16, s = q.slot[r], n = b * BN + c;
+      if (m0 + r < a.M && n < t.D && (s >= 0 || (s == -2 && zi == 0)))
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + ((size_t)(m0 + r) * a.ldo + n) * Sh::kElt) =
+            *reinterpret_cast<const uint4*>(yb + (r * Sh::kLdY + c) * Sh::kElt);
     }
   }
   cp_wait<0>();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 16 * sub + (lane >> 2) + 8 * h, m = m0 + r, s = sm.q.slot[r];
-    if (m >= a.M || s == -1 || (s == -2 && zi != 0)) continue;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int n = n0 + 64 * nh + 8 * j + 2 * (lane & 3);
-      if (n >= t.D) continue;
-      float v0 = delta[j][2 * h], v1 = delta[j][2 * h + 1];
-      if (a.f32) {
-        if (a.y) {
-          const float2 y = *reinterpret_cast<const float2*>(static_cast<const float*>(a.y) + (size_t)m * a.ldy + n);
-          v0 += y.x;
-          v1 += y.y;
-        }
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + (size_t)m * a.ldo + n) = make_float2(v0, v1);
-      } else {
-        if (a.y) {
-          const uint32_t y =
-              *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.y) + (size_t)m * a.ldy + n);
-          v0 += bf16_bits_to_float(y & 0xFFFFu);
-          v1 += bf16_bits_to_float(y >> 16);
-        }
-        const __nv_bfloat162 o = __floats2bfloat162_rn(v0, v1);
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + (size_t)m * a.ldo + n) = o;
-      }
-    }
-  }
 }
 
 // ---------------------------------------------------------------- outer
@@ -620,15 +680,23 @@ cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* id
   return launch_pdl(lora_shrink_kernel, grid, dim3(kThreads), sizeof(ShrinkSmem), st, a);
 }
 
+template <bool F32>
+cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t st) {
+  using Sh = ExpandShape<F32>;
+  cudaError_t e = ensure_smem_attr<lora_expand_kernel<F32>>((int)Sh::smem(kMaxRank));
+  if (e != cudaSuccess) return e;
+  // about six CTAs per SM in all: the last wave is short, and the work that a
+  // CTA does once stays a small part of it
+  const int tiles = ceil_div(a.M, kTok), blocks = ceil_div(a.t.D, Sh::kBN);
+  const dim3 grid(std::max(1, std::min(blocks, ceil_div(6 * num_sms(), tiles * a.kz))), tiles, a.kz);
+  return launch_pdl(lora_expand_kernel<F32>, grid, dim3(kThreads), Sh::smem(a.rp), st, a);
+}
+
 cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, int splits, const void* y, int ldy,
                    void* out, int ldo, int dtype, float* s, cudaStream_t st) {
-  ExpandArgs a{t, ids, M, p, splits, share(M, t), y, out, ldy, ldo, dtype == AQ_F32, s};
-  const size_t most = sizeof(ExpandSmem) + 3 * kTok * (kMaxRank + 8) * 2;
-  const size_t smem = sizeof(ExpandSmem) + 3 * kTok * ((t.max_rank + 15) / 16 * 16 + 8) * 2;
-  cudaError_t e = ensure_smem_attr<lora_expand_kernel>((int)most);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(ceil_div(t.D, kDC), ceil_div(M, kTok), a.kz);
-  return launch_pdl(lora_expand_kernel, grid, dim3(kThreads), smem, st, a);
+  const int rp = (t.max_rank + 15) / 16 * 16;
+  const ExpandArgs a{t, ids, M, p, splits, share(M, t), y, out, ldy, ldo, s, rp, std::min(rp, kRank)};
+  return dtype == AQ_F32 ? launch_expand<true>(a, st) : launch_expand<false>(a, st);
 }
 
 cudaError_t outer(const Table& t, const int32_t* ids, int M, const float* p, int psplits, const void* x,
@@ -690,6 +758,9 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 0)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (lora_decode_fits(ad, M))
+    return launch_lora_decode(ad, x, ldx, ids, M, y, ldy, out, ldo, ydtype == AQ_F32, s, st) == cudaSuccess ? AQ_OK
+                                                                                                            : AQ_ERR_CUDA;
   const Table ta = table_a(ad);
   float* p = static_cast<float*>(ws);
   cudaError_t e = shrink(ta, x, ldx, ids, M, p, st);
