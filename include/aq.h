@@ -443,6 +443,7 @@ typedef struct aq_lora {
  *        aq_lora_backward takes
  *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned; its contents
  *        need no initialization, and calls that share it must not run concurrently
+ *        (one of 16 bytes is not touched: decode batches need none)
  * Rows are 16-byte aligned: x, y, out on 16 bytes, ld % 8 == 0 (bf16) or
  * ld % 4 == 0 (fp32).  1 <= M <= 4194240.  Asynchronous.
  * Errors: AQ_ERR_ARG, AQ_ERR_SHAPE (N, K, L, R, max_rank), AQ_ERR_WORKSPACE, AQ_ERR_CUDA.

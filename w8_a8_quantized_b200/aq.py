@@ -600,21 +600,48 @@ class Group:
 AQ_LORA_MAX_RANK = 256
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int):
-    """A 2-D [>= M][>= width] tensor with unit inner stride whose rows the kernels
-    read or write through a leading dimension."""
+_F32, _BF16 = torch.float32, torch.bfloat16
+# the current stream's handle without building a stream object (2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _stream
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int) -> int:
+    """Check a 2-D [>= M][>= width] tensor with unit inner stride whose rows the
+    kernels read or write; returns its leading dimension (a single row's stride
+    says nothing: its width rounded up stands in)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must live on {device if device is not None else 'a CUDA device'}")
-    if t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < M or t.shape[1] < width or \
-            (t.shape[0] > 1 and t.stride(0) < width):
-        raise ValueError(f"{name} must be [>= {M}][>= {width}] with unit inner stride and rows that do not overlap")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must live on {device if device.type == 'cuda' else 'a CUDA device'}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and stride[1] == 1 and shape[0] >= M and shape[1] >= width:
+        if shape[0] == 1:
+            return -(-shape[1] // 16) * 16
+        if stride[0] >= width:
+            return stride[0]
+    raise ValueError(f"{name} must be [>= {M}][>= {width}] with unit inner stride and rows that do not overlap")
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Leading dimension; a single row's stride says nothing, so its width stands in."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
+def _matrix(t: torch.Tensor, name: str):
+    """Rows, columns and device of the 2-D tensor that sets a call's sizes."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D torch.bfloat16 tensor")
+    return *t.shape, t.device
+
+
+def _call(fn, name: str, device, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != AQ_OK:
+        raise AqError(rc, name)
+
+
+_NO_WS = 16  # workspace bytes of a call that does not touch its workspace
 
 
 class Adapters:
@@ -641,18 +668,16 @@ class Adapters:
         self.struct = AqLoraStruct(N=bt.shape[1], K=a.shape[1], L=len(self.ranks), R=a.shape[0],
                                    max_rank=max(self.ranks), a=a.data_ptr(), bt=bt.data_ptr(),
                                    off=self.off.data_ptr(), scale=self.scale.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+        self.N, self.K, self.L, self.R, self.max_rank = (getattr(self.struct, n) for n in ("N", "K", "L", "R", "max_rank"))
+        self.ws_bytes = {}  # workspace bytes by (tokens, backward): a function of the sizes alone
+        self.no_ws = torch.empty(_NO_WS, dtype=torch.uint8, device=self.device)  # for calls that touch no workspace
 
     @classmethod
     def from_pairs(cls, pairs, scales) -> "Adapters":
         """From (A [r][K], B [N][r]) bf16 pairs on one CUDA device."""
         return cls(torch.cat([a for a, _ in pairs]).contiguous(), torch.cat([b.t() for _, b in pairs]).contiguous(),
                    [a.shape[0] for a, _ in pairs], scales)
-
-    N = property(lambda s: s.struct.N)
-    K = property(lambda s: s.struct.K)
-    L = property(lambda s: s.struct.L)
-    R = property(lambda s: s.struct.R)
-    max_rank = property(lambda s: s.struct.max_rank)
 
     def split(self, da: torch.Tensor, dbt: torch.Tensor):
         """Views of aq_lora_backward's gradients per adapter: (dA [r][K], dB [N][r]) pairs."""
@@ -663,16 +688,20 @@ def aq_lora_workspace_bytes(ad: Adapters, M: int, backward: bool) -> int:
     return int(lib().aq_lora_workspace_bytes(ctypes.byref(ad.struct), M, int(bool(backward))))
 
 
-def _lora_ws(ad: Adapters, M: int, backward: bool, ws):
+def _lora_ws(ad: Adapters, M: int, backward: int, ws):
     """The call's workspace: the caller's, or a fresh one from torch's allocator (it
     needs no initialization, so nothing is shared between calls, streams or graphs)."""
-    need = aq_lora_workspace_bytes(ad, M, backward)
+    if ws is not None:
+        _need(ws, "ws", torch.uint8, ad.device)
+        return ws
+    need = ad.ws_bytes.get((M, backward))
+    if need is None:
+        need = ad.ws_bytes[M, backward] = aq_lora_workspace_bytes(ad, M, backward)
     if need == 0:
         raise ValueError("invalid adapters or token count")
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=ad.device)
-    _need(ws, "ws", torch.uint8, ad.device)
-    return ws
+    if need == _NO_WS:
+        return ad.no_ws
+    return torch.empty(need, dtype=torch.uint8, device=ad.device)
 
 
 def _lora_ids(ad: Adapters, ids: torch.Tensor, M: int):
@@ -681,35 +710,34 @@ def _lora_ids(ad: Adapters, ids: torch.Tensor, M: int):
         raise ValueError(f"ids must be int32 [{M}], one adapter index per token")
 
 
+def _lora_s(ad: Adapters, s: torch.Tensor, M: int):
+    _need(s, "s", torch.float32, ad.device)
+    if s.shape != (M, ad.max_rank):
+        raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
+
+
 def aq_lora_apply(ad: Adapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Tensor = None, s: torch.Tensor = None,
                   out: torch.Tensor = None, out_dtype=torch.float32, ws: torch.Tensor = None) -> torch.Tensor:
     """y + scale_l B_l A_l x per token, l = ids[m] (none outside [0, L)): x bf16 [M][K],
     ids int32 [M], y float32 or bfloat16 [M][N] (None: the adapters' part alone, in
     out_dtype).  out may be y.  s float32 [M][max_rank] receives the products that
     aq_lora_backward takes."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise TypeError("x must be a 2-D torch.bfloat16 tensor")
-    M, dev = x.shape[0], ad.device
-    _rows(x, "x", (torch.bfloat16,), dev, M, ad.K)
+    M, _, _ = _matrix(x, "x")
+    dev, N = ad.device, ad.N
+    ldx = _rows(x, "x", (_BF16,), dev, M, ad.K)
     _lora_ids(ad, ids, M)
-    dtypes = (torch.float32, torch.bfloat16)
+    ldy = 0
     if y is not None:
-        _rows(y, "y", dtypes, dev, M, ad.N)
-        out_dtype = y.dtype
+        ldy, out_dtype = _rows(y, "y", (_F32, _BF16), dev, M, N), y.dtype
     if out is None:
-        out = torch.empty((M, ad.N), dtype=out_dtype, device=dev)
-    _rows(out, "out", dtypes if y is None else (y.dtype,), dev, M, ad.N)
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    ldo = _rows(out, "out", (_F32, _BF16) if y is None else (out_dtype,), dev, M, N)
     if s is not None:
-        _need(s, "s", torch.float32, dev)
-        if tuple(s.shape) != (M, ad.max_rank):
-            raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
-    ws = _lora_ws(ad, M, False, ws)
-    with torch.cuda.device(dev):
-        _check(lib().aq_lora_apply(ctypes.byref(ad.struct), x.data_ptr(), _ld(x), ids.data_ptr(), M,
-                                   y.data_ptr() if y is not None else None, _ld(y) if y is not None else 0,
-                                   out.data_ptr(), _ld(out), AQ_F32 if out.dtype == torch.float32 else AQ_BF16,
-                                   s.data_ptr() if s is not None else None, ws.data_ptr(), ws.numel(), _stream(dev)),
-               "aq_lora_apply")
+        _lora_s(ad, s, M)
+    ws = _lora_ws(ad, M, 0, ws)
+    _call(lib().aq_lora_apply, "aq_lora_apply", dev, ad.ref, x.data_ptr(), ldx, ids.data_ptr(), M,
+          None if y is None else y.data_ptr(), ldy, out.data_ptr(), ldo, AQ_F32 if out.dtype == _F32 else AQ_BF16,
+          None if s is None else s.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -722,44 +750,36 @@ def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch
     8-bit checkpoint (int8 codes with token scales sx, as aq_quant_act made them)
     or bf16 (sx None).  dx = add + the adapters' part, in add's dtype (dx_dtype
     without add); dx may be add."""
-    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
-        raise TypeError("dy must be a 2-D torch.bfloat16 tensor")
-    M, dev = dy.shape[0], ad.device
-    _rows(dy, "dy", (torch.bfloat16,), dev, M, ad.N)
+    M, _, _ = _matrix(dy, "dy")
+    dev, N, K, R = ad.device, ad.N, ad.K, ad.R
+    ldd = _rows(dy, "dy", (_BF16,), dev, M, N)
     _lora_ids(ad, ids, M)
-    _need(s, "s", torch.float32, dev)
-    if tuple(s.shape) != (M, ad.max_rank):
-        raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
-    _rows(x, "x", (torch.bfloat16,) if sx is None else (torch.int8,), dev, M, ad.K)
+    _lora_s(ad, s, M)
+    ldx = _rows(x, "x", (_BF16,) if sx is None else (torch.int8,), dev, M, K)
     if sx is not None:
         _need(sx, "sx", torch.float32, dev)
         if sx.numel() < M:
             raise ValueError(f"sx must hold M = {M} token scales")
-    dtypes = (torch.float32, torch.bfloat16)
+    ldadd = lddx = 0
     if add is not None:
-        _rows(add, "add", dtypes, dev, M, ad.K)
-        dx_dtype = add.dtype
+        ldadd, dx_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if dx is None and (want_dx or add is not None):
-        dx = torch.empty((M, ad.K), dtype=dx_dtype, device=dev)
+        dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
     if dx is not None:
-        _rows(dx, "dx", dtypes if add is None else (add.dtype,), dev, M, ad.K)
+        lddx = _rows(dx, "dx", (_F32, _BF16) if add is None else (dx_dtype,), dev, M, K)
     if da is None:
-        da = torch.empty((ad.R, ad.K), dtype=torch.float32, device=dev)
+        da = torch.empty((R, K), dtype=_F32, device=dev)
     if dbt is None:
-        dbt = torch.empty((ad.R, ad.N), dtype=torch.float32, device=dev)
-    for t, name, width in ((da, "da", ad.K), (dbt, "dbt", ad.N)):
-        _need(t, name, torch.float32, dev)
-        if tuple(t.shape) != (ad.R, width):
-            raise ValueError(f"{name} must be float32 [{ad.R}][{width}]")
-    ws = _lora_ws(ad, M, True, ws)
-    with torch.cuda.device(dev):
-        _check(lib().aq_lora_backward(ctypes.byref(ad.struct), dy.data_ptr(), _ld(dy), ids.data_ptr(), M, s.data_ptr(),
-                                      x.data_ptr(), _ld(x), sx.data_ptr() if sx is not None else None, da.data_ptr(),
-                                      dbt.data_ptr(), add.data_ptr() if add is not None else None,
-                                      _ld(add) if add is not None else 0, dx.data_ptr() if dx is not None else None,
-                                      _ld(dx) if dx is not None else 0,
-                                      AQ_BF16 if dx is None or dx.dtype == torch.bfloat16 else AQ_F32, ws.data_ptr(),
-                                      ws.numel(), _stream(dev)), "aq_lora_backward")
+        dbt = torch.empty((R, N), dtype=_F32, device=dev)
+    for t, name, width in ((da, "da", K), (dbt, "dbt", N)):
+        _need(t, name, _F32, dev)
+        if t.shape != (R, width):
+            raise ValueError(f"{name} must be float32 [{R}][{width}]")
+    ws = _lora_ws(ad, M, 1, ws)
+    _call(lib().aq_lora_backward, "aq_lora_backward", dev, ad.ref, dy.data_ptr(), ldd, ids.data_ptr(), M, s.data_ptr(),
+          x.data_ptr(), ldx, None if sx is None else sx.data_ptr(), da.data_ptr(), dbt.data_ptr(),
+          None if add is None else add.data_ptr(), ldadd, None if dx is None else dx.data_ptr(), lddx,
+          AQ_F32 if dx is not None and dx.dtype == _F32 else AQ_BF16, ws.data_ptr(), ws.numel())
     return da, dbt, dx
 
 
@@ -772,52 +792,43 @@ def aq_silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, keep: bool = False, 
     -> (hq int8 [M][F], sh float32 [M]), the down projection's input.  keep=True
     appends the 8-bit checkpoints of gate and up for aq_silu_mul_backward: (..., gq
     int8 [M][F], gs float32 [M][ceil(F/128)], uq, us)."""
-    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
-        raise TypeError("gate must be a 2-D torch.bfloat16 tensor")
-    (M, F), dev = gate.shape, gate.device
-    _rows(gate, "gate", (torch.bfloat16,), None, M, F)
-    _rows(up, "up", (torch.bfloat16,), dev, M, F)
-    if tuple(up.shape) != (M, F):
+    M, F, dev = _matrix(gate, "gate")
+    ldg, ldu = _rows(gate, "gate", (_BF16,), dev, M, F), _rows(up, "up", (_BF16,), dev, M, F)
+    if up.shape != (M, F):
         raise ValueError("gate and up must have one shape")
-    codes = [hq if hq is not None else torch.empty((M, F), dtype=torch.int8, device=dev)]
-    sh = torch.empty((M,), dtype=torch.float32, device=dev) if sh is None else sh
-    _need(codes[0], "hq", torch.int8, dev)
-    _need(sh, "sh", torch.float32, dev)
-    if tuple(codes[0].shape) != (M, F) or sh.numel() < M:
+    hq = torch.empty((M, F), dtype=torch.int8, device=dev) if hq is None else hq
+    sh = torch.empty((M,), dtype=_F32, device=dev) if sh is None else sh
+    _need(hq, "hq", torch.int8, dev)
+    _need(sh, "sh", _F32, dev)
+    if hq.shape != (M, F) or sh.numel() < M:
         raise ValueError("hq must be int8 [M][F] and sh hold M scales")
-    groups = -(-F // AQ_GATED_GROUP)
-    kept = ()
+    kept, ptrs = (), (None,) * 4
     if keep:
+        groups = -(-F // AQ_GATED_GROUP)
         kept = tuple(t for _ in range(2) for t in (torch.empty((M, F), dtype=torch.int8, device=dev),
-                                                   torch.empty((M, groups), dtype=torch.float32, device=dev)))
-    ptrs = [t.data_ptr() for t in kept] if keep else [None] * 4
-    with torch.cuda.device(dev):
-        _check(lib().aq_silu_mul_quant(gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), M, F, codes[0].data_ptr(),
-                                       sh.data_ptr(), *ptrs, _stream(dev)), "aq_silu_mul_quant")
-    return (codes[0], sh) + kept
+                                                   torch.empty((M, groups), dtype=_F32, device=dev)))
+        ptrs = tuple(t.data_ptr() for t in kept)
+    _call(lib().aq_silu_mul_quant, "aq_silu_mul_quant", dev, gate.data_ptr(), ldg, up.data_ptr(), ldu, M, F,
+          hq.data_ptr(), sh.data_ptr(), *ptrs)
+    return (hq, sh) + kept
 
 
 def aq_silu_mul_backward(dh: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, uq: torch.Tensor, us: torch.Tensor,
                          dgate: torch.Tensor = None, dup: torch.Tensor = None):
     """Gradients of silu(gate) * up from its 8-bit checkpoints: dh bf16 [M][F] ->
     (dgate, dup) bf16 [M][F]."""
-    if not isinstance(dh, torch.Tensor) or dh.dim() != 2:
-        raise TypeError("dh must be a 2-D torch.bfloat16 tensor")
-    (M, F), dev = dh.shape, dh.device
-    _rows(dh, "dh", (torch.bfloat16,), None, M, F)
+    M, F, dev = _matrix(dh, "dh")
+    ldd, groups = _rows(dh, "dh", (_BF16,), dev, M, F), -(-F // AQ_GATED_GROUP)
     for q, s, name in ((gq, gs, "g"), (uq, us, "u")):
         _need(q, name + "q", torch.int8, dev)
-        _need(s, name + "s", torch.float32, dev)
-        if tuple(q.shape) != (M, F) or tuple(s.shape) != (M, -(-F // AQ_GATED_GROUP)):
+        _need(s, name + "s", _F32, dev)
+        if q.shape != (M, F) or s.shape != (M, groups):
             raise ValueError(f"{name}q must be int8 [M][F] and {name}s float32 [M][ceil(F/{AQ_GATED_GROUP})]")
-    dgate = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if dgate is None else dgate
-    dup = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if dup is None else dup
-    _rows(dgate, "dgate", (torch.bfloat16,), dev, M, F)
-    _rows(dup, "dup", (torch.bfloat16,), dev, M, F)
-    with torch.cuda.device(dev):
-        _check(lib().aq_silu_mul_backward(dh.data_ptr(), _ld(dh), gq.data_ptr(), gs.data_ptr(), uq.data_ptr(),
-                                          us.data_ptr(), M, F, dgate.data_ptr(), _ld(dgate), dup.data_ptr(), _ld(dup),
-                                          _stream(dev)), "aq_silu_mul_backward")
+    dgate = torch.empty((M, F), dtype=_BF16, device=dev) if dgate is None else dgate
+    dup = torch.empty((M, F), dtype=_BF16, device=dev) if dup is None else dup
+    ldg, ldu = _rows(dgate, "dgate", (_BF16,), dev, M, F), _rows(dup, "dup", (_BF16,), dev, M, F)
+    _call(lib().aq_silu_mul_backward, "aq_silu_mul_backward", dev, dh.data_ptr(), ldd, gq.data_ptr(), gs.data_ptr(),
+          uq.data_ptr(), us.data_ptr(), M, F, dgate.data_ptr(), ldg, dup.data_ptr(), ldu)
     return dgate, dup
 
 
@@ -828,43 +839,44 @@ def aq_linear_backward_workspace_bytes(M: int, w: PackedWeights) -> int:
 def _backward_workspace(M: int, w: PackedWeights) -> torch.Tensor:
     """A zero-filled workspace: cached per device and stream, or the call's own while
     a graph is captured (so that graphs share none)."""
-    need = aq_linear_backward_workspace_bytes(M, w)
+    sizes = w.__dict__.setdefault("backward_ws_bytes", {})
+    need = sizes.get(M)
+    if need is None:
+        need = sizes[M] = aq_linear_backward_workspace_bytes(M, w)
     if need == 0:
         raise ValueError("invalid arguments for a workspace")
-    with torch.cuda.device(w.device):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(need, dtype=torch.uint8, device=w.device)
-        key = (w.device, "backward", _stream(w.device))
-        ws = _ws_cache.get(key)
-        if ws is None or ws.numel() < need:
-            ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=w.device)
-        return ws
+    key = (w.device, "backward", _raw_stream(w.device.index))
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(need, dtype=torch.uint8, device=w.device)
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=w.device)
+    return ws
 
 
 def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = None, out: torch.Tensor = None,
                        out_dtype=torch.bfloat16, ws: torch.Tensor = None) -> torch.Tensor:
     """Input gradient of a packed projection: dx = add + dy W (W dequantized), dy bf16
     [M][N] -> [M][K] in add's dtype (out_dtype without add).  out may be add."""
-    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
-        raise TypeError("dy must be a 2-D torch.bfloat16 tensor")
-    M, dev = dy.shape[0], w.device
-    _rows(dy, "dy", (torch.bfloat16,), dev, M, w.N)
-    dtypes = (torch.float32, torch.bfloat16)
+    M, _, _ = _matrix(dy, "dy")
+    dev, K = w.device, w.K
+    ldd = _rows(dy, "dy", (_BF16,), dev, M, w.N)
+    ldadd = 0
     if add is not None:
-        _rows(add, "add", dtypes, dev, M, w.K)
-        out_dtype = add.dtype
+        ldadd, out_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if out is None:
-        out = torch.empty((M, w.K), dtype=out_dtype, device=dev)
-    _rows(out, "out", dtypes if add is None else (add.dtype,), dev, M, w.K)
-    if ws is None:
+        out = torch.empty((M, K), dtype=out_dtype, device=dev)
+    ldo = _rows(out, "out", (_F32, _BF16) if add is None else (out_dtype,), dev, M, K)
+    if ws is not None:
+        _need(ws, "ws", torch.uint8, dev)
+    elif torch.cuda.current_device() == dev.index:
         ws = _backward_workspace(M, w)
-    _need(ws, "ws", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        _check(lib().aq_linear_backward(ctypes.byref(w.struct), dy.data_ptr(), _ld(dy), M,
-                                        add.data_ptr() if add is not None else None,
-                                        _ld(add) if add is not None else 0, out.data_ptr(), _ld(out),
-                                        AQ_F32 if out.dtype == torch.float32 else AQ_BF16, ws.data_ptr(), ws.numel(),
-                                        _stream(dev)), "aq_linear_backward")
+    else:
+        with torch.cuda.device(dev):
+            ws = _backward_workspace(M, w)
+    _call(lib().aq_linear_backward, "aq_linear_backward", dev, ctypes.byref(w.struct), dy.data_ptr(), ldd, M,
+          None if add is None else add.data_ptr(), ldadd, out.data_ptr(), ldo,
+          AQ_F32 if out.dtype == _F32 else AQ_BF16, ws.data_ptr(), ws.numel())
     return out
 
 

@@ -9,16 +9,25 @@
 // bit: a product with R in place of the quotient.)  Backward, from the checkpoints g~ = gs gq, u~ = us uq:
 //   p = 1 / (1 + exp(-g~));  dg = dh u~ p (1 + g~ (1 - p));  du = dh g~ p.
 //
-// Both are bound by HBM: 4 bytes read and 1 (3 with checkpoints) written per
-// element forward, 4 read and 4 written backward.
+// Both are bound by HBM on paper (4 bytes read and 1, with checkpoints 3, written
+// per element forward; 4 and 4 backward), and by the instructions per element in
+// practice: at 3 codes an element, 40 instructions take as long as the bytes.
+// Hence float2 arithmetic, two multifunction operations per sigmoid, no clamps (a
+// quotient cannot pass 127 by more than its rounding), and one comparison per
+// eight codes; what that cannot decide is redone one element at a time.
 //
-// The codes are those of h, s and the quotient in fp64.  h is formed in fp32
-// first; everything that fp32 cannot decide is redone in fp64:
-//  - the row's largest |h|: every element within 2e-6 of the fp32 maximum;
+// The codes are those of h, s and the quotient in fp64.  fp32 decides all but:
+//  - the row's largest |h|: every element within 2e-6 of the fp32 maximum is redone;
 //  - a code whose fp32 quotient lies within its error bound of a half-integer.
-// fp32 error bound: expf 2 ulp, and one rounding each of 1 + e, the reciprocal,
-// two products, fp32(s), its reciprocal and the last product: 11 * 2^-24 <
-// 6.6e-7 relative; 1e-6 is used.
+// Error bounds in units of 2^-24, relative.  exp(-g) = 2^(-g L1) (1 - c g), L1 the
+// leading 16 bits of log2 e (with a bf16 g an exact product) and c = (log2 e - L1)
+// ln 2: ex2.approx 4, the dropped (c g)^2 / 2 below 2 for |g| <= 88, two roundings.
+// Then 1 + e: 1, rcp.approx 2, two products 2: h within 13.  The row's maximum
+// likewise, its product with R 2, the reciprocal 2: a quotient within 30,
+// 127 * 30 * 2^-24 < 2.3e-4.
+// Checkpoint quotients (x is exact): 127 * 3 * 2^-24 < 4e-5.
+#include <algorithm>
+
 #include "aq_internal.cuh"
 
 namespace aq {
@@ -26,48 +35,162 @@ namespace {
 
 constexpr int kGroup = 128;  // features per scale of a checkpoint: 16 threads x 8
 constexpr float kHMaxFast = 1e37f;  // rows with a larger |h| take fp64 throughout
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: see quantize8
+constexpr float kNearH = 0.5f - 2.5e-4f, kNearX = 0.5f - 4.5e-5f;
 
 __device__ __forceinline__ double gated64(float g, float u) {
   const double gd = g;
   return gd * (1.0 / (1.0 + exp(-gd))) * static_cast<double>(u);
 }
 
-// fp32 h within 6.6e-7 relative of gated64 (below -80 exp overflows towards
-// fp32's limit: there the fp64 value, rounded).
-__device__ __forceinline__ float gated32(float g, float u) {
-  if (g < -80.f) return static_cast<float>(gated64(g, u));
-  return g * __frcp_rn(1.f + expf(-g)) * u;
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = bf16_bits_to_float((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
+constexpr float kL1 = 1.44268798828125f;       // log2 e to 16 bits
+constexpr float kLc = 4.888495152129525e-06f;  // (log2 e - kL1) ln 2
+
+// exp(-g) of two bf16 values.
+__device__ __forceinline__ float2 exp_neg2(float2 g) {
+  const float2 y = __fmul2_rn(g, make_float2(-kL1, -kL1));
+  const float2 c = __ffma2_rn(g, make_float2(-kLc, -kLc), make_float2(1.f, 1.f));
+  return __fmul2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), c);
+}
+
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+// Element e of eight bf16 values, e not known to the compiler.
+__device__ __forceinline__ float pick(const uint4& v, int e) {
+  const uint32_t w = word(v, e >> 1);
+  return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
 }
 
 __device__ __forceinline__ double scale64(double amax) { return fmax(amax * (1.0 / 127.0), 1e-12); }
 
-// Codes and scale of one 128-feature group held by 16 neighbouring lanes.
-__device__ __forceinline__ void checkpoint8(const uint4& v, bool in, int8_t* q, float* s, size_t qi, size_t si) {
-  float amax = in ? abs_max8(v, 0.f) : 0.f;
+__device__ __forceinline__ int code64(double x, double s) {
+  return static_cast<int>(fmin(fmax(rint(x / s), -127.0), 127.0));
+}
+
+// clamp(rint(fl64(x / s))) of a bf16 x whose quotient t (fp32) is all but a
+// half-integer b, without the division: with r = b s - |x| (one rounding, so its
+// sign is right), the quotient rounds to b itself, and then to even, when |r| is
+// within half a unit of b times s (half of that below a power of two: b = 1/2).
+// Equal to the division for every pair of bf16 mantissas (checked).
+__device__ __forceinline__ int tie_code(float x, float t, double s) {
+  const float k = floorf(fabsf(t)), bf = k + 0.5f;
+  const double r = fma(static_cast<double>(bf), s, -static_cast<double>(fabsf(x)));
+  const int e = (__float_as_int(bf) >> 23) - 127;  // half a unit of b: 2^(e - 53)
+  const double half = s * __hiloint2double((e - 53 + 1023) << 20, 0);
+  const int ki = static_cast<int>(k);
+  int c = ki + (ki & 1);
+  if (r > (bf == 0.5f ? 0.5 * half : half)) c = ki;
+  if (-r > half) c = ki + 1;
+  return x < 0.f ? -c : c;
+}
+
+// Codes of eight values; bit e of the result: element e is too near a half-integer.
+// `limit`: 0.5 less the quotients' error bound.
+__device__ __forceinline__ uint32_t codes8(const float2 (&x)[4], float r32, float limit, uint2& out) {
+  const float2 r2 = make_float2(r32, r32), round2 = make_float2(kRound, kRound), back2 = make_float2(-kRound, -kRound);
+  uint32_t c[8];
+  float2 d[4];
+  float far = 0.f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const double sd = scale64(amax);
+  for (int i = 0; i < 4; ++i) {
+    const float2 r = __ffma2_rn(x[i], r2, round2);
+    const float2 k = __fadd2_rn(r, back2);
+    d[i] = __ffma2_rn(x[i], r2, make_float2(-k.x, -k.y));
+    far = fmaxf(far, fmaxf(fabsf(d[i].x), fabsf(d[i].y)));
+    c[2 * i] = __float_as_uint(r.x);
+    c[2 * i + 1] = __float_as_uint(r.y);
+  }
+  out = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                   __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+  uint32_t slow = 0;
+  if (!(far <= limit)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      slow |= (fabsf(d[i].x) <= limit ? 0u : 1u << (2 * i)) | (fabsf(d[i].y) <= limit ? 0u : 2u << (2 * i));
+  }
+  return slow;
+}
+
+__device__ __forceinline__ void put_code(uint2& out, int e, int code) {
+  const uint32_t sel = 0x3210u ^ ((4u ^ (e & 3)) << (4 * (e & 3)));  // byte e & 3 from the second operand
+  if (e < 4) out.x = __byte_perm(out.x, code, sel);
+  else out.y = __byte_perm(out.y, code, sel);
+}
+
+// Scale of a checkpoint group: fp32 of max(amax R, 1e-12) in fp64.  R1 has 16
+// bits, so with a bf16 amax both products are exact and the sum is rounded once
+// (checked against the fp64 form for every bf16 amax).
+__device__ __forceinline__ float scale32(float amax) {
+  constexpr float kR1 = 0x1.0204p-7f, kR2 = 0x1.020408p-28f;
+  return fmaxf(fmaf(amax, kR2, amax * kR1), 1e-12f);
+}
+
+// Checkpoints of g and u: codes and scales of one 128-feature group of each,
+// held by 16 neighbouring lanes.
+__device__ __forceinline__ void checkpoint8(const uint4& gv, const uint4& uv, const float2 (&g)[4],
+                                            const float2 (&u)[4], bool in, int8_t* gq, float* gs, int8_t* uq, float* us,
+                                            size_t qi, size_t si) {
+  // |bf16| patterns order as integers: both maxima in the halves of one word
+  const uint32_t a = __vmaxu2(__vmaxu2(gv.x & 0x7FFF7FFFu, gv.y & 0x7FFF7FFFu),
+                              __vmaxu2(gv.z & 0x7FFF7FFFu, gv.w & 0x7FFF7FFFu));
+  const uint32_t b = __vmaxu2(__vmaxu2(uv.x & 0x7FFF7FFFu, uv.y & 0x7FFF7FFFu),
+                              __vmaxu2(uv.z & 0x7FFF7FFFu, uv.w & 0x7FFF7FFFu));
+  uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ga = __uint_as_float(m << 16), ua = __uint_as_float(m & 0xFFFF0000u);
+  const float sg = scale32(ga), su = scale32(ua);
+  uint2 cg, cu;
+  const float rg = rcp_approx(sg), ru = rcp_approx(su);
+  uint32_t slow = codes8(g, rg, kNearX, cg) | (codes8(u, ru, kNearX, cu) << 8);
+  if (!in) slow = 0;
+  // ties are common (0.3% of the elements: ratios of 8-bit mantissas times 127);
+  // one element per lane and round
+  while (__any_sync(0xffffffffu, slow != 0)) {
+    if (slow) {
+      const int i = __ffs(slow) - 1, e = i & 7;
+      slow &= slow - 1;
+      const float x = pick(i < 8 ? gv : uv, e);
+      const int code = tie_code(x, x * (i < 8 ? rg : ru), scale64(i < 8 ? ga : ua));
+      if (i < 8) put_code(cg, e, code);
+      else put_code(cu, e, code);
+    }
+  }
   if (in) {
-    *reinterpret_cast<uint2*>(q + qi) = quantize8(v, sd, act_recip(sd));
-    if ((threadIdx.x & 15) == 0) s[si] = static_cast<float>(sd);
+    *reinterpret_cast<uint2*>(gq + qi) = cg;
+    *reinterpret_cast<uint2*>(uq + qi) = cu;
+    if ((threadIdx.x & 15) == 0) {
+      gs[si] = sg;
+      us[si] = su;
+    }
   }
 }
 
-// One CTA per row; a thread holds CV vectors of 8 h values in registers.
-template <int CV, int THREADS, bool KEEP>
-__global__ void __launch_bounds__(THREADS)
+// One CTA per row; a thread holds CV vectors of 8 h values in registers.  The
+// block is as wide as the row needs (whole warps).
+template <int CV, int MAXT, int MINB, bool KEEP>
+__global__ void __launch_bounds__(MAXT, MINB)
     silu_mul_quant_kernel(const uint16_t* __restrict__ gate, int ldg, const uint16_t* __restrict__ up, int ldu, int F,
                           int8_t* __restrict__ hq, float* __restrict__ sh, int8_t* __restrict__ gq,
                           float* __restrict__ gs, int8_t* __restrict__ uq, float* __restrict__ us) {
-  __shared__ float red[THREADS / 32];
+  __shared__ float red[MAXT / 32];
   __shared__ unsigned long long top;  // bits of the row's largest fp64 |h| (non-negative doubles order as integers)
-  const int m = blockIdx.x;
+  const int m = blockIdx.x, threads = blockDim.x;
   const uint4* grow = reinterpret_cast<const uint4*>(gate + (size_t)m * ldg);
   const uint4* urow = reinterpret_cast<const uint4*>(up + (size_t)m * ldu);
   const int nvec = F / 8, groups = (F + kGroup - 1) / kGroup;
@@ -75,172 +198,188 @@ __global__ void __launch_bounds__(THREADS)
   pdl_launch_dependents();
   pdl_wait();
 
-  float h[CV][8];
+  // all loads first: the checkpoints' rounds below would keep later ones waiting
+  uint4 gl[CV], ul[CV];
+#pragma unroll
+  for (int i = 0; i < CV; ++i) {
+    const int v = threadIdx.x + i * threads;
+    gl[i] = v < nvec ? __ldg(grow + v) : make_uint4(0, 0, 0, 0);
+    ul[i] = v < nvec ? __ldg(urow + v) : make_uint4(0, 0, 0, 0);
+  }
+  float2 h[CV][4];
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < CV; ++i) {
-    const int v = threadIdx.x + i * THREADS;
+    const int v = threadIdx.x + i * threads;
     const bool in = v < nvec;
-    const uint4 gv = in ? __ldg(grow + v) : make_uint4(0, 0, 0, 0);
-    const uint4 uv = in ? __ldg(urow + v) : make_uint4(0, 0, 0, 0);
-    float g[8], u[8];
-    unpack8(gv, g);
-    unpack8(uv, u);
+    const uint4 gv = gl[i], uv = ul[i];
+    const float2 g[4] = {widen2(gv.x), widen2(gv.y), widen2(gv.z), widen2(gv.w)};
+    const float2 u[4] = {widen2(uv.x), widen2(uv.y), widen2(uv.z), widen2(uv.w)};
+    float low = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[i][e] = gated32(g[e], u[e]);
-      amax = fmaxf(amax, fabsf(h[i][e]));
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = __fadd2_rn(exp_neg2(g[e]), make_float2(1.f, 1.f));
+      h[i][e] = __fmul2_rn(__fmul2_rn(g[e], make_float2(rcp_approx(x.x), rcp_approx(x.y))), u[e]);
+      low = fminf(low, fminf(g[e].x, g[e].y));
     }
-    if (KEEP) {
-      checkpoint8(gv, in, gq, gs, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
-      checkpoint8(uv, in, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
+    if (low < -80.f) {  // exp leaves fp32's range: the fp64 value, rounded
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (g[e].x < -80.f) h[i][e].x = static_cast<float>(gated64(g[e].x, u[e].x));
+        if (g[e].y < -80.f) h[i][e].y = static_cast<float>(gated64(g[e].y, u[e].y));
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(h[i][e].x), fabsf(h[i][e].y)));
+    if (KEEP)
+      checkpoint8(gv, uv, g, u, in, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
   __syncthreads();
   amax = red[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 32; ++w) amax = fmaxf(amax, red[w]);
+  for (int w = 1; w < threads / 32; ++w) amax = fmaxf(amax, red[w]);
   const bool wide = !(amax < kHMaxFast);
 
   // the exact maximum: redo every element that may be it (none where the scale
   // is at its floor: 1e-11 / 127 < 1e-12)
   const float near = wide ? 0.f : amax * (1.f - 2e-6f);
-  const bool floored = amax <= 1e-11f;
-  double best = 0.0;
+  if (amax > 1e-11f || wide) {
+    double best = 0.0;
+#pragma unroll
+    for (int i = 0; i < CV; ++i) {
+      const int v = threadIdx.x + i * threads;
+      float big = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(h[i][e].x), fabsf(h[i][e].y)));
+      if (v < nvec && !(big < near)) {
+        const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v);
+        for (int e = 0; e < 8; ++e) {
+          const float2 p = e < 4 ? (e < 2 ? h[i][0] : h[i][1]) : (e < 6 ? h[i][2] : h[i][3]);
+          if (!(fabsf(e & 1 ? p.y : p.x) < near)) best = fmax(best, fabs(gated64(pick(gv, e), pick(uv, e))));
+        }
+      }
+    }
+    if (best > 0.0) atomicMax(&top, static_cast<unsigned long long>(__double_as_longlong(best)));
+  }
+
+  // codes by the fp32 scale; undecided ones are noted
+  const float r32 = rcp_approx(fmaxf(amax * (1.f / 127.f), 1e-12f));
+  uint32_t undecided[(CV + 3) / 4];
+#pragma unroll
+  for (int i = 0; i < (CV + 3) / 4; ++i) undecided[i] = 0;
 #pragma unroll
   for (int i = 0; i < CV; ++i) {
-    const int v = threadIdx.x + i * THREADS;
-    bool any = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) any = any || !(fabsf(h[i][e]) < near);
-    if (v < nvec && any && !floored) {
-      float g[8], u[8];
-      unpack8(__ldg(grow + v), g);
-      unpack8(__ldg(urow + v), u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!(fabsf(h[i][e]) < near)) best = fmax(best, fabs(gated64(g[e], u[e])));
+    const int v = threadIdx.x + i * threads;
+    if (v < nvec) {
+      uint2 c;
+      const uint32_t slow = codes8(h[i], r32, kNearH, c);
+      undecided[i / 4] |= (wide ? 0xFFu : slow) << (8 * (i & 3));
+      reinterpret_cast<uint2*>(hq + (size_t)m * F)[v] = c;
     }
   }
-  if (best > 0.0) atomicMax(&top, static_cast<unsigned long long>(__double_as_longlong(best)));
   __syncthreads();
-  const double amax64 = __longlong_as_double(static_cast<long long>(top));
-  const double s = scale64(amax64);
-  const float r32 = act_recip(s);
+  const double s = scale64(__longlong_as_double(static_cast<long long>(top)));
   if (threadIdx.x == 0) sh[m] = static_cast<float>(s);
-
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: see quantize8
 #pragma unroll
-  for (int i = 0; i < CV; ++i) {
-    const int v = threadIdx.x + i * THREADS;
-    if (v >= nvec) continue;
-    uint32_t c[8];
-    uint32_t slow = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = h[i][e] * r32;
-      const float r = __fadd_rn(fminf(fmaxf(t, -127.f), 127.f), kRound);
-      const float k = __fsub_rn(r, kRound);
-      slow |= (0.5f - fabsf(t - k) > 1.0e-6f * fabsf(t) ? 0u : 1u) << e;
-      c[e] = __float_as_uint(r);
+  for (int j = 0; j < (CV + 3) / 4; ++j)
+    for (uint32_t w = undecided[j]; w; w &= w - 1) {
+      const int i = __ffs(w) - 1;
+      const size_t f = (size_t)(threadIdx.x + (4 * j + (i >> 3)) * threads) * 8 + (i & 7);
+      const float g = bf16_bits_to_float(__ldg(gate + (size_t)m * ldg + f)), u = bf16_bits_to_float(__ldg(up + (size_t)m * ldu + f));
+      hq[(size_t)m * F + f] = static_cast<int8_t>(code64(gated64(g, u), s));
     }
-    if (wide) slow = 0xFFu;
-    if (slow) {
-      float g[8], u[8];
-      unpack8(__ldg(grow + v), g);
-      unpack8(__ldg(urow + v), u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((slow >> e) & 1u)
-          c[e] = static_cast<uint32_t>(static_cast<int>(fmin(fmax(rint(gated64(g[e], u[e]) / s), -127.0), 127.0)));
-    }
-    const uint32_t l0 = __byte_perm(c[0], c[1], 0x0040), h0 = __byte_perm(c[2], c[3], 0x0040);
-    const uint32_t l1 = __byte_perm(c[4], c[5], 0x0040), h1 = __byte_perm(c[6], c[7], 0x0040);
-    reinterpret_cast<uint2*>(hq + (size_t)m * F)[v] =
-        make_uint2(__byte_perm(l0, h0, 0x5410), __byte_perm(l1, h1, 0x5410));
-  }
 }
 
-// 16 features per thread.
-constexpr int kBwdThreads = 256;
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-__global__ void __launch_bounds__(kBwdThreads)
+// Two codes (bytes 2i, 2i + 1 of x, offset by 128) times their scale.
+template <int I>
+__device__ __forceinline__ float2 restore2(uint32_t x, float2 s) {
+  constexpr uint32_t sel = 0x7440u | (I ? 0x2u : 0u);
+  const float2 p = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, sel)),
+                               __uint_as_float(__byte_perm(x, 0x4B000000u, sel + 1)));
+  return __fmul2_rn(__fadd2_rn(p, make_float2(-8388736.f, -8388736.f)), s);
+}
+
+// Gradients of two elements.  x = exp(-|g|), so that p and 1 - p keep their bits
+// wherever g lies (formed 2^24 too large, since ex2.approx flushes subnormals);
+// its relative error, |g| 2^-24 and a few units, is far below bf16's rounding.
+__device__ __forceinline__ void back2(float2 g, float2 u, float2 d, float2& dg, float2& du) {
+  constexpr float kL = 1.4426950408889634f;
+  const float2 one = make_float2(1.f, 1.f);
+  float2 x = make_float2(ex2_approx(fmaf(fabsf(g.x), -kL, 24.f)), ex2_approx(fmaf(fabsf(g.y), -kL, 24.f)));
+  x = __fmul2_rn(x, make_float2(0x1p-24f, 0x1p-24f));
+  const float2 y = __fadd2_rn(x, one);
+  const float2 r = make_float2(rcp_approx(y.x), rcp_approx(y.y));
+  const float2 xr = __fmul2_rn(x, r);
+  const float2 p = make_float2(g.x < 0.f ? xr.x : r.x, g.y < 0.f ? xr.y : r.y);
+  const float2 np = make_float2(g.x < 0.f ? r.x : xr.x, g.y < 0.f ? r.y : xr.y);
+  dg = __fmul2_rn(d, __fmul2_rn(u, __fmul2_rn(p, __ffma2_rn(g, np, one))));
+  du = __fmul2_rn(d, __fmul2_rn(g, p));
+}
+
+// One CTA per row, 16 features per thread and round.
+__global__ void __launch_bounds__(256)
     silu_mul_backward_kernel(const uint16_t* __restrict__ dh, int ldd, const int8_t* __restrict__ gq,
                              const float* __restrict__ gs, const int8_t* __restrict__ uq, const float* __restrict__ us,
-                             int M, int F, uint16_t* __restrict__ dgate, int ldg, uint16_t* __restrict__ dup,
-                             int ldu) {
-  const int nv = F / 16, groups = (F + kGroup - 1) / kGroup;
+                             int F, uint16_t* __restrict__ dgate, int ldg, uint16_t* __restrict__ dup, int ldu) {
+  const int m = blockIdx.x, nv = F / 16, groups = (F + kGroup - 1) / kGroup;
+  const uint4* grow = reinterpret_cast<const uint4*>(gq + (size_t)m * F);
+  const uint4* urow = reinterpret_cast<const uint4*>(uq + (size_t)m * F);
+  const uint4* drow = reinterpret_cast<const uint4*>(dh + (size_t)m * ldd);
+  uint4* go = reinterpret_cast<uint4*>(dgate + (size_t)m * ldg);
+  uint4* uo = reinterpret_cast<uint4*>(dup + (size_t)m * ldu);
   pdl_launch_dependents();
   pdl_wait();
-  const long long total = (long long)M * nv;
-  for (long long i = (long long)blockIdx.x * kBwdThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kBwdThreads) {
-    const int m = (int)(i / nv), v = (int)(i - (long long)m * nv);
-    const uint4 gv = __ldg(reinterpret_cast<const uint4*>(gq + (size_t)m * F) + v);
-    const uint4 uv = __ldg(reinterpret_cast<const uint4*>(uq + (size_t)m * F) + v);
-    const uint4* drow = reinterpret_cast<const uint4*>(dh + (size_t)m * ldd) + 2 * v;
-    const uint4 d0 = __ldg(drow), d1 = __ldg(drow + 1);
+#pragma unroll 2
+  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+    const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v), d0 = __ldg(drow + 2 * v), d1 = __ldg(drow + 2 * v + 1);
     const float sg = __ldg(gs + (size_t)m * groups + v / 8), su = __ldg(us + (size_t)m * groups + v / 8);
-    float d[16];
-    {
-      float a[8], b[8];
-      unpack8(d0, a);
-      unpack8(d1, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] = a[e];
-        d[8 + e] = b[e];
-      }
-    }
-    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
+    const float2 sg2 = make_float2(sg, sg), su2 = make_float2(su, su);
     uint32_t og[8], ou[8];
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      float rg[2], ru[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int b = e + k;
-        const float g = sg * static_cast<float>(static_cast<int8_t>(gw[b >> 2] >> (8 * (b & 3))));
-        const float u = su * static_cast<float>(static_cast<int8_t>(uw[b >> 2] >> (8 * (b & 3))));
-        // from exp(-|g|) both p and 1 - p keep their bits wherever g lies
-        const float x = expf(-fabsf(g)), r = __frcp_rn(1.f + x), xr = x * r;
-        const float p = g < 0.f ? xr : r, np = g < 0.f ? r : xr;
-        rg[k] = d[b] * (u * (p * fmaf(g, np, 1.f)));
-        ru[k] = d[b] * (g * p);
-      }
-      og[e / 2] = pack_bf16(rg[0], rg[1]);
-      ou[e / 2] = pack_bf16(ru[0], ru[1]);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t gw = word(gv, i) ^ 0x80808080u, uw = word(uv, i) ^ 0x80808080u;
+      const uint32_t da = word(i < 2 ? d0 : d1, 2 * (i & 1)), db = word(i < 2 ? d0 : d1, 2 * (i & 1) + 1);
+      float2 dg, du;
+      back2(restore2<0>(gw, sg2), restore2<0>(uw, su2), widen2(da), dg, du);
+      og[2 * i] = pack2(dg);
+      ou[2 * i] = pack2(du);
+      back2(restore2<1>(gw, sg2), restore2<1>(uw, su2), widen2(db), dg, du);
+      og[2 * i + 1] = pack2(dg);
+      ou[2 * i + 1] = pack2(du);
     }
-    uint4* go = reinterpret_cast<uint4*>(dgate + (size_t)m * ldg) + 2 * v;
-    uint4* uo = reinterpret_cast<uint4*>(dup + (size_t)m * ldu) + 2 * v;
-    go[0] = make_uint4(og[0], og[1], og[2], og[3]);
-    go[1] = make_uint4(og[4], og[5], og[6], og[7]);
-    uo[0] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-    uo[1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
+    go[2 * v] = make_uint4(og[0], og[1], og[2], og[3]);
+    go[2 * v + 1] = make_uint4(og[4], og[5], og[6], og[7]);
+    uo[2 * v] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    uo[2 * v + 1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
   }
+}
+
+template <int CV, int MAXT, int MINB, bool KEEP>
+cudaError_t launch_row(const uint16_t* gate, int ldg, const uint16_t* up, int ldu, int M, int F, int8_t* hq, float* sh,
+                       int8_t* gq, float* gs, int8_t* uq, float* us, cudaStream_t st) {
+  const int per = (F / 8 + CV - 1) / CV, threads = std::max(32, (per + 31) / 32 * 32);
+  return launch_pdl(silu_mul_quant_kernel<CV, MAXT, MINB, KEEP>, dim3(M), dim3(threads), 0, st, gate, ldg, up, ldu, F,
+                    hq, sh, gq, gs, uq, us);
 }
 
 template <bool KEEP>
 cudaError_t launch_fwd(const uint16_t* gate, int ldg, const uint16_t* up, int ldu, int M, int F, int8_t* hq, float* sh,
                        int8_t* gq, float* gs, int8_t* uq, float* us, cudaStream_t st) {
   const int nvec = F / 8;
-#define AQ_GATED(CV, T)                                                                                            \
-  return launch_pdl(silu_mul_quant_kernel<CV, T, KEEP>, dim3(M), dim3(T), 0, st, gate, ldg, up, ldu, F, hq, sh, gq, \
-                    gs, uq, us)
-  if (nvec <= 256) AQ_GATED(1, 256);
-  if (nvec <= 512) AQ_GATED(2, 256);
-  if (nvec <= 1024) AQ_GATED(4, 256);
-  if (nvec <= 2048) AQ_GATED(4, 512);
-  if (nvec <= 4096) AQ_GATED(4, 1024);
-  AQ_GATED(8, 1024);
+#define AQ_GATED(CV, T, B) return launch_row<CV, T, B, KEEP>(gate, ldg, up, ldu, M, F, hq, sh, gq, gs, uq, us, st)
+  if (nvec <= 256) AQ_GATED(1, 256, 4);
+  if (M <= num_sms() && nvec <= 2048) AQ_GATED(2, 1024, 1);  // a row per SM: the shortest chain per thread
+  if (nvec <= 512) AQ_GATED(2, 256, 4);
+  if (nvec <= 1792) AQ_GATED(4, 448, 2);
+  if (nvec <= 4096) AQ_GATED(8, 512, 1);
+  AQ_GATED(8, 1024, 1);
 #undef AQ_GATED
 }
 
@@ -274,10 +413,10 @@ extern "C" int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* g
   if (ldd < F || ldg < F || ldu < F || ldd % 8 || ldg % 8 || ldu % 8) return AQ_ERR_ARG;
   if (((uintptr_t)dh | (uintptr_t)gq | (uintptr_t)uq | (uintptr_t)dgate | (uintptr_t)dup) & 15) return AQ_ERR_ARG;
   if (((uintptr_t)gs | (uintptr_t)us) & 3) return AQ_ERR_ARG;
-  const long long blocks = ((long long)M * (F / 16) + kBwdThreads - 1) / kBwdThreads;
-  const int grid = (int)(blocks < 65535ll * 16 ? blocks : 65535ll * 16);
-  return launch_pdl(silu_mul_backward_kernel, dim3(grid), dim3(kBwdThreads), 0, static_cast<cudaStream_t>(stream), dh,
-                    ldd, gq, gs, uq, us, M, F, dgate, ldg, dup, ldu) == cudaSuccess
+  // whole warps, up to four rounds a thread
+  const int nv = F / 16, rounds = (nv + 255) / 256, threads = ((nv + rounds - 1) / rounds + 31) / 32 * 32;
+  return launch_pdl(silu_mul_backward_kernel, dim3(M), dim3(threads), 0, static_cast<cudaStream_t>(stream), dh, ldd, gq,
+                    gs, uq, us, F, dgate, ldg, dup, ldu) == cudaSuccess
              ? AQ_OK
              : AQ_ERR_CUDA;
 }

@@ -30,7 +30,9 @@
 // the workspace are not touched before.
 //
 // Few units (short sequences): the range of n is split, partial sums go to the
-// workspace, and the CTA that finishes a unit last adds them in split order.
+// workspace, and a second launch adds them in split order.  (Summed by the unit's
+// last CTA instead, 77 x 2560 x 1088 took 60 us: one CTA's loads wait for one
+// another, a grid's do not.)
 // Every wait is bounded, as in tc_linear_kernel.
 #include <algorithm>
 #include <cstring>
@@ -63,7 +65,7 @@ struct BwdShape {
       (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
   static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
   static_assert(kStages >= 3 && kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
-  static_assert((2 * kRawSlots + 3 * kStages + 4 + 2) * 8 + kRawSlots * 4 + 4 * 4 <= kCtrl, "control area");
+  static_assert((2 * kRawSlots + 3 * kStages + 4 + 1) * 8 + kRawSlots * 4 + 3 * 4 <= kCtrl, "control area");
 };
 
 struct BwdMaps {
@@ -81,8 +83,6 @@ struct BwdArgs {
   int ldadd, lddx, f32;
   void* ws;
   float* partial;  // [S][M][K]
-  int* counters;   // [C * ntb]
-  int ws_clear;
 };
 
 struct BwdUnit {
@@ -172,13 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = b_full + S_;              // the stage's MMAs are complete
   uint64_t* acc_full = done + S_;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* epi_sync = acc_empty + 2;
-  uint64_t* drain = epi_sync + 1;
+  uint64_t* drain = acc_empty + 2;
   volatile uint32_t* raw_int4 = reinterpret_cast<volatile uint32_t*>(drain + 1);
   uint32_t* tmem_slot = const_cast<uint32_t*>(raw_int4 + kRawSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = abort_flag + 1;
-  volatile int* never_flag = abort_flag + 2;
+  volatile int* never_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -195,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kEpiWarps);
     }
-    mbar_init(epi_sync, 32 * kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *never_flag = 0;
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto fail = [&](int info) {
     *abort_flag = 1;
-    record_error(a.ws, AQ_ERR_TIMEOUT, info, a.ws_clear);
+    record_error(a.ws, AQ_ERR_TIMEOUT, info, 0);
   };
 
   if (warp == 0) {
@@ -382,9 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;
     const size_t kcol = 32 * quad + lane;
     pdl_wait();
-    uint32_t sync_phase = 0;
     int ui = 0;
-    bool ok = true;
     auto put = [&](int m, size_t k, float v) {
       if (a.f32) {
         if (a.add) v += static_cast<const float*>(a.add)[(size_t)m * a.ldadd + k];
@@ -394,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         static_cast<__nv_bfloat16*>(a.dx)[(size_t)m * a.lddx + k] = __float2bfloat16_rn(v);
       }
     };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++ui) {
+    for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++ui) {
       const BwdUnit x = bwd_unit(a, u);
       const int buf = ui & 1, m0 = x.tb * NT;
       const size_t k = (size_t)x.kb * kTileK + kcol;
@@ -422,33 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
-      if (a.S == 1) continue;
-      // the CTA that comes last adds the splits in increasing order
-      __threadfence();
-      mbar_arrive(epi_sync);
-      if (!__all_sync(0xffffffffu, mbar_wait(epi_sync, sync_phase, abort_flag))) {
-        fail(7);
-        break;
-      }
-      sync_phase ^= 1;
-      int* counter = a.counters + x.kb * a.ntb + x.tb;
-      if (quad == 0 && lane == 0) *last_flag = atomicAdd(counter, 1) == a.S - 1;
-      mbar_arrive(epi_sync);
-      if (!__all_sync(0xffffffffu, mbar_wait(epi_sync, sync_phase, abort_flag))) {
-        fail(8);
-        break;
-      }
-      sync_phase ^= 1;
-      if (*last_flag) {
-        __threadfence();
-        const int m1 = min(m0 + NT, a.M);
-        for (int m = m0; m < m1; ++m) {
-          float v = 0.f;
-          for (int s = 0; s < a.S; ++s) v += __ldcg(a.partial + ((size_t)s * a.M + m) * a.K + k);
-          put(m, k, v);
-        }
-        if (quad == 0 && lane == 0) *counter = 0;
-      }
     }
   }
 
@@ -457,6 +425,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, Sh::kTmemCols);
+  }
+}
+
+// dx = add + the partial sums, splits in increasing order; four columns a thread.
+__global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs a) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = a.K / 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (i >= a.M * per) return;
+  const int m = (int)(i / per), k = (int)(i - m * per) * 4;
+  const float4* p = reinterpret_cast<const float4*>(a.partial + (size_t)m * a.K + k);
+  const size_t step = (size_t)a.M * a.K / 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < a.S; ++s) {
+    const float4 w = __ldcg(p + s * step);
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  if (a.f32) {
+    if (a.add) {
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + (size_t)m * a.ldadd + k);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + (size_t)m * a.lddx + k) = v;
+  } else {
+    if (a.add) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.add) + (size_t)m * a.ldadd + k);
+      v.x += bf16_bits_to_float(w.x & 0xFFFFu);
+      v.y += bf16_bits_to_float(w.x >> 16);
+      v.z += bf16_bits_to_float(w.y & 0xFFFFu);
+      v.w += bf16_bits_to_float(w.y >> 16);
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dx) + (size_t)m * a.lddx + k) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
 }
 
@@ -484,8 +493,6 @@ BwdPlan plan_bwd(int M, int N, int C) {
   }
   return best;
 }
-
-size_t bwd_counter_bytes(const BwdPlan& p, int C) { return ((size_t)C * p.ntb * sizeof(int) + 255) / 256 * 256; }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -541,7 +548,7 @@ using namespace aq;
 extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) {
   if (validate_packed(w) != AQ_OK || M < 1 || M > kMaxBwdTokens) return 0;
   const BwdPlan p = plan_bwd(M, w->N, w->C);
-  return kWsHeader + bwd_counter_bytes(p, w->C) + (p.S > 1 ? (size_t)p.S * M * w->K * sizeof(float) : 0);
+  return kWsHeader + (p.S > 1 ? (size_t)p.S * M * w->K * sizeof(float) : 0);
 }
 
 extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
@@ -556,7 +563,6 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   if (!ws || ws_bytes < aq_linear_backward_workspace_bytes(M, w)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
   const BwdPlan p = plan_bwd(M, w->N, w->C);
-  const size_t counters = bwd_counter_bytes(p, w->C);
   BwdArgs a;
   memset(&a, 0, sizeof(a));
   a.bitmap = w->bitmap; a.tile_idx = w->tile_idx; a.scales = w->scales;
@@ -566,9 +572,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   a.units = w->C * p.ntb * p.S;
   a.add = add; a.dx = dx; a.ldadd = ldadd; a.lddx = lddx; a.f32 = dxdtype == AQ_F32;
   a.ws = ws;
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(ws) + kWsHeader);
-  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader + counters);
-  a.ws_clear = p.S > 1 ? (int)counters : 0;
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
   switch (p.nt) {
@@ -577,6 +581,10 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
     case 128: e = launch_bwd<128>(w, dy, ldd, a, st); break;
     case 192: e = launch_bwd<192>(w, dy, ldd, a, st); break;
     case 256: e = launch_bwd<256>(w, dy, ldd, a, st); break;
+  }
+  if (e == cudaSuccess && p.S > 1) {
+    const long long blocks = ((long long)M * (w->K / 4) + 255) / 256;
+    e = launch_pdl(linear_backward_sum_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a);
   }
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

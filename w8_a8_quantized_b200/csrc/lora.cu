@@ -741,7 +741,7 @@ using namespace aq;
 extern "C" size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward) {
   if (check_lora(ad) != AQ_OK || M < 1 || M > kMaxTokens) return 0;
   const Table ta = table_a(ad), tb = table_b(ad);
-  if (!backward) return p_bytes(M, ta);
+  if (!backward) return lora_decode_fits(ad, M) ? 16 : p_bytes(M, ta);
   return p_bytes(M, tb) + std::max(g_bytes(M, ta), g_bytes(M, tb)) + 256;
 }
 
