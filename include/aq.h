@@ -441,9 +441,9 @@ typedef struct aq_lora {
  *  out   [M][ldo], same dtype; may be y itself, otherwise must not overlap an input
  *  s     fp32 [M][max_rank] or NULL: receives S (zeros behind a token's rank), which
  *        aq_lora_backward takes
- *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned; its contents
- *        need no initialization, and calls that share it must not run concurrently
- *        (one of 16 bytes is not touched: decode batches need none)
+ *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned, zero-filled once
+ *        when allocated; calls that share it must not run concurrently (one of 16
+ *        bytes is not touched: decode batches need none)
  * Rows are 16-byte aligned: x, y, out on 16 bytes, ld % 8 == 0 (bf16) or
  * ld % 4 == 0 (fp32).  1 <= M <= 4194240.  Asynchronous.
  * Errors: AQ_ERR_ARG, AQ_ERR_SHAPE (N, K, L, R, max_rank), AQ_ERR_WORKSPACE, AQ_ERR_CUDA.
@@ -468,7 +468,8 @@ int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* 
  *  da    fp32 [R][K], dbt fp32 [R][N], 16-byte aligned, written
  *  add   [M][ldadd] of dxdtype or NULL (zero), e.g. aq_linear_backward's result
  *  dx    [M][lddx], fp32 or bf16 (dxdtype), or NULL (not wanted); may be add itself
- *  ws    >= aq_lora_workspace_bytes(ad, M, 1) bytes, as for aq_lora_apply
+ *  ws    >= aq_lora_workspace_bytes(ad, M, 1) bytes, as for aq_lora_apply; a bounded wait
+ *        that gives up is recorded there and reported by aq_workspace_status
  * Alignment, M and errors as for aq_lora_apply.
  */
 int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M, const float* s,

@@ -688,20 +688,39 @@ def aq_lora_workspace_bytes(ad: Adapters, M: int, backward: bool) -> int:
     return int(lib().aq_lora_workspace_bytes(ctypes.byref(ad.struct), M, int(bool(backward))))
 
 
+def _stream_ws(tag: str, need: int, device) -> torch.Tensor:
+    """A zero-filled workspace of the current stream, cached and grown on demand; a
+    call that is captured into a graph gets its own, so that graphs share none."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(need, dtype=torch.uint8, device=device)
+    key = (device, tag, _raw_stream(device.index))
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _own_ws(tag: str, need: int, device) -> torch.Tensor:
+    if need == 0:
+        raise ValueError("invalid arguments for a workspace")
+    if torch.cuda.current_device() == device.index:
+        return _stream_ws(tag, need, device)
+    with torch.cuda.device(device):
+        return _stream_ws(tag, need, device)
+
+
 def _lora_ws(ad: Adapters, M: int, backward: int, ws):
-    """The call's workspace: the caller's, or a fresh one from torch's allocator (it
-    needs no initialization, so nothing is shared between calls, streams or graphs)."""
+    """The call's workspace: the caller's or the stream's; none to speak of for a
+    decode batch."""
     if ws is not None:
         _need(ws, "ws", torch.uint8, ad.device)
         return ws
     need = ad.ws_bytes.get((M, backward))
     if need is None:
         need = ad.ws_bytes[M, backward] = aq_lora_workspace_bytes(ad, M, backward)
-    if need == 0:
-        raise ValueError("invalid adapters or token count")
     if need == _NO_WS:
         return ad.no_ws
-    return torch.empty(need, dtype=torch.uint8, device=ad.device)
+    return _own_ws("lora", need, ad.device)
 
 
 def _lora_ids(ad: Adapters, ids: torch.Tensor, M: int):
@@ -836,24 +855,6 @@ def aq_linear_backward_workspace_bytes(M: int, w: PackedWeights) -> int:
     return int(lib().aq_linear_backward_workspace_bytes(M, ctypes.byref(w.struct)))
 
 
-def _backward_workspace(M: int, w: PackedWeights) -> torch.Tensor:
-    """A zero-filled workspace: cached per device and stream, or the call's own while
-    a graph is captured (so that graphs share none)."""
-    sizes = w.__dict__.setdefault("backward_ws_bytes", {})
-    need = sizes.get(M)
-    if need is None:
-        need = sizes[M] = aq_linear_backward_workspace_bytes(M, w)
-    if need == 0:
-        raise ValueError("invalid arguments for a workspace")
-    key = (w.device, "backward", _raw_stream(w.device.index))
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(need, dtype=torch.uint8, device=w.device)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < need:
-        ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=w.device)
-    return ws
-
-
 def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = None, out: torch.Tensor = None,
                        out_dtype=torch.bfloat16, ws: torch.Tensor = None) -> torch.Tensor:
     """Input gradient of a packed projection: dx = add + dy W (W dequantized), dy bf16
@@ -869,11 +870,12 @@ def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = N
     ldo = _rows(out, "out", (_F32, _BF16) if add is None else (out_dtype,), dev, M, K)
     if ws is not None:
         _need(ws, "ws", torch.uint8, dev)
-    elif torch.cuda.current_device() == dev.index:
-        ws = _backward_workspace(M, w)
     else:
-        with torch.cuda.device(dev):
-            ws = _backward_workspace(M, w)
+        sizes = w.__dict__.setdefault("backward_ws_bytes", {})  # by token count: a function of the sizes alone
+        need = sizes.get(M)
+        if need is None:
+            need = sizes[M] = aq_linear_backward_workspace_bytes(M, w)
+        ws = _own_ws("backward", need, dev)
     _call(lib().aq_linear_backward, "aq_linear_backward", dev, ctypes.byref(w.struct), dy.data_ptr(), ldd, M,
           None if add is None else add.data_ptr(), ldadd, out.data_ptr(), ldo,
           AQ_F32 if out.dtype == _F32 else AQ_BF16, ws.data_ptr(), ws.numel())

@@ -38,6 +38,7 @@
 #include <cstring>
 
 #include "aq_internal.cuh"
+#include "tc_bf16.cuh"
 
 namespace aq {
 namespace {
@@ -49,7 +50,6 @@ constexpr int kXfWarp0 = 4, kXfWarps = 8, kXfThreads = 32 * kXfWarps;
 constexpr int kEpiWarp0 = kXfWarp0 + kXfWarps, kEpiWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kMaxBwdSplits = 16;
-constexpr unsigned long long kGraceNs = 200000;
 
 template <int NT>
 struct BwdShape {
@@ -60,9 +60,7 @@ struct BwdShape {
   static constexpr int kTmemCols = 2 * NT <= 32 ? 32 : 2 * NT <= 64 ? 64 : 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
   static constexpr int kCtrl = 512;
   static constexpr int kSmem = 1024 + kStages * kStage + kRawSlots * kRawBytes + kCtrl;
-  // D fp32; A, B bf16; A MN-major, B K-major
-  static constexpr uint32_t kIdesc =
-      (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+  static constexpr uint32_t kIdesc = idesc_bf16(NT, true, false);
   static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
   static_assert(kStages >= 3 && kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
   static_assert((2 * kRawSlots + 3 * kStages + 4 + 1) * 8 + kRawSlots * 4 + 3 * 4 <= kCtrl, "control area");
@@ -100,40 +98,6 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   return x;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, one CTA.
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Descriptor of an MN-major operand in the 128-byte swizzle: groups of 8 rows
-// (contraction) 1024 bytes apart, halves of 64 columns 64 x 128 bytes apart.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
-  d |= (uint64_t)((kStep * 128) >> 4) << 16;  // leading: the next 64 columns
-  d |= (uint64_t)(1024 >> 4) << 32;           // stride: the next 8 rows
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-struct Ring {
-  uint32_t i, ph;
-  template <int N>
-  __device__ __forceinline__ void next() {
-    if (++i == N) {
-      i = 0;
-      ph ^= 1u;
-    }
-  }
-};
-
 // Four codes (two's-complement bytes) times sw, as two bf16 pairs.
 // A byte b = q + 128 in the low mantissa bits of 2^23 is 8388608 + b exactly.
 __device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw) {
@@ -147,11 +111,6 @@ __device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw) {
   q = __fmul2_rn(__fadd2_rn(q, bias), sw);
   const __nv_bfloat162 a = __floats2bfloat162_rn(p.x, p.y), b = __floats2bfloat162_rn(q.x, q.y);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
-__device__ __forceinline__ void grace() {
-  const unsigned long long t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 < kGraceNs) __nanosleep(1000);
 }
 
 template <int NT>
@@ -272,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0))), bdesc0 = sw128_desc(smem_u32(stage_b(0)));
+      const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kStep * 128), bdesc0 = sw128_desc(smem_u32(stage_b(0)));
       Ring sr{0, 0};
       bool ok = true, any = false;
       int ui = 0;
@@ -492,32 +451,6 @@ BwdPlan plan_bwd(int M, int N, int C) {
     }
   }
   return best;
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode() {
-  static const EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeFn>(p) : nullptr;
-  }();
-  return fn;
-}
-
-bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch,
-            uint32_t box_cols, uint32_t box_rows, bool swizzle) {
-  EncodeFn fn = encode();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
-  const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
-  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NT>

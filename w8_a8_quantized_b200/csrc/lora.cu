@@ -10,7 +10,7 @@
 //             dx[m][k] = add[m][k] + sum_r T[m][r] A_l[r][k]
 //             dA_l[r][k] = sum_m T[m][r] x[m][k];  dB_l^T[r][n] = sum_m S[m][r] dy[m][n]
 // so three kernels serve both: contract a long axis to the rank (shrink),
-// the rank to a long axis (expand), and the tokens (outer).
+// the rank to a long axis (expand), and the tokens (lora_grad.cu).
 //
 // Products run on mma.sync (bf16 in, fp32 out): the tables and x, dy are bf16
 // (8-bit codes are exact in bf16), and S and T, fp32, enter as three bf16 terms
@@ -38,7 +38,6 @@ constexpr int kMaxRank = 256;  // largest rank of an adapter
 constexpr int kThreads = 256;  // 8 warps
 constexpr int kDC = 128;       // columns of a chunk of the long axis
 constexpr int kLd = kDC + 8;   // row pitch in shared memory: 17 x 16 bytes, conflict-free for ldmatrix
-constexpr int kLdR = kRank + 8;
 
 struct Table {  // one of the two tables of an adapter set
   const uint16_t* w;   // [R][D]
@@ -147,18 +146,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// v as three bf16 terms: hi + mid + lo = v to 24 bits.  A non-finite v stays in hi.
-__device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  float r = v - __bfloat162float(h);
-  if (!(fabsf(r) < 3e38f)) r = 0.f;
-  const __nv_bfloat16 m = __float2bfloat16_rn(r);
-  const __nv_bfloat16 l = __float2bfloat16_rn(r - __bfloat162float(m));
-  hi = __bfloat16_as_ushort(h);
-  mid = __bfloat16_as_ushort(m);
-  lo = __bfloat16_as_ushort(l);
 }
 
 // ---------------------------------------------------------------- shrink
@@ -488,162 +475,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const ExpandAr
   cp_wait<0>();
 }
 
-// ---------------------------------------------------------------- outer
-struct OuterArgs {
-  Table t;              // rows and ranks (the table itself is not read)
-  const int32_t* ids;
-  int M;
-  const float* p;       // [psplits][M][max_rank]
-  int psplits;
-  const void* x;        // bf16 [M][ldx], or int8 codes with sx [M]
-  const float* sx;
-  int ldx;
-  float* g;             // [splits][R][D]
-  int splits;
-};
-
-struct OuterSmem {
-  uint16_t x[kTok][kLd];
-  uint16_t t[3][kTok][kLdR];
-  int in[kTok];
-};
-
-template <bool CODES>
-__global__ void __launch_bounds__(kThreads) lora_outer_kernel(const OuterArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  OuterSmem& sm = *reinterpret_cast<OuterSmem*>(raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rblocks = (a.t.max_rank + kRank - 1) / kRank;
-  const int d0 = blockIdx.x * kDC, l = blockIdx.y / rblocks, rb0 = blockIdx.y % rblocks * kRank, split = blockIdx.z;
-  const Table& t = a.t;
-  pdl_launch_dependents();
-  pdl_wait();
-  int row0, rank;
-  rows_of(t, l, row0, rank);
-  const int nr = min(rank - rb0, kRank);
-  if (nr <= 0) return;
-  const int chunks = (a.M + kTok - 1) / kTok;
-  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
-  const int mt = (nr + 15) / 16;
-  float tot[4][2][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tot[i][j][e] = 0.f;
-  for (int c = c0; c < c1; ++c) {
-    const int m0 = c * kTok;
-    bool in = false;
-    if (tid < kTok) {
-      in = m0 + tid < a.M && __ldg(a.ids + m0 + tid) == l;
-      sm.in[tid] = in;
-    }
-    if (!__syncthreads_or(in)) continue;
-    // activations: rows of other adapters as zeros
-    if (CODES) {
-      for (int i = tid; i < kTok * (kDC / 16); i += kThreads) {
-        const int r = i / (kDC / 16), cc = i % (kDC / 16) * 16;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (sm.in[r] && d0 + cc < t.D)
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.x) + (size_t)(m0 + r) * a.ldx + d0 + cc));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int b0 = static_cast<int8_t>(w[e >> 1] >> (16 * (e & 1)));
-          const int b1 = static_cast<int8_t>(w[e >> 1] >> (16 * (e & 1) + 8));
-          const __nv_bfloat162 p = __floats2bfloat162_rn((float)b0, (float)b1);
-          o[e] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-        *reinterpret_cast<uint4*>(&sm.x[r][cc]) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(&sm.x[r][cc + 8]) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-    } else {
-      for (int i = tid; i < kTok * (kDC / 8); i += kThreads) {
-        const int r = i / (kDC / 8), cc = i % (kDC / 8) * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (sm.in[r] && d0 + cc < t.D)
-          v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (size_t)(m0 + r) * a.ldx + d0 + cc));
-        *reinterpret_cast<uint4*>(&sm.x[r][cc]) = v;
-      }
-    }
-    for (int i = tid; i < kTok * 16 * mt; i += kThreads) {
-      const int r = i / (16 * mt), cc = i % (16 * mt);
-      float v = 0.f;
-      if (sm.in[r] && cc < nr) {
-        for (int k = 0; k < a.psplits; ++k) v += __ldg(a.p + ((size_t)k * a.M + m0 + r) * t.max_rank + rb0 + cc);
-        if (CODES) v *= __ldg(a.sx + m0 + r);
-      }
-      split3(v, sm.t[0][r][cc], sm.t[1][r][cc], sm.t[2][r][cc]);
-    }
-    __syncthreads();
-    float acc[4][2][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint32_t fb[4];
-      ldsm4t(fb, &sm.x[16 * ks + (lane & 7) + 8 * ((lane >> 3) & 1)][16 * warp + 8 * (lane >> 4)]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < mt) {
-#pragma unroll
-          for (int sp = 2; sp >= 0; --sp) {
-            uint32_t fa[4];
-            ldsm4t(fa, &sm.t[sp][16 * ks + (lane & 7) + 8 * (lane >> 4)][16 * i + 8 * ((lane >> 3) & 1)]);
-            mma16816(acc[i][0], fa, fb[0], fb[1]);
-            mma16816(acc[i][1], fa, fb[2], fb[3]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tot[i][j][e] += acc[i][j][e];
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * i + (lane >> 2) + 8 * h;
-      if (r >= nr) continue;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int d = d0 + 16 * warp + 8 * j + 2 * (lane & 3);
-        if (d < t.D)
-          *reinterpret_cast<float2*>(a.g + ((size_t)split * t.R + row0 + rb0 + r) * t.D + d) =
-              make_float2(tot[i][j][2 * h], tot[i][j][2 * h + 1]);
-      }
-    }
-}
-
-// g[i] = sum of the splits' values, splits in increasing order.
-__global__ void __launch_bounds__(256) lora_sum_kernel(const float4* __restrict__ p, int splits, size_t n,
-                                                       float4* __restrict__ g) {
-  pdl_launch_dependents();
-  pdl_wait();
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-    float4 v = p[i];
-    for (int k = 1; k < splits; ++k) {
-      const float4 w = p[(size_t)k * n + i];
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
-    }
-    g[i] = v;
-  }
-}
-
 // ---------------------------------------------------------------- host side
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -659,19 +490,9 @@ int shrink_splits(int M, const Table& t) {
   return std::max(1, std::min(chunks, ceil_div(2 * num_sms(), tiles)));
 }
 
-int outer_splits(int M, const Table& t) {
-  const int tiles = ceil_div(M, kTok), blocks = ceil_div(t.D, kDC);
-  return std::max(1, std::min(std::min(tiles, 16), ceil_div(2 * num_sms(), blocks)));
-}
-
 size_t p_bytes(int M, const Table& t) {
   return align256((size_t)shrink_splits(M, t) * M * t.max_rank * sizeof(float));
 }
-size_t g_bytes(int M, const Table& t) {
-  const int s = outer_splits(M, t);
-  return s > 1 ? align256((size_t)s * t.R * t.D * sizeof(float)) : 0;
-}
-
 cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p, cudaStream_t st) {
   ShrinkArgs a{t, x, ldx, M, ids, p, shrink_splits(M, t), share(M, t)};
   cudaError_t e = ensure_smem_attr<lora_shrink_kernel>(sizeof(ShrinkSmem));
@@ -699,25 +520,6 @@ cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, in
   return dtype == AQ_F32 ? launch_expand<true>(a, st) : launch_expand<false>(a, st);
 }
 
-cudaError_t outer(const Table& t, const int32_t* ids, int M, const float* p, int psplits, const void* x,
-                  const float* sx, int ldx, float* g, float* part, cudaStream_t st) {
-  const int splits = outer_splits(M, t);
-  OuterArgs a{t, ids, M, p, psplits, x, sx, ldx, splits > 1 ? part : g, splits};
-  const dim3 grid(ceil_div(t.D, kDC), t.L * ceil_div(t.max_rank, kRank), splits);
-  cudaError_t e = sx ? ensure_smem_attr<lora_outer_kernel<true>>(sizeof(OuterSmem))
-                     : ensure_smem_attr<lora_outer_kernel<false>>(sizeof(OuterSmem));
-  if (e == cudaSuccess)
-    e = sx ? launch_pdl(lora_outer_kernel<true>, grid, dim3(kThreads), sizeof(OuterSmem), st, a)
-           : launch_pdl(lora_outer_kernel<false>, grid, dim3(kThreads), sizeof(OuterSmem), st, a);
-  if (e == cudaSuccess && splits > 1) {
-    const size_t n = (size_t)t.R * t.D / 4;
-    const int blocks = (int)std::min<size_t>((n + 255) / 256, 8 * (size_t)num_sms());
-    e = launch_pdl(lora_sum_kernel, dim3(blocks), dim3(256), 0, st, reinterpret_cast<const float4*>(part), splits, n,
-                   reinterpret_cast<float4*>(g));
-  }
-  return e;
-}
-
 int check_lora(const aq_lora* ad) {
   if (!ad || !ad->a || !ad->bt || !ad->off || !ad->scale) return AQ_ERR_ARG;
   if (ad->N < 8 || ad->K < 8 || ad->N % 8 || ad->K % 8 || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
@@ -741,8 +543,8 @@ using namespace aq;
 extern "C" size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward) {
   if (check_lora(ad) != AQ_OK || M < 1 || M > kMaxTokens) return 0;
   const Table ta = table_a(ad), tb = table_b(ad);
-  if (!backward) return lora_decode_fits(ad, M) ? 16 : p_bytes(M, ta);
-  return p_bytes(M, tb) + std::max(g_bytes(M, ta), g_bytes(M, tb)) + 256;
+  if (!backward) return lora_decode_fits(ad, M) ? 16 : kWsHeader + p_bytes(M, ta);
+  return kWsHeader + p_bytes(M, tb) + lora_grad_ws_bytes(ad, M);
 }
 
 extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
@@ -762,7 +564,7 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
     return launch_lora_decode(ad, x, ldx, ids, M, y, ldy, out, ldo, ydtype == AQ_F32, s, st) == cudaSuccess ? AQ_OK
                                                                                                             : AQ_ERR_CUDA;
   const Table ta = table_a(ad);
-  float* p = static_cast<float*>(ws);
+  float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaError_t e = shrink(ta, x, ldx, ids, M, p, st);
   if (e == cudaSuccess)
     e = expand(table_b(ad), ids, M, p, shrink_splits(M, ta), y, ldy, out, ldo, ydtype, s, st);
@@ -789,12 +591,12 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Table ta = table_a(ad), tb = table_b(ad);
-  float* p = static_cast<float*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p_bytes(M, tb));
+  float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   const int splits = shrink_splits(M, tb);
   cudaError_t e = shrink(tb, dy, ldd, ids, M, p, st);
   if (e == cudaSuccess && dx) e = expand(ta, ids, M, p, splits, add, ldadd, dx, lddx, dxdtype, nullptr, st);
-  if (e == cudaSuccess) e = outer(ta, ids, M, p, splits, x, sx, ldx, da, part, st);
-  if (e == cudaSuccess) e = outer(tb, ids, M, s, 1, dy, nullptr, ldd, dbt, part, st);
+  if (e == cudaSuccess)
+    e = launch_lora_grad(ad, ids, M, p, splits, x, ldx, sx, da, s, dy, ldd, dbt, ws,
+                         reinterpret_cast<char*>(p) + p_bytes(M, tb), st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

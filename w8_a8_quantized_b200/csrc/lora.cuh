@@ -10,4 +10,27 @@ bool lora_decode_fits(const aq_lora* ad, int M);
 cudaError_t launch_lora_decode(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
                                int ldy, void* out, int ldo, bool f32, float* s, cudaStream_t st);
 
+// Weight gradients (lora_grad.cu): t [tsplits][M][max_rank] partial sums of the
+// output's gradient times B, s [M][max_rank] the forward products.  `header`: the
+// error word of a call's workspace; `ws`: lora_grad_ws_bytes, 256-byte aligned
+// behind a workspace that starts on 16 bytes.
+size_t lora_grad_ws_bytes(const aq_lora* ad, int M);
+cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, const void* x,
+                             int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
+                             float* dbt, void* header, void* ws, cudaStream_t st);
+
+#if defined(__CUDACC__)
+// v as three bf16 terms: hi + mid + lo = v to 24 bits.  A non-finite v stays in hi.
+__device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uint16_t& lo) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  float r = v - __bfloat162float(h);
+  if (!(fabsf(r) < 3e38f)) r = 0.f;
+  const __nv_bfloat16 m = __float2bfloat16_rn(r);
+  const __nv_bfloat16 l = __float2bfloat16_rn(r - __bfloat162float(m));
+  hi = __bfloat16_as_ushort(h);
+  mid = __bfloat16_as_ushort(m);
+  lo = __bfloat16_as_ushort(l);
+}
+#endif
+
 }  // namespace aq

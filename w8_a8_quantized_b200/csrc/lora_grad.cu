@@ -1,0 +1,531 @@
+// Weight gradients of the adapters on the 5th-generation tensor cores:
+//   g_l[r][d] = sum over the tokens m of adapter l of T[m][r] x[m][d]
+// with x the activations (8-bit codes or bf16; then T holds dS, times the token
+// scale for codes) or the output's gradient (then T holds S).
+//
+// T is fp32 and enters as three bf16 terms, 24 bits, side by side along N:
+//   D[128 d][hi | mid | lo] += x[64 tokens][128 d]^T [T_hi | T_mid | T_lo][64 tokens]
+// so one pass over x serves all three; codes are exact in bf16.  Both operands are
+// MN-major, that is, as they lie in memory.  A first kernel writes the terms
+// (zeros behind a token's rank) and says of each 64 tokens whether one adapter has
+// them all.  It is bound by the bytes of x: 64 x 128 of them per step against
+// 64 x 128 x 3r multiplications.
+//
+// A CTA takes 128 columns, one adapter and a range of tokens, and skips the 64s
+// that its adapter has no part in.  Where a 64 holds other adapters' tokens too,
+// their rows are cleared in shared memory on both sides, so that nothing of them,
+// not even an infinity, reaches the sum.  Tensor memory sums 512 tokens at a time;
+// the epilogue adds those sums in fp32 registers, rounding to nearest.
+//
+// Roles: warp 0 codes (TMA), warp 1 tensor memory and MMA, warp 2 terms and bf16
+// activations (TMA), warps 4-7 codes -> bf16 and the clearing, warps 8-11 epilogue.
+// Every wait is bounded; one that gives up is recorded in the workspace.
+#include <algorithm>
+#include <cstring>
+
+#include "lora.cuh"
+#include "tc_bf16.cuh"
+
+namespace aq {
+namespace {
+
+constexpr int kTok = 64;       // tokens of a step
+constexpr int kD = 128;        // columns of a CTA
+constexpr int kThreads = 384;
+constexpr int kUnit = 8;       // steps summed in tensor memory
+constexpr int kXf = 4, kEpi = 4;  // warps
+
+// ---------------------------------------------------------------- terms
+struct TermsJob {
+  const float* p;     // [splits][M][max_rank]
+  int splits;
+  const float* sx;    // [M] or null
+  uint16_t* terms;    // [M][npad]: hi, mid, lo of `rc` ranks each
+};
+struct TermsArgs {
+  TermsJob job[2];
+  const int32_t* ids;
+  const int32_t* off;
+  int M, L, R, max_rank;
+  int rb0, rc, npad;
+  int32_t* info;      // per 64 tokens: the adapter that has them all, -1 none has any, -2 mixed
+};
+
+__global__ void __launch_bounds__(256) lora_terms_kernel(const TermsArgs a) {
+  __shared__ int rank[kTok];
+  const int tid = threadIdx.x, m0 = blockIdx.x * kTok;
+  const TermsJob& j = a.job[blockIdx.y];
+  pdl_launch_dependents();
+  pdl_wait();
+  if (tid < kTok) {
+    const int n = min(kTok, a.M - m0);
+    int v = tid < n ? __ldg(a.ids + m0 + tid) : -1, r = 0;
+    if (v < 0 || v >= a.L) v = -1;
+    if (v >= 0) {
+      const int b = min(max(__ldg(a.off + v), 0), a.R);
+      r = min(min(max(__ldg(a.off + v + 1), b), a.R) - b, a.max_rank) - a.rb0;
+    }
+    rank[tid] = r;
+    int lead = __ldg(a.ids + m0);
+    if (lead < 0 || lead >= a.L) lead = -1;
+    const bool same = __all_sync(0xffffffffu, tid >= n || v == lead);
+    const bool none = __all_sync(0xffffffffu, v < 0);
+    __shared__ int kind[2];
+    if ((tid & 31) == 0) kind[tid >> 5] = none ? 1 : same ? 2 : 0;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    if (tid == 0 && blockIdx.y == 0 && a.rb0 == 0) {
+      const bool all_same = n > 32 ? kind[0] && kind[0] == kind[1] : kind[0] != 0;
+      a.info[blockIdx.x] = !all_same ? -2 : kind[0] == 1 ? -1 : lead;
+    }
+  }
+  __syncthreads();
+  for (int t = tid >> 4; t < kTok && m0 + t < a.M; t += 16) {
+    const float scale = j.sx && rank[t] > 0 ? __ldg(j.sx + m0 + t) : 1.f;
+    for (int c = tid & 15; c < a.rc; c += 16) {
+      float v = 0.f;
+      if (c < rank[t]) {
+        const float* src = j.p + (size_t)(m0 + t) * a.max_rank + a.rb0 + c;
+        for (int k = 0; k < j.splits; ++k) v += __ldg(src + (size_t)k * a.M * a.max_rank);
+        v *= scale;
+      }
+      uint16_t* d = j.terms + (size_t)(m0 + t) * a.npad + c;
+      split3(v, d[0], d[a.rc], d[2 * a.rc]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+template <int NB, bool CODES>
+struct GradShape {
+  static constexpr int kRanks = NB / 3;
+  static constexpr int kAtoms = (NB + 63) / 64;       // 64 terms x 64 tokens, 8 KiB each
+  static constexpr int kA = kTok * kD * 2, kB = kAtoms * 8192, kStage = kA + kB;
+  // two CTAs per SM up to 32 ranks: a CTA's start and end are then covered by the other
+  static constexpr int kPerSm = NB <= 96 ? 2 : 1;
+  static constexpr int kStages = NB <= 48 ? 3 : NB <= 96 ? (CODES ? 2 : 3) : 4;
+  static constexpr int kRaw = CODES ? 3 : 0;          // ring of codes, 8 KiB each
+  static constexpr int kTmem = 2 * NB <= 128 ? 128 : 2 * NB <= 256 ? 256 : 512;
+  static constexpr int kCtrl = 512 + kThreads * 2;
+  static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kTok * kD + kCtrl;
+  static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
+  static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  static_assert(kPerSm * kTmem <= 512, "tensor memory");
+};
+
+struct GradMaps {
+  CUtensorMap x, terms;
+};
+
+struct GradArgs {
+  const int32_t* ids;
+  const int32_t* off;
+  const int32_t* info;
+  int M, D, L, R, max_rank, rb0;
+  float* g;  // [splits][R][D]
+  int splits;
+  void* ws;
+};
+
+// Eight codes (bytes) as bf16: 128 + the low seven bits, less 128 or 256 by the sign, exact.
+__device__ __forceinline__ uint4 widen_codes8(uint2 w) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = __byte_perm(i < 2 ? w.x : w.y, 0x43434343u, (i & 1) ? 0x4342 : 0x4140);
+    const uint32_t lo = h & 0xFF7FFF7Fu, hi = h & 0xFF80FF80u;
+    const __nv_bfloat162 v =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi));
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int NB, bool CODES>
+__global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
+    lora_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs a) {
+  using Sh = GradShape<NB, CODES>;
+  constexpr int S_ = Sh::kStages, RW = CODES ? Sh::kRaw : 1;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  auto stage_a = [&](int st) { return smem + st * Sh::kStage; };
+  auto stage_b = [&](int st) { return smem + st * Sh::kStage + Sh::kA; };
+  auto raw_slot = [&](int s) { return smem + S_ * Sh::kStage + s * kTok * kD; };
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S_ * Sh::kStage + Sh::kRaw * kTok * kD);
+  uint64_t* raw_empty = raw_full + RW;
+  uint64_t* a_full = raw_empty + RW;   // transform warps done with the stage
+  uint64_t* b_full = a_full + S_;      // terms (and bf16 activations) landed
+  uint64_t* done = b_full + S_;        // the stage's MMAs are complete
+  uint64_t* acc_full = done + S_;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* never_flag = abort_flag + 1;
+  volatile int* count = abort_flag + 2;  // [12] listed chunks of each warp
+  volatile uint16_t* list = reinterpret_cast<volatile uint16_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int d0 = blockIdx.x * kD, l = blockIdx.y, split = blockIdx.z;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row0 = min(max(__ldg(a.off + l), 0), a.R);
+  const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
+  if (nr <= 0) return;
+  const int chunks = (a.M + kTok - 1) / kTok;
+  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
+  // whether the 64 tokens c are this adapter's: 0 none, 1 all, 2 some
+  auto part_in = [&](int c) {
+    const int v = c < c1 ? __ldg(a.info + c) : -1;
+    int take = v == l;
+    if (v == -2)
+      for (int m = c * kTok; m < min((c + 1) * kTok, a.M); ++m)
+        if (__ldg(a.ids + m) == l) take = 2;
+    return take;
+  };
+  if (c1 - c0 <= kThreads && !__syncthreads_or(part_in(c0 + tid))) {  // nothing here: zeros
+    const int width = min(kD, a.D - d0);
+    for (int i = tid; i < nr * width; i += kThreads)
+      a.g[((size_t)split * a.R + row0 + a.rb0 + i / width) * a.D + d0 + i % width] = 0.f;
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < RW; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], kXf);
+    }
+    for (int i = 0; i < S_; ++i) {
+      mbar_init(&a_full[i], kXf);
+      mbar_init(&b_full[i], 1);
+      mbar_init(&done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpi);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.x);
+    prefetch_tmap(&maps.terms);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, Sh::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  auto fail = [&](int info) {
+    *abort_flag = 1;
+    record_error(a.ws, AQ_ERR_TIMEOUT, info, 0);
+  };
+
+  Ring sr{0, 0}, rr{0, 0}, ar{0, 0};  // stage, raw slot, accumulator
+  bool ok = true, issued = false;
+  float tot[Sh::kRanks];
+#pragma unroll
+  for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
+
+  for (int base = c0; base < c1; base += kThreads) {
+    // the 64s of this adapter among the next 384, in order; bit 15: others' tokens too
+    __syncthreads();
+    const int take = part_in(base + tid);
+    const unsigned vote = __ballot_sync(0xffffffffu, take != 0);
+    if (lane == 0) count[warp] = __popc(vote);
+    __syncthreads();
+    int at = __popc(vote & ((1u << lane) - 1)), n = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += count[w];
+      n += count[w];
+    }
+    if (take) list[at] = (uint16_t)(tid | (take == 2 ? 0x8000 : 0));
+    __syncthreads();
+
+    if (warp == 0 && CODES) {
+      // ------------------------------------------------------------ codes
+      if (lane == 0) {
+        for (int i = 0; ok && i < n; ++i) {
+          if (!mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag)) {
+            fail(21);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&raw_full[rr.i], kTok * kD);
+          tma_load_2d(raw_slot(rr.i), &maps.x, d0, (base + (list[i] & 0x7FFF)) * kTok, &raw_full[rr.i]);
+          rr.template next<RW>();
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA
+      if (lane == 0) {
+        const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kTok * 128), bdesc0 = mn_desc(smem_u32(stage_b(0)), kTok * 128);
+        for (int i = 0; ok && i < n; ++i) {
+          if (i % kUnit == 0 && !mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag)) {
+            fail(22);
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(&b_full[sr.i], sr.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
+            fail(23);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t off = (uint64_t)((sr.i * Sh::kStage) >> 4);
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of eight rows
+            mma_bf16(tmem_base + ar.i * NB, adesc0 + off + 128 * k, bdesc0 + off + 128 * k, Sh::kIdesc,
+                     i % kUnit > 0 || k > 0);
+          mma_commit(&done[sr.i]);
+          issued = true;
+          sr.template next<S_>();
+          if (i % kUnit == kUnit - 1 || i + 1 == n) {
+            mma_commit(&acc_full[ar.i]);
+            ar.template next<2>();
+          }
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ terms, bf16 activations
+      if (lane == 0) {
+        for (int i = 0; ok && i < n; ++i) {
+          if (!mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag)) {
+            fail(24);
+            ok = false;
+            break;
+          }
+          const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
+          mbar_arrive_expect_tx(&b_full[sr.i], Sh::kB + (CODES ? 0 : Sh::kA));
+#pragma unroll
+          for (int c = 0; c < Sh::kAtoms; ++c)
+            tma_load_2d(stage_b(sr.i) + c * 8192, &maps.terms, 64 * c, m0, &b_full[sr.i]);
+          if (!CODES) {
+            tma_load_2d(stage_a(sr.i), &maps.x, d0, m0, &b_full[sr.i]);
+            tma_load_2d(stage_a(sr.i) + 8192, &maps.x, d0 + 64, m0, &b_full[sr.i]);
+          }
+          sr.template next<S_>();
+        }
+      }
+    } else if (warp >= 4 && warp < 4 + kXf) {
+      // ------------------------------------------------------------ transform
+      const int t = tid - 128, c = t & 15, r0 = t >> 4;
+      for (int i = 0; ok && i < n; ++i) {
+        const bool mixed = list[i] & 0x8000;
+        const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
+        bool got = mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag);
+        if (CODES) got = got && mbar_wait(&raw_full[rr.i], rr.ph, abort_flag);
+        if (mixed) got = got && mbar_wait(&b_full[sr.i], sr.ph, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          fail(25);
+          ok = false;
+          break;
+        }
+        if (CODES) {
+          const uint8_t* src = raw_slot(rr.i);
+          uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kTok * 128);
+#pragma unroll
+          for (int k = 0; k < kTok / 8; ++k) {
+            const int r = r0 + 8 * k;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                widen_codes8(*reinterpret_cast<const uint2*>(src + r * kD + c * 8));
+          }
+        }
+        if (mixed) {
+          // rows of tokens that this adapter does not have: two lanes per row, the
+          // rows that this warp itself has written
+          __syncwarp();
+          const int w2 = 2 * (warp - 4), r = w2 + (lane >> 4) + 8 * ((lane & 15) >> 1), half = lane & 1, m = m0 + r;
+          if (m >= a.M || __ldg(a.ids + m) != l) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stage_a(sr.i) + half * 8192 + r * 128 + q * 16) = zero;
+            for (int q = half; q < 8 * Sh::kAtoms; q += 2)
+              *reinterpret_cast<uint4*>(stage_b(sr.i) + (q >> 3) * 8192 + r * 128 + (q & 7) * 16) = zero;
+          }
+        }
+        if (CODES || mixed) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&a_full[sr.i]);
+          if (CODES) mbar_arrive(&raw_empty[rr.i]);
+        }
+        sr.template next<S_>();
+        if (CODES) rr.template next<RW>();
+      }
+    } else if (warp >= 4 + kXf) {
+      // ------------------------------------------------------------ epilogue
+      for (int i = 0; ok && i < n; i += kUnit) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
+          fail(26);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + ar.i * NB;
+#pragma unroll
+        for (int r = 0; r < Sh::kRanks; r += 16) {
+#pragma unroll
+          for (int sp = 2; sp >= 0; --sp) {
+            uint32_t v[16];
+            tmem_ld16(taddr + sp * Sh::kRanks + r, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              asm volatile("" : "+r"(v[e]));
+              tot[r + e] += __uint_as_float(v[e]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ar.i]);
+        ar.template next<2>();
+      }
+    }
+  }
+
+  if (warp >= 4 + kXf) {
+    const int d = d0 + 32 * (warp & 3) + lane;
+    if (d < a.D) {
+      float* g = a.g + ((size_t)split * a.R + row0 + a.rb0) * a.D + d;
+#pragma unroll
+      for (int r = 0; r < Sh::kRanks; ++r)
+        if (r < nr) g[(size_t)r * a.D] = tot[r];
+    }
+  } else if (warp == 1 && lane == 0 && issued) {
+    mma_commit(drain);
+    mbar_wait(drain, 0, never_flag);
+  } else if ((warp == 0 || warp == 2) && lane == 0 && (!ok || *abort_flag)) {
+    grace();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Sh::kTmem);
+  }
+}
+
+// g[i] = sum of the splits' values, splits in increasing order.
+__global__ void __launch_bounds__(256) lora_sum_kernel(const float4* __restrict__ p, int splits, size_t n,
+                                                       float4* __restrict__ g) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+    float4 v = p[i];
+#pragma unroll 4
+    for (int k = 1; k < splits; ++k) {
+      const float4 w = p[(size_t)k * n + i];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    g[i] = v;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+int rank_blocks(int max_rank) { return ceil_div(max_rank, 64); }
+int block_ranks(int max_rank, int rb) { return (std::min(64, max_rank - 64 * rb) + 15) / 16 * 16; }
+int block_pad(int max_rank, int rb) { return (3 * block_ranks(max_rank, rb) + 63) / 64 * 64; }
+size_t terms_bytes(int M, int max_rank) {
+  size_t b = 0;
+  for (int rb = 0; rb < rank_blocks(max_rank); ++rb) b += align256((size_t)M * block_pad(max_rank, rb) * 2);
+  return b;
+}
+
+// Token ranges: about four CTAs per SM, eight or more 64s each.
+int grad_splits(int M, int D, int L) {
+  const int chunks = ceil_div(M, kTok);
+  return std::max(1, std::min(std::min(ceil_div(chunks, kUnit), 16), 4 * num_sms() / std::max(1, ceil_div(D, kD) * L)));
+}
+
+size_t part_bytes(const aq_lora* ad, int M, int D) {
+  const int s = grad_splits(M, D, ad->L);
+  return s > 1 ? align256((size_t)s * ad->R * D * sizeof(float)) : 0;
+}
+
+template <int NB, bool CODES>
+cudaError_t launch_shape(const GradMaps& maps, const GradArgs& a, cudaStream_t st) {
+  using Sh = GradShape<NB, CODES>;
+  cudaError_t e = ensure_smem_attr<lora_grad_kernel<NB, CODES>>(Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.L, a.splits), dim3(kThreads),
+                    (size_t)Sh::kSmem, st, maps, a);
+}
+
+template <bool CODES>
+cudaError_t launch_ranks(int ranks, const GradMaps& maps, const GradArgs& a, cudaStream_t st) {
+  switch (ranks) {
+    case 16: return launch_shape<48, CODES>(maps, a, st);
+    case 32: return launch_shape<96, CODES>(maps, a, st);
+    case 48: return launch_shape<144, CODES>(maps, a, st);
+    case 64: return launch_shape<192, CODES>(maps, a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t lora_grad_ws_bytes(const aq_lora* ad, int M) {
+  return align256((size_t)ceil_div(M, kTok) * 4) + 2 * terms_bytes(M, ad->max_rank) +
+         std::max(part_bytes(ad, M, ad->K), part_bytes(ad, M, ad->N));
+}
+
+cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, const void* x,
+                             int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
+                             float* dbt, void* header, void* ws, cudaStream_t st) {
+  char* at = static_cast<char*>(ws);
+  int32_t* info = reinterpret_cast<int32_t*>(at);
+  at += align256((size_t)ceil_div(M, kTok) * 4);
+  char* terms[2] = {at, at + terms_bytes(M, ad->max_rank)};
+  float* part = reinterpret_cast<float*>(at + 2 * terms_bytes(M, ad->max_rank));
+  cudaError_t e = cudaSuccess;
+  size_t off = 0;
+  for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
+    const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
+    TermsArgs a{{{t, tsplits, sx, reinterpret_cast<uint16_t*>(terms[0] + off)},
+                 {s, 1, nullptr, reinterpret_cast<uint16_t*>(terms[1] + off)}},
+                ids, ad->off, M, ad->L, ad->R, ad->max_rank, 64 * rb, rc, npad, info};
+    e = launch_pdl(lora_terms_kernel, dim3(ceil_div(M, kTok), 2), dim3(256), 0, st, a);
+    off += align256((size_t)M * npad * 2);
+  }
+  for (int side = 0; side < 2 && e == cudaSuccess; ++side) {
+    const int D = side ? ad->N : ad->K;
+    const bool codes = !side && sx;
+    float* out = side ? dbt : da;
+    const int splits = grad_splits(M, D, ad->L);
+    off = 0;
+    for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
+      const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
+      GradMaps maps;
+      memset(&maps, 0, sizeof(maps));
+      bool ok = map_2d(&maps.terms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, terms[side] + off, npad, M, (uint64_t)npad * 2,
+                       64, kTok, true);
+      ok = ok && (codes ? map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, D, M, ldx, kD, kTok, false)
+                  : side ? map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, D, M, (uint64_t)ldd * 2, 64, kTok, true)
+                         : map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, D, M, (uint64_t)ldx * 2, 64, kTok, true));
+      if (!ok) return cudaErrorInvalidValue;
+      const GradArgs a{ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb, splits > 1 ? part : out, splits, header};
+      e = codes ? launch_ranks<true>(rc, maps, a, st) : launch_ranks<false>(rc, maps, a, st);
+      off += align256((size_t)M * npad * 2);
+    }
+    if (e == cudaSuccess && splits > 1) {
+      const size_t n = (size_t)ad->R * D / 4;
+      const int blocks = (int)std::min<size_t>((n + 255) / 256, 8 * (size_t)num_sms());
+      e = launch_pdl(lora_sum_kernel, dim3(blocks), dim3(256), 0, st, reinterpret_cast<const float4*>(part), splits, n,
+                     reinterpret_cast<float4*>(out));
+    }
+  }
+  return e;
+}
+
+}  // namespace aq
