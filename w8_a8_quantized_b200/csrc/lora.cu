@@ -490,9 +490,20 @@ int shrink_splits(int M, const Table& t) {
   return std::max(1, std::min(chunks, ceil_div(2 * num_sms(), tiles)));
 }
 
-size_t p_bytes(int M, const Table& t) {
-  return align256((size_t)shrink_splits(M, t) * M * t.max_rank * sizeof(float));
+// Partial sums of the products: as the kernels that write and read them split the long axis and pitch the rows.
+struct Products {
+  int splits, ld;
+};
+Products products(const aq_lora* ad, int M, bool b_side) {
+  const Table t = b_side ? table_b(ad) : table_a(ad);
+  return lora_tc_fits(ad, M) ? Products{lora_tc_splits(M, t.D), (t.max_rank + 15) / 16 * 16}
+                             : Products{shrink_splits(M, t), t.max_rank};
 }
+size_t p_bytes(const aq_lora* ad, int M, bool b_side) {
+  const Products p = products(ad, M, b_side);
+  return align256((size_t)p.splits * M * p.ld * sizeof(float));
+}
+
 cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p, cudaStream_t st) {
   ShrinkArgs a{t, x, ldx, M, ids, p, shrink_splits(M, t), share(M, t)};
   cudaError_t e = ensure_smem_attr<lora_shrink_kernel>(sizeof(ShrinkSmem));
@@ -520,6 +531,20 @@ cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, in
   return dtype == AQ_F32 ? launch_expand<true>(a, st) : launch_expand<false>(a, st);
 }
 
+// p = the products of x with the a (or b) side; out = y + p's sums times the other side.
+cudaError_t shrink_any(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p,
+                       void* header, cudaStream_t st) {
+  return lora_tc_fits(ad, M) ? launch_lora_shrink_tc(ad, b_side, x, ldx, ids, M, p, header, st)
+                             : shrink(b_side ? table_b(ad) : table_a(ad), x, ldx, ids, M, p, st);
+}
+cudaError_t expand_any(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, const void* y, int ldy,
+                       void* out, int ldo, int dtype, float* s, void* header, cudaStream_t st) {
+  const int splits = products(ad, M, !b_side).splits;
+  return lora_tc_fits(ad, M)
+             ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, y, ldy, out, ldo, dtype == AQ_F32, s, header, st)
+             : expand(b_side ? table_b(ad) : table_a(ad), ids, M, p, splits, y, ldy, out, ldo, dtype, s, st);
+}
+
 int check_lora(const aq_lora* ad) {
   if (!ad || !ad->a || !ad->bt || !ad->off || !ad->scale) return AQ_ERR_ARG;
   if (ad->N < 8 || ad->K < 8 || ad->N % 8 || ad->K % 8 || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
@@ -542,9 +567,8 @@ using namespace aq;
 
 extern "C" size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward) {
   if (check_lora(ad) != AQ_OK || M < 1 || M > kMaxTokens) return 0;
-  const Table ta = table_a(ad), tb = table_b(ad);
-  if (!backward) return lora_decode_fits(ad, M) ? 16 : kWsHeader + p_bytes(M, ta);
-  return kWsHeader + p_bytes(M, tb) + lora_grad_ws_bytes(ad, M);
+  if (!backward) return lora_decode_fits(ad, M) ? 16 : kWsHeader + p_bytes(ad, M, false);
+  return kWsHeader + p_bytes(ad, M, true) + lora_grad_ws_bytes(ad, M);
 }
 
 extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
@@ -563,11 +587,9 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
   if (lora_decode_fits(ad, M))
     return launch_lora_decode(ad, x, ldx, ids, M, y, ldy, out, ldo, ydtype == AQ_F32, s, st) == cudaSuccess ? AQ_OK
                                                                                                             : AQ_ERR_CUDA;
-  const Table ta = table_a(ad);
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
-  cudaError_t e = shrink(ta, x, ldx, ids, M, p, st);
-  if (e == cudaSuccess)
-    e = expand(table_b(ad), ids, M, p, shrink_splits(M, ta), y, ldy, out, ldo, ydtype, s, st);
+  cudaError_t e = shrink_any(ad, false, x, ldx, ids, M, p, ws, st);
+  if (e == cudaSuccess) e = expand_any(ad, true, ids, M, p, y, ldy, out, ldo, ydtype, s, ws, st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }
 
@@ -590,13 +612,12 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 1)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Table ta = table_a(ad), tb = table_b(ad);
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
-  const int splits = shrink_splits(M, tb);
-  cudaError_t e = shrink(tb, dy, ldd, ids, M, p, st);
-  if (e == cudaSuccess && dx) e = expand(ta, ids, M, p, splits, add, ldadd, dx, lddx, dxdtype, nullptr, st);
+  const Products t = products(ad, M, true);
+  cudaError_t e = shrink_any(ad, true, dy, ldd, ids, M, p, ws, st);
+  if (e == cudaSuccess && dx) e = expand_any(ad, false, ids, M, p, add, ldadd, dx, lddx, dxdtype, nullptr, ws, st);
   if (e == cudaSuccess)
-    e = launch_lora_grad(ad, ids, M, p, splits, x, ldx, sx, da, s, dy, ldd, dbt, ws,
-                         reinterpret_cast<char*>(p) + p_bytes(M, tb), st);
+    e = launch_lora_grad(ad, ids, M, p, t.splits, t.ld, x, ldx, sx, da, s, dy, ldd, dbt, ws,
+                         reinterpret_cast<char*>(p) + p_bytes(ad, M, true), st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

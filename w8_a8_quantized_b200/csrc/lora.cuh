@@ -10,12 +10,24 @@ bool lora_decode_fits(const aq_lora* ad, int M);
 cudaError_t launch_lora_decode(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
                                int ldy, void* out, int ldo, bool f32, float* s, cudaStream_t st);
 
-// Weight gradients (lora_grad.cu): t [tsplits][M][max_rank] partial sums of the
+// More than 64 tokens, ranks up to 64 (lora_tc.cu).  Shrink: p [splits][M][rp] (rp =
+// max_rank rounded up to 16) from the a side or the b side of the tables; expand:
+// out = y + p's sums times the other side.  `header`: the error word of the call's
+// workspace.
+bool lora_tc_fits(const aq_lora* ad, int M);
+int lora_tc_splits(int M, int D);
+cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M,
+                                  float* p, void* header, cudaStream_t st);
+cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
+                                  const void* y, int ldy, void* out, int ldo, bool f32, float* s, void* header,
+                                  cudaStream_t st);
+
+// Weight gradients (lora_grad.cu): t [tsplits][M][ldt] partial sums of the
 // output's gradient times B, s [M][max_rank] the forward products.  `header`: the
 // error word of a call's workspace; `ws`: lora_grad_ws_bytes, 256-byte aligned
 // behind a workspace that starts on 16 bytes.
 size_t lora_grad_ws_bytes(const aq_lora* ad, int M);
-cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, const void* x,
+cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
                              int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
                              float* dbt, void* header, void* ws, cudaStream_t st);
 

@@ -37,8 +37,8 @@ constexpr int kXf = 4, kEpi = 4;  // warps
 
 // ---------------------------------------------------------------- terms
 struct TermsJob {
-  const float* p;     // [splits][M][max_rank]
-  int splits;
+  const float* p;     // [splits][M][ld]
+  int splits, ld;
   const float* sx;    // [M] or null
   uint16_t* terms;    // [M][npad]: hi, mid, lo of `rc` ranks each
 };
@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsArgs a) {
     for (int c = tid & 15; c < a.rc; c += 16) {
       float v = 0.f;
       if (c < rank[t]) {
-        const float* src = j.p + (size_t)(m0 + t) * a.max_rank + a.rb0 + c;
-        for (int k = 0; k < j.splits; ++k) v += __ldg(src + (size_t)k * a.M * a.max_rank);
+        const float* src = j.p + (size_t)(m0 + t) * j.ld + a.rb0 + c;
+        for (int k = 0; k < j.splits; ++k) v += __ldg(src + (size_t)k * a.M * j.ld);
         v *= scale;
       }
       uint16_t* d = j.terms + (size_t)(m0 + t) * a.npad + c;
@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int d0 = blockIdx.x * kD, l = blockIdx.y, split = blockIdx.z;
-  pdl_launch_dependents();
   pdl_wait();
   const int row0 = min(max(__ldg(a.off + l), 0), a.R);
   const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
@@ -219,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // not earlier: a later kernel's CTA that held this one's tensor memory while it
+  // waits for this one to end would never see it end
+  pdl_launch_dependents();
 
   auto fail = [&](int info) {
     *abort_flag = 1;
@@ -480,7 +482,7 @@ size_t lora_grad_ws_bytes(const aq_lora* ad, int M) {
          std::max(part_bytes(ad, M, ad->K), part_bytes(ad, M, ad->N));
 }
 
-cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, const void* x,
+cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
                              int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
                              float* dbt, void* header, void* ws, cudaStream_t st) {
   char* at = static_cast<char*>(ws);
@@ -492,8 +494,8 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
   size_t off = 0;
   for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
     const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
-    TermsArgs a{{{t, tsplits, sx, reinterpret_cast<uint16_t*>(terms[0] + off)},
-                 {s, 1, nullptr, reinterpret_cast<uint16_t*>(terms[1] + off)}},
+    TermsArgs a{{{t, tsplits, ldt, sx, reinterpret_cast<uint16_t*>(terms[0] + off)},
+                 {s, 1, ad->max_rank, nullptr, reinterpret_cast<uint16_t*>(terms[1] + off)}},
                 ids, ad->off, M, ad->L, ad->R, ad->max_rank, 64 * rb, rc, npad, info};
     e = launch_pdl(lora_terms_kernel, dim3(ceil_div(M, kTok), 2), dim3(256), 0, st, a);
     off += align256((size_t)M * npad * 2);
