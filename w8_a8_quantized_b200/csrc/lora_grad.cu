@@ -11,11 +11,13 @@
 // them all.  It is bound by the bytes of x: 64 x 128 of them per step against
 // 64 x 128 x 3r multiplications.
 //
-// A CTA takes 128 columns, one adapter and a range of tokens, and skips the 64s
-// that its adapter has no part in.  Where a 64 holds other adapters' tokens too,
-// their rows are cleared in shared memory on both sides, so that nothing of them,
-// not even an infinity, reaches the sum.  Tensor memory sums 512 tokens at a time;
-// the epilogue adds those sums in fp32 registers, rounding to nearest.
+// A CTA takes 128 columns and a range of tokens, whoever's they are, so that
+// unequal adapters do not make unequal CTAs; it goes through the adapters of its
+// range one after another, over the 64s that have a part in each.  Where a 64 holds
+// other adapters' tokens too, their rows are cleared in shared memory on both sides,
+// so that nothing of them, not even an infinity, reaches the sum.  Tensor memory
+// sums 512 tokens at a time; the epilogue adds those sums in fp32 registers,
+// rounding to nearest.  Partial sums of the ranges are added in range order.
 //
 // Roles: warp 0 codes (TMA), warp 1 tensor memory and MMA, warp 2 terms and bf16
 // activations (TMA), warps 4-7 codes -> bf16 and the clearing, warps 8-11 epilogue.
@@ -34,6 +36,7 @@ constexpr int kD = 128;        // columns of a CTA
 constexpr int kThreads = 384;
 constexpr int kUnit = 8;       // steps summed in tensor memory
 constexpr int kXf = 4, kEpi = 4;  // warps
+constexpr int kMaxAdapters = 16384;
 
 // ---------------------------------------------------------------- terms
 struct TermsJob {
@@ -79,17 +82,36 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsArgs a) {
     }
   }
   __syncthreads();
-  for (int t = tid >> 4; t < kTok && m0 + t < a.M; t += 16) {
-    const float scale = j.sx && rank[t] > 0 ? __ldg(j.sx + m0 + t) : 1.f;
-    for (int c = tid & 15; c < a.rc; c += 16) {
-      float v = 0.f;
-      if (c < rank[t]) {
-        const float* src = j.p + (size_t)(m0 + t) * j.ld + a.rb0 + c;
-        for (int k = 0; k < j.splits; ++k) v += __ldg(src + (size_t)k * a.M * j.ld);
-        v *= scale;
+  const int per_row = a.rc / 8;
+  for (int i = tid; i < kTok * per_row; i += 256) {
+    const int t = i / per_row, c = (i - t * per_row) * 8, m = m0 + t;
+    if (m >= a.M) break;
+    const int left = rank[t] - c;
+    float v[8] = {};
+    if (left > 0) {
+      const float* src = j.p + (size_t)m * j.ld + a.rb0 + c;
+      const size_t step = (size_t)a.M * j.ld;
+#pragma unroll 4
+      for (int k = 0; k < j.splits; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) v[e] += __ldg(src + k * step + e);
+      if (j.sx) {
+        const float scale = __ldg(j.sx + m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= scale;
       }
-      uint16_t* d = j.terms + (size_t)(m0 + t) * a.npad + c;
-      split3(v, d[0], d[a.rc], d[2 * a.rc]);
+    }
+    uint16_t h[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split3(v[e], h[0][e], h[1][e], h[2][e]);
+    uint16_t* d = j.terms + (size_t)m * a.npad + c;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = h[k][2 * e] | ((uint32_t)h[k][2 * e + 1] << 16);
+      *reinterpret_cast<uint4*>(d + k * a.rc) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -105,7 +127,7 @@ struct GradShape {
   static constexpr int kStages = NB <= 48 ? 3 : NB <= 96 ? (CODES ? 2 : 3) : 4;
   static constexpr int kRaw = CODES ? 3 : 0;          // ring of codes, 8 KiB each
   static constexpr int kTmem = 2 * NB <= 128 ? 128 : 2 * NB <= 256 ? 256 : 512;
-  static constexpr int kCtrl = 512 + kThreads * 2;
+  static constexpr int kCtrl = 512 + kThreads * 2 + kMaxAdapters / 8;
   static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kTok * kD + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
   static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
@@ -121,8 +143,9 @@ struct GradArgs {
   const int32_t* off;
   const int32_t* info;
   int M, D, L, R, max_rank, rb0;
-  float* g;  // [splits][R][D]
+  float* g;       // [splits][R][D]
   int splits;
+  uint8_t* has;   // [L][splits]: whether the range has tokens of the adapter
   void* ws;
 };
 
@@ -164,30 +187,24 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   volatile int* never_flag = abort_flag + 1;
   volatile int* count = abort_flag + 2;  // [12] listed chunks of each warp
   volatile uint16_t* list = reinterpret_cast<volatile uint16_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512);
+  uint32_t* present = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512 + kThreads * 2);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int d0 = blockIdx.x * kD, l = blockIdx.y, split = blockIdx.z;
+  const int d0 = blockIdx.x * kD, split = blockIdx.y;
   pdl_wait();
-  const int row0 = min(max(__ldg(a.off + l), 0), a.R);
-  const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
-  if (nr <= 0) return;
   const int chunks = (a.M + kTok - 1) / kTok;
   const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
-  // whether the 64 tokens c are this adapter's: 0 none, 1 all, 2 some
-  auto part_in = [&](int c) {
-    const int v = c < c1 ? __ldg(a.info + c) : -1;
-    int take = v == l;
-    if (v == -2)
-      for (int m = c * kTok; m < min((c + 1) * kTok, a.M); ++m)
-        if (__ldg(a.ids + m) == l) take = 2;
-    return take;
-  };
-  if (c1 - c0 <= kThreads && !__syncthreads_or(part_in(c0 + tid))) {  // nothing here: zeros
-    const int width = min(kD, a.D - d0);
-    for (int i = tid; i < nr * width; i += kThreads)
-      a.g[((size_t)split * a.R + row0 + a.rb0 + i / width) * a.D + d0 + i % width] = 0.f;
-    return;
-  }
+  // the adapters of this range's (at most 384) 64s, one of which each thread looks after
+  const int words = (a.L + 31) / 32, own = c0 + tid < c1 ? __ldg(a.info + c0 + tid) : -1;
+  const int own_m0 = (c0 + tid) * kTok, own_m1 = min(own_m0 + kTok, a.M);
+  for (int i = tid; i < words; i += kThreads) present[i] = 0;
+  __syncthreads();
+  if (own >= 0) atomicOr(&present[own >> 5], 1u << (own & 31));
+  if (own == -2)
+    for (int m = own_m0; m < own_m1; ++m) {
+      const int v = __ldg(a.ids + m);
+      if (v >= 0 && v < a.L) atomicOr(&present[v >> 5], 1u << (v & 31));
+    }
 
   if (tid == 0) {
     for (int i = 0; i < RW; ++i) {
@@ -229,14 +246,23 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
 
   Ring sr{0, 0}, rr{0, 0}, ar{0, 0};  // stage, raw slot, accumulator
   bool ok = true, issued = false;
-  float tot[Sh::kRanks];
-#pragma unroll
-  for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
 
-  for (int base = c0; base < c1; base += kThreads) {
-    // the 64s of this adapter among the next 384, in order; bit 15: others' tokens too
+  for (int l = 0; l < a.L; ++l) {
+    const uint32_t bits = present[l >> 5] >> (l & 31);
+    if (bits == 0) {  // none up to the word's end
+      l |= 31;
+      continue;
+    }
+    l += __ffs(bits) - 1;
+    const int row0 = min(max(__ldg(a.off + l), 0), a.R);
+    const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
+    if (nr <= 0) continue;
+    // its 64s, in order; bit 15: others' tokens too
     __syncthreads();
-    const int take = part_in(base + tid);
+    int take = own == l;
+    if (own == -2)
+      for (int m = own_m0; m < own_m1; ++m)
+        if (__ldg(a.ids + m) == l) take = 2;
     const unsigned vote = __ballot_sync(0xffffffffu, take != 0);
     if (lane == 0) count[warp] = __popc(vote);
     __syncthreads();
@@ -247,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     }
     if (take) list[at] = (uint16_t)(tid | (take == 2 ? 0x8000 : 0));
     __syncthreads();
+    const int base = c0;
 
     if (warp == 0 && CODES) {
       // ------------------------------------------------------------ codes
@@ -360,6 +387,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       }
     } else if (warp >= 4 + kXf) {
       // ------------------------------------------------------------ epilogue
+      float tot[Sh::kRanks];
+#pragma unroll
+      for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
       for (int i = 0; ok && i < n; i += kUnit) {
         if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
           fail(26);
@@ -387,21 +417,35 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
         if (lane == 0) mbar_arrive(&acc_empty[ar.i]);
         ar.template next<2>();
       }
+      const int d = d0 + 32 * (warp & 3) + lane;
+      if (d < a.D) {
+        float* g = a.g + ((size_t)split * a.R + row0 + a.rb0) * a.D + d;
+#pragma unroll
+        for (int r = 0; r < Sh::kRanks; ++r)
+          if (r < nr) g[(size_t)r * a.D] = tot[r];
+      }
     }
   }
 
-  if (warp >= 4 + kXf) {
-    const int d = d0 + 32 * (warp & 3) + lane;
-    if (d < a.D) {
-      float* g = a.g + ((size_t)split * a.R + row0 + a.rb0) * a.D + d;
-#pragma unroll
-      for (int r = 0; r < Sh::kRanks; ++r)
-        if (r < nr) g[(size_t)r * a.D] = tot[r];
+  // adapters without tokens here: noted for the sum, or zeros where there is none
+  if (a.splits > 1) {
+    if (blockIdx.x == 0 && a.rb0 == 0)
+      for (int l = tid; l < a.L; l += kThreads) a.has[(size_t)l * a.splits + split] = (present[l >> 5] >> (l & 31)) & 1u;
+  } else {
+    const int width = min(kD, a.D - d0);
+    for (int l = 0; l < a.L; ++l) {
+      if ((present[l >> 5] >> (l & 31)) & 1u) continue;
+      const int row0 = min(max(__ldg(a.off + l), 0), a.R);
+      const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
+      for (int i = tid; i < nr * width; i += kThreads)
+        a.g[(size_t)(row0 + a.rb0 + i / width) * a.D + d0 + i % width] = 0.f;
     }
-  } else if (warp == 1 && lane == 0 && issued) {
+  }
+  if (warp == 1 && lane == 0 && issued) {
     mma_commit(drain);
     mbar_wait(drain, 0, never_flag);
-  } else if ((warp == 0 || warp == 2) && lane == 0 && (!ok || *abort_flag)) {
+  }
+  if ((warp == 0 || warp == 2) && lane == 0 && (!ok || *abort_flag)) {
     grace();
   }
   tc_fence_before();
@@ -412,22 +456,27 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   }
 }
 
-// g[i] = sum of the splits' values, splits in increasing order.
-__global__ void __launch_bounds__(256) lora_sum_kernel(const float4* __restrict__ p, int splits, size_t n,
-                                                       float4* __restrict__ g) {
+// g = the sum of the ranges' partial sums in range order, for one adapter and 1024 columns.
+__global__ void __launch_bounds__(256)
+    lora_sum_kernel(const float* __restrict__ p, const uint8_t* __restrict__ has, const int32_t* __restrict__ off,
+                    int splits, int R, int D, int max_rank, float* __restrict__ g) {
   pdl_launch_dependents();
   pdl_wait();
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-    float4 v = p[i];
-#pragma unroll 4
-    for (int k = 1; k < splits; ++k) {
-      const float4 w = p[(size_t)k * n + i];
+  const int l = blockIdx.y, d = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (d >= D) return;
+  const int row0 = min(max(__ldg(off + l), 0), R), row1 = min(row0 + max_rank, min(max(__ldg(off + l + 1), row0), R));
+  const uint8_t* mine = has + (size_t)l * splits;
+  for (int r = row0 + blockIdx.z; r < row1; r += gridDim.z) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < splits; ++k) {
+      if (!mine[k]) continue;
+      const float4 w = *reinterpret_cast<const float4*>(p + ((size_t)k * R + r) * D + d);
       v.x += w.x;
       v.y += w.y;
       v.z += w.z;
       v.w += w.w;
     }
-    g[i] = v;
+    *reinterpret_cast<float4*>(g + (size_t)r * D + d) = v;
   }
 }
 
@@ -444,15 +493,26 @@ size_t terms_bytes(int M, int max_rank) {
   return b;
 }
 
-// Token ranges: about four CTAs per SM, eight or more 64s each.
-int grad_splits(int M, int D, int L) {
-  const int chunks = ceil_div(M, kTok);
-  return std::max(1, std::min(std::min(ceil_div(chunks, kUnit), 16), 4 * num_sms() / std::max(1, ceil_div(D, kD) * L)));
+// Token ranges: at most 384 64s each; the fewest steps on the longest path over two
+// CTAs per SM, counting a CTA's start and end as ten.
+int grad_splits(int M, int D) {
+  const int chunks = ceil_div(M, kTok), blocks = ceil_div(D, kD), slots = 2 * num_sms();
+  const int least = ceil_div(chunks, kThreads);
+  int best = least;
+  long long cost = 0;
+  for (int s = least; s <= std::max(least, std::min(chunks, 16)); ++s) {
+    const long long c = (long long)ceil_div((long long)blocks * s, slots) * (ceil_div(chunks, s) + 10);
+    if (cost == 0 || c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
 }
 
 size_t part_bytes(const aq_lora* ad, int M, int D) {
-  const int s = grad_splits(M, D, ad->L);
-  return s > 1 ? align256((size_t)s * ad->R * D * sizeof(float)) : 0;
+  const int s = grad_splits(M, D);
+  return s > 1 ? align256((size_t)s * ad->R * D * sizeof(float)) + align256((size_t)ad->L * s) : 0;
 }
 
 template <int NB, bool CODES>
@@ -460,7 +520,7 @@ cudaError_t launch_shape(const GradMaps& maps, const GradArgs& a, cudaStream_t s
   using Sh = GradShape<NB, CODES>;
   cudaError_t e = ensure_smem_attr<lora_grad_kernel<NB, CODES>>(Sh::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.L, a.splits), dim3(kThreads),
+  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.splits), dim3(kThreads),
                     (size_t)Sh::kSmem, st, maps, a);
 }
 
@@ -504,7 +564,8 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
     const int D = side ? ad->N : ad->K;
     const bool codes = !side && sx;
     float* out = side ? dbt : da;
-    const int splits = grad_splits(M, D, ad->L);
+    const int splits = grad_splits(M, D);
+    uint8_t* has = reinterpret_cast<uint8_t*>(part) + align256((size_t)splits * ad->R * D * sizeof(float));
     off = 0;
     for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
       const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
@@ -516,15 +577,13 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
                   : side ? map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, D, M, (uint64_t)ldd * 2, 64, kTok, true)
                          : map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, D, M, (uint64_t)ldx * 2, 64, kTok, true));
       if (!ok) return cudaErrorInvalidValue;
-      const GradArgs a{ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb, splits > 1 ? part : out, splits, header};
+      const GradArgs a{ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb, splits > 1 ? part : out, splits, has, header};
       e = codes ? launch_ranks<true>(rc, maps, a, st) : launch_ranks<false>(rc, maps, a, st);
       off += align256((size_t)M * npad * 2);
     }
     if (e == cudaSuccess && splits > 1) {
-      const size_t n = (size_t)ad->R * D / 4;
-      const int blocks = (int)std::min<size_t>((n + 255) / 256, 8 * (size_t)num_sms());
-      e = launch_pdl(lora_sum_kernel, dim3(blocks), dim3(256), 0, st, reinterpret_cast<const float4*>(part), splits, n,
-                     reinterpret_cast<float4*>(out));
+      e = launch_pdl(lora_sum_kernel, dim3(ceil_div(D, 1024), ad->L, std::min(ad->max_rank, 16)), dim3(256), 0, st, part, has, ad->off, splits, ad->R,
+                     D, ad->max_rank, out);
     }
   }
   return e;

@@ -329,8 +329,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
 // 2^-17 of a product, where out is rounded to bf16), table rows by asynchronous
 // copies that clear the rows behind the adapter's rank, y and out by TMA through
 // the same buffer.  Blocks of 128 bf16 or 64 fp32 columns: 32 KiB of y.
-constexpr int kEThreads = 384;
-constexpr int kEY = 3, kEW = 3, kEAcc = 4;
+// Eight epilogue warps: four per half block, each half with its own stores, so that
+// a warp's chain per block (y, sums, back) is short.
+constexpr int kEThreads = 512;
+constexpr int kEY = 4, kEAcc = 4;
 constexpr int kYBytes = 2 * kTok * 128;
 
 struct ExpandMaps {
@@ -345,8 +347,11 @@ struct ExpandTcArgs {
   void* ws;
 };
 
-template <bool F32>
+// kEW: slots of table rows, as many as fit (3 for 64 ranks, 5 up to 32): with k slots
+// k - 1 loads are on their way.
+template <bool F32, int EW>
 struct ExpandTcShape {
+  static constexpr int kEW = EW;
   static constexpr int kBN = F32 ? 64 : 128, kTerms = F32 ? 3 : 2, kPer16 = F32 ? 4 : 8;
   static constexpr int kHalf = 8 * kPer16;  // columns of 128 bytes
   static constexpr int kCtrl = 512;
@@ -373,10 +378,10 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
                : "memory");
 }
 
-template <bool F32>
+template <bool F32, int kEW>
 __global__ void __launch_bounds__(kEThreads, 1)
     lora_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const __grid_constant__ ExpandTcArgs a) {
-  using Sh = ExpandTcShape<F32>;
+  using Sh = ExpandTcShape<F32, kEW>;
   constexpr int BN = Sh::kBN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -393,8 +398,8 @@ __global__ void __launch_bounds__(kEThreads, 1)
   uint64_t* w_free = w_full + kEW;
   uint64_t* acc_full = w_free + kEW;
   uint64_t* acc_empty = acc_full + kEAcc;
-  uint64_t* epi = acc_empty + kEAcc;
-  uint64_t* drain = epi + 1;
+  uint64_t* epi = acc_empty + kEAcc;  // [2]
+  uint64_t* drain = epi + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_flag = abort_flag + 1;
@@ -408,7 +413,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kEY; ++i) {
       mbar_init(&y_full[i], 1);
-      mbar_init(&y_free[i], 1);
+      mbar_init(&y_free[i], 2);
     }
     for (int i = 0; i < kEW; ++i) {
       mbar_init(&w_full[i], 4);
@@ -416,9 +421,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
     }
     for (int i = 0; i < kEAcc; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);
     }
-    mbar_init(epi, 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&epi[i], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     *never_flag = 0;
@@ -540,9 +545,20 @@ __global__ void __launch_bounds__(kEThreads, 1)
     // ------------------------------------------------------------ table rows
     const int lt = tid - 128;
     Ring wr{0, 0}, pr{0, 0};  // the slot being filled, the slot being published
-    int pending = 0;
+    int pending = 0;          // loads on their way
+    auto publish = [&]() {    // the oldest has landed
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_full[pr.i]);
+      pr.template next<kEW>();
+      --pending;
+    };
     for (int b = b0; ok && b < b1; ++b)
       for (int i = 0; i < na; ++i) {
+        if (pending == kEW - 1) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kEW - 2) : "memory");
+          publish();
+        }
         if (!__all_sync(0xffffffffu, mbar_wait(&w_free[wr.i], wr.ph ^ 1u, abort_flag))) {
           fail(43);
           ok = false;
@@ -559,34 +575,29 @@ __global__ void __launch_bounds__(kEThreads, 1)
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         wr.template next<kEW>();
-        if (pending) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&w_full[pr.i]);
-          pr.template next<kEW>();
-        }
-        pending = 1;
+        ++pending;
       }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (pending && lane == 0) mbar_arrive(&w_full[pr.i]);
+    while (pending) publish();
   } else if (warp >= 8) {
     // ------------------------------------------------------------ epilogue
-    const int w = warp & 3, row = 32 * w + lane, mine = q.slot[row];
+    const int w = warp & 3, half = (warp - 8) >> 2, row = 32 * w + lane, mine = q.slot[row];
+    const bool stores = w == 0 && lane == 0;
+    constexpr int HC = BN / 2, kLd = HC / 16, kPer = 16 / Sh::kPer16;  // columns, loads, chunks per load
     Ring yr{0, 0}, ar{0, 0};
     uint32_t phase = 0;
     int freed = 0;  // next y buffer to hand back
     for (int b = b0; ok && b < b1; ++b) {
-      uint8_t* yrow = ybuf(yr.i) + row * 128;
+      uint8_t* ybase = ybuf(yr.i) + half * (kYBytes / 2);
+      uint4* yrow = reinterpret_cast<uint4*>(ybase + row * 128);  // chunk c of the row at c ^ (row & 7)
       if (!__all_sync(0xffffffffu, mbar_wait(&y_full[yr.i], yr.ph, abort_flag))) {
         fail(44);
         ok = false;
         break;
       }
-      if (!a.has_y && mine < 0)
-        for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(yrow + (c >> 3) * (kYBytes / 2) + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      uint4 y[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) y[c] = a.has_y ? yrow[c ^ (row & 7)] : make_uint4(0, 0, 0, 0);
       for (int i = 0; i < na; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
           fail(45);
@@ -595,39 +606,32 @@ __global__ void __launch_bounds__(kEThreads, 1)
         }
         tc_fence_after();
         if (q.mask[i][w]) {
-          const uint32_t taddr = tmem_base + ((uint32_t)(32 * w) << 16) + ar.i * BN;
-          uint32_t v[2][16];
-          tmem_ld16(taddr, v[0]);
+          const uint32_t taddr = tmem_base + ((uint32_t)(32 * w) << 16) + ar.i * BN + half * HC;
+          uint32_t v[kLd][16];
 #pragma unroll
-          for (int c = 0; c < BN / 16; ++c) {
-            tmem_wait_ld();
+          for (int c = 0; c < kLd; ++c) tmem_ld16(taddr + 16 * c, v[c]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[c & 1][e]));
-            if (c + 1 < BN / 16) tmem_ld16(taddr + 16 * (c + 1), v[(c + 1) & 1]);
-            if (mine == i) {
-              const uint32_t(&d)[16] = v[c & 1];
+          for (int c = 0; c < kLd; ++c)
 #pragma unroll
-              for (int k = 0; k < 16 / Sh::kPer16; ++k) {
-                const int ch = c * (16 / Sh::kPer16) + k;  // 16-byte chunk of the row
-                uint4* at = reinterpret_cast<uint4*>(yrow + (ch >> 3) * (kYBytes / 2) + (((ch & 7) ^ (row & 7)) << 4));
-                uint4 y = a.has_y ? *at : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[c][e]));
+          if (mine == i) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint32_t* d = &v[c / kPer][(c % kPer) * Sh::kPer16];
+              uint32_t o[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
                 if constexpr (F32) {
-                  y.x = __float_as_uint(__uint_as_float(y.x) + __uint_as_float(d[4 * k]));
-                  y.y = __float_as_uint(__uint_as_float(y.y) + __uint_as_float(d[4 * k + 1]));
-                  y.z = __float_as_uint(__uint_as_float(y.z) + __uint_as_float(d[4 * k + 2]));
-                  y.w = __float_as_uint(__uint_as_float(y.w) + __uint_as_float(d[4 * k + 3]));
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(d[e]));
                 } else {
-                  uint32_t* o = &y.x;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 s2 =
-                        __floats2bfloat162_rn(__uint_as_float(o[e] << 16) + __uint_as_float(d[8 * k + 2 * e]),
-                                              __uint_as_float(o[e] & 0xFFFF0000u) + __uint_as_float(d[8 * k + 2 * e + 1]));
-                    o[e] = *reinterpret_cast<const uint32_t*>(&s2);
-                  }
+                  const __nv_bfloat162 s2 =
+                      __floats2bfloat162_rn(__uint_as_float(o[e] << 16) + __uint_as_float(d[2 * e]),
+                                            __uint_as_float(o[e] & 0xFFFF0000u) + __uint_as_float(d[2 * e + 1]));
+                  o[e] = *reinterpret_cast<const uint32_t*>(&s2);
                 }
-                *at = y;
               }
+              y[c] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
           tc_fence_before();
@@ -637,17 +641,20 @@ __global__ void __launch_bounds__(kEThreads, 1)
         ar.template next<kEAcc>();
       }
       if (!ok) break;
+      if (mine >= 0 || !a.has_y)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) yrow[c ^ (row & 7)] = y[c];
       fence_proxy_async_smem();
-      // everyone waits: a warp that ran ahead would arrive for the next block in place
-      // of one that has not finished this block
-      mbar_arrive(epi);
-      if (!__all_sync(0xffffffffu, mbar_wait(epi, phase, abort_flag))) {
+      __syncwarp();
+      // every warp waits: one that ran ahead would arrive for the next block in place of
+      // one that has not finished this block
+      if (lane == 0) mbar_arrive(&epi[half]);
+      if (!__all_sync(0xffffffffu, mbar_wait(&epi[half], phase, abort_flag))) {
         fail(46);
         break;
       }
-      if (warp == 8 && lane == 0) {
-        tma_store_2d(&maps.out, ybuf(yr.i), b * BN, m0);
-        if (b * BN + Sh::kHalf < t.D) tma_store_2d(&maps.out, ybuf(yr.i) + kYBytes / 2, b * BN + Sh::kHalf, m0);
+      if (stores) {
+        if (b * BN + half * Sh::kHalf < t.D) tma_store_2d(&maps.out, ybase, b * BN + half * Sh::kHalf, m0);
         bulk_commit();
         if (b > b0) {  // the store before this one has read its buffer
           bulk_wait_read<1>();
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
       __syncwarp();
       yr.template next<kEY>();
     }
-    if (warp == 8 && lane == 0) bulk_wait_all();
+    if (stores) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -687,10 +694,10 @@ cudaError_t launch_shrink(const ShrinkMaps& maps, const ShrinkTcArgs& a, cudaStr
                     maps, a);
 }
 
-template <bool F32>
+template <bool F32, int EW>
 cudaError_t launch_expand(const ExpandMaps& maps, const ExpandTcArgs& a, cudaStream_t st) {
-  using Sh = ExpandTcShape<F32>;
-  cudaError_t e = ensure_smem_attr<lora_expand_tc_kernel<F32>>(Sh::smem(kMaxTcRank));
+  using Sh = ExpandTcShape<F32, EW>;
+  cudaError_t e = ensure_smem_attr<lora_expand_tc_kernel<F32, EW>>(Sh::smem(EW == 3 ? kMaxTcRank : 32));
   if (e != cudaSuccess) return e;
   // column ranges per tile: the fewest blocks on the longest path, counting the
   // start of a CTA (list, terms, first copies) as four blocks
@@ -705,7 +712,7 @@ cudaError_t launch_expand(const ExpandMaps& maps, const ExpandTcArgs& a, cudaStr
       best = g;
     }
   }
-  return launch_pdl(lora_expand_tc_kernel<F32>, dim3(best, tiles), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st, maps, a);
+  return launch_pdl(lora_expand_tc_kernel<F32, EW>, dim3(best, tiles), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st, maps, a);
 }
 
 }  // namespace
@@ -748,7 +755,8 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
       (y && !map_2d(&maps.y, type, y, t.D, M, (uint64_t)ldy * elt, 128 / elt, kTok, true)))
     return cudaErrorInvalidValue;
   const ExpandTcArgs a{t, ids, M, splits, y != nullptr, y == out, p, s, header};
-  return f32 ? launch_expand<true>(maps, a, st) : launch_expand<false>(maps, a, st);
+  if (t.rp <= 32) return f32 ? launch_expand<true, 5>(maps, a, st) : launch_expand<false, 5>(maps, a, st);
+  return f32 ? launch_expand<true, 3>(maps, a, st) : launch_expand<false, 3>(maps, a, st);
 }
 
 }  // namespace aq
