@@ -23,14 +23,18 @@
 //   warp 1       allocates tensor memory; one lane issues tcgen05.mma (kind::f16,
 //                M = 128, N = NT, K = 16) four times per step
 //   warp 3       dY producer (TMA, 128-byte swizzle), after the previous kernel
-//   warps 4-11   transform: codes -> sw q in bf16 -> the swizzled A stage
-//   warps 12-15  epilogue: tensor memory -> add -> dx, while the next unit runs in
+//   warps 4-15   transform: codes -> sw q in bf16 -> the swizzled A stage, in three
+//                groups of four warps that take every third step (one step's chain of
+//                waits and latencies is longer than its MMAs)
+//   warps 16-19  epilogue: tensor memory -> add -> dx, while the next unit runs in
 //                the other accumulator buffer
 // The weights are read before the previous kernel has finished; dY, add, dx and
 // the workspace are not touched before.
 //
-// Few units (short sequences): the range of n is split, partial sums go to the
-// workspace, and a second launch adds them in split order.  (Summed by the unit's
+// Whole units go to the CTAs as long as every CTA gets one; the units that are left
+// (all of them for short sequences) are split over n so that they fill the GPU once
+// more, their partial sums go to the workspace, and a second launch adds them in
+// split order.  (Summed by the unit's
 // last CTA instead, 77 x 2560 x 1088 took 60 us: one CTA's loads wait for one
 // another, a grid's do not.)
 // Every wait is bounded, as in tc_linear_kernel.
@@ -46,8 +50,8 @@ namespace {
 constexpr int kStep = 64;       // rows n per step
 constexpr int kRawSlots = 3;    // ring of packed codes and scales
 constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 scales
-constexpr int kXfWarp0 = 4, kXfWarps = 8, kXfThreads = 32 * kXfWarps;
-constexpr int kEpiWarp0 = kXfWarp0 + kXfWarps, kEpiWarps = 4;
+constexpr int kXfWarp0 = 4, kXfGroups = 3, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
+constexpr int kEpiWarp0 = kXfWarp0 + kXfGroups * kXfWarps, kEpiWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kMaxBwdSplits = 16;
 
@@ -75,40 +79,45 @@ struct BwdArgs {
   const int32_t* tile_idx;
   const uint16_t* scales;
   int N, K, bN, C, T4, T8;
-  int M, ntb, S, units, steps;  // steps of the whole range: N / 64
+  int M, ntb, steps;   // steps of a unit: N / 64
+  int whole, S, units;  // units done whole, splits of the others, work items in all
   const void* add;
   void* dx;
   int ldadd, lddx, f32;
   void* ws;
-  float* partial;  // [S][M][K]
+  float* partial;  // [split work item][NT][128]
 };
 
 struct BwdUnit {
-  int kb, tb, s, i0, i1;
+  int kb, tb, i0, i1;
+  int part;  // index among the split work items, or -1
 };
 
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   BwdUnit x;
-  x.s = u % a.S;
-  const int rest = u / a.S;
-  x.tb = rest % a.ntb;
-  x.kb = rest / a.ntb;
-  x.i0 = (int)((long long)a.steps * x.s / a.S);
-  x.i1 = (int)((long long)a.steps * (x.s + 1) / a.S);
+  x.part = u - a.whole;
+  x.i0 = 0;
+  x.i1 = a.steps;
+  if (x.part >= 0) {
+    const int s = x.part % a.S;
+    u = a.whole + x.part / a.S;
+    x.i0 = (int)((long long)a.steps * s / a.S);
+    x.i1 = (int)((long long)a.steps * (s + 1) / a.S);
+  }
+  x.tb = u % a.ntb;
+  x.kb = u / a.ntb;
   return x;
 }
 
-// Four codes (two's-complement bytes) times sw, as two bf16 pairs.
-// A byte b = q + 128 in the low mantissa bits of 2^23 is 8388608 + b exactly.
-__device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw) {
+// Four codes (two's-complement bytes) times sw, as two bf16 pairs.  The byte
+// b = q + 128 in the middle of a mantissa is 32768 + b, and 32896 sw is exact (9 + 11
+// bits), so one fused multiply-add gives sw q exactly, which is then rounded once.
+__device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw, float2 off) {
   const uint32_t x = w ^ 0x80808080u;
-  const float2 bias = make_float2(-8388736.f, -8388736.f);
-  float2 p = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440)),
-                         __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441)));
-  float2 q = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442)),
-                         __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443)));
-  p = __fmul2_rn(__fadd2_rn(p, bias), sw);
-  q = __fmul2_rn(__fadd2_rn(q, bias), sw);
+  const float2 p = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7604)),
+                                          __uint_as_float(__byte_perm(x, 0x47000000u, 0x7614))), sw, off);
+  const float2 q = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7624)),
+                                          __uint_as_float(__byte_perm(x, 0x47000000u, 0x7634))), sw, off);
   const __nv_bfloat162 a = __floats2bfloat162_rn(p.x, p.y), b = __floats2bfloat162_rn(q.x, q.y);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
@@ -290,45 +299,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ transform
     // 8 codes of one row per thread and round: 16 threads cover a row, so that
     // a quarter warp writes the eight 16-byte chunks of one 128-byte row.
-    const int t = threadIdx.x - 32 * kXfWarp0, c = t & 15, r0 = t >> 4;
+    const int t = (threadIdx.x - 32 * kXfWarp0) % kXfThreads, group = (warp - kXfWarp0) / kXfWarps;
+    const int c = t & 15, r0 = t >> 4;
     Ring sr{0, 0}, rr{0, 0};
     bool ok = true;
+    int turn = 0;
     for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
       const BwdUnit x = bwd_unit(a, u);
       for (int i = x.i0; i < x.i1; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag) &&
-                                         mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag))) {
-          fail(5);
-          ok = false;
-          break;
-        }
-        const uint8_t* src = raw_slot(rr.i);
-        const uint16_t* scl = reinterpret_cast<const uint16_t*>(src + kStep * kTileK);
-        uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kStep * 128);
-        const bool is4 = raw_int4[rr.i];
-#pragma unroll
-        for (int k = 0; k < kStep / 16; ++k) {
-          const int r = r0 + 16 * k;
-          float s = __half2float(__ushort_as_half(scl[r]));
-          uint2 v;
-          if (is4) {  // nibbles as 16 q: see tc_linear.cu
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * (kTileK / 2) + c * 4);
-            const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
-            v = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
-            s *= 0.0625f;
-          } else {
-            v = *reinterpret_cast<const uint2*>(src + r * kTileK + c * 8);
+        if (turn == group) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag) &&
+                                           mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag))) {
+            fail(5);
+            ok = false;
+            break;
           }
-          const float2 s2 = make_float2(s, s);
-          const uint2 e0 = codes4(v.x, s2), e1 = codes4(v.y, s2);
-          *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+          const uint8_t* src = raw_slot(rr.i);
+          const uint16_t* scl = reinterpret_cast<const uint16_t*>(src + kStep * kTileK);
+          uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kStep * 128);
+          const bool is4 = raw_int4[rr.i];
+#pragma unroll
+          for (int k = 0; k < kStep / 8; ++k) {
+            const int r = r0 + 8 * k;
+            float s = __half2float(__ushort_as_half(scl[r]));
+            uint2 v;
+            if (is4) {  // nibbles as 16 q: see tc_linear.cu
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * (kTileK / 2) + c * 4);
+              const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
+              v = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+              s *= 0.0625f;
+            } else {
+              v = *reinterpret_cast<const uint2*>(src + r * kTileK + c * 8);
+            }
+            const float o = -32896.f * s;
+            const float2 s2 = make_float2(s, s), o2 = make_float2(o, o);
+            const uint2 e0 = codes4(v.x, s2, o2), e1 = codes4(v.y, s2, o2);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&a_full[sr.i]);
+            mbar_arrive(&raw_empty[rr.i]);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&a_full[sr.i]);
-          mbar_arrive(&raw_empty[rr.i]);
-        }
+        turn = turn == kXfGroups - 1 ? 0 : turn + 1;
         sr.template next<S_>();
         rr.template next<kRawSlots>();
       }
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("" : "+r"(v[e]));
           const int m = m0 + c0 + e;
           if (m < a.M) {
-            if (a.S > 1) __stcg(a.partial + ((size_t)x.s * a.M + m) * a.K + k, __uint_as_float(v[e]));
+            if (x.part >= 0) __stcg(a.partial + ((size_t)x.part * NT + c0 + e) * kTileK + kcol, __uint_as_float(v[e]));
             else put(m, k, __uint_as_float(v[e]));
           }
         }
@@ -387,15 +402,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// dx = add + the partial sums, splits in increasing order; four columns a thread.
-__global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs a) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = a.K / 4;
+// dx = add + the partial sums of the split units, splits in increasing order; four
+// columns of a token per thread, blockIdx.y the split unit.
+__global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs a, int nt) {
+  const int i = blockIdx.x * 256 + threadIdx.x, c = i / (kTileK / 4), u = a.whole + blockIdx.y;
+  const int m = u % a.ntb * nt + c, k = u / a.ntb * kTileK + i % (kTileK / 4) * 4;
   pdl_launch_dependents();
   pdl_wait();
-  if (i >= a.M * per) return;
-  const int m = (int)(i / per), k = (int)(i - m * per) * 4;
-  const float4* p = reinterpret_cast<const float4*>(a.partial + (size_t)m * a.K + k);
-  const size_t step = (size_t)a.M * a.K / 4;
+  if (c >= nt || m >= a.M) return;
+  const float4* p = reinterpret_cast<const float4*>(a.partial) + (size_t)blockIdx.y * a.S * nt * (kTileK / 4) + i;
+  const size_t step = (size_t)nt * (kTileK / 4);
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int s = 0; s < a.S; ++s) {
@@ -430,23 +446,31 @@ __global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs 
 
 // ---------------------------------------------------------------- host side
 struct BwdPlan {
-  int nt, ntb, S;
+  int nt, ntb;
+  long long whole;  // units done whole
+  int rest, S;      // units that are split, and their splits
 };
 
-// Token-block width and splits.  A step takes the longer of the MMAs (2 NT
-// cycles) and the dequantization; whole units go to the CTAs in waves.
+// Token-block width and splits.  A step takes the longer of the MMAs (2 NT cycles)
+// and what does not depend on NT (about 400: measured).
 BwdPlan plan_bwd(int M, int N, int C) {
   const int sms = num_sms(), steps = N / kStep;
-  BwdPlan best{0, 0, 1};
+  BwdPlan best{0, 0, 0, 0, 1};
   long long best_cost = 0;
   for (int nt : {32, 64, 128, 192, 256}) {
     const int ntb = (M + nt - 1) / nt;
-    const long long blocks = (long long)C * ntb;
-    const int S = (int)std::max<long long>(1, std::min<long long>({sms / blocks, (long long)steps / 4, kMaxBwdSplits}));
-    const long long waves = (blocks * S + sms - 1) / sms;
-    const long long cost = waves * ((steps + S - 1) / S + 4) * std::max(2 * nt, 400);
+    const long long units = (long long)C * ntb;
+    BwdPlan p{nt, ntb, units / sms * sms, (int)(units % sms), 1};
+    if (p.rest > 0) p.S = std::max(1, std::min({sms / p.rest, steps / 4, kMaxBwdSplits}));
+    long long path = p.whole / sms * (long long)(steps + 2);
+    if (p.rest > 0) path += (steps + p.S - 1) / p.S + 4 + (p.S > 1 ? 6 : 0);
+    if (p.S == 1) {  // nothing to split
+      p.whole = units;
+      p.rest = 0;
+    }
+    const long long cost = path * std::max(2 * nt, 400);
     if (best.nt == 0 || cost < best_cost) {
-      best = {nt, ntb, S};
+      best = p;
       best_cost = cost;
     }
   }
@@ -481,7 +505,7 @@ using namespace aq;
 extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) {
   if (validate_packed(w) != AQ_OK || M < 1 || M > kMaxBwdTokens) return 0;
   const BwdPlan p = plan_bwd(M, w->N, w->C);
-  return kWsHeader + (p.S > 1 ? (size_t)p.S * M * w->K * sizeof(float) : 0);
+  return kWsHeader + (size_t)p.rest * p.S * p.nt * kTileK * sizeof(float);
 }
 
 extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
@@ -501,8 +525,9 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   a.bitmap = w->bitmap; a.tile_idx = w->tile_idx; a.scales = w->scales;
   a.N = w->N; a.K = w->K; a.bN = w->bN; a.C = w->C; a.T4 = w->T4; a.T8 = w->T8;
   a.M = M; a.ntb = p.ntb; a.S = p.S; a.steps = w->N / kStep;
-  if ((long long)w->C * p.ntb * p.S > 0x7FFFFFFFll) return AQ_ERR_ARG;
-  a.units = w->C * p.ntb * p.S;
+  if (p.whole > 0x7FFF0000ll) return AQ_ERR_ARG;
+  a.whole = (int)p.whole;
+  a.units = a.whole + p.rest * p.S;
   a.add = add; a.dx = dx; a.ldadd = ldadd; a.lddx = lddx; a.f32 = dxdtype == AQ_F32;
   a.ws = ws;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
@@ -515,9 +540,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
     case 192: e = launch_bwd<192>(w, dy, ldd, a, st); break;
     case 256: e = launch_bwd<256>(w, dy, ldd, a, st); break;
   }
-  if (e == cudaSuccess && p.S > 1) {
-    const long long blocks = ((long long)M * (w->K / 4) + 255) / 256;
-    e = launch_pdl(linear_backward_sum_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a);
-  }
+  if (e == cudaSuccess && p.rest > 0)
+    e = launch_pdl(linear_backward_sum_kernel, dim3((p.nt * (kTileK / 4) + 255) / 256, p.rest), dim3(256), 0, st, a, p.nt);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

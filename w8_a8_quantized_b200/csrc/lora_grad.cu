@@ -19,8 +19,8 @@
 // sums 512 tokens at a time; the epilogue adds those sums in fp32 registers,
 // rounding to nearest.  Partial sums of the ranges are added in range order.
 //
-// Roles: warp 0 codes (TMA), warp 1 tensor memory and MMA, warp 2 terms and bf16
-// activations (TMA), warps 4-7 codes -> bf16 and the clearing, warps 8-11 epilogue.
+// Roles: warp 0 codes or bf16 activations (TMA), warp 1 tensor memory and MMA, warp 2
+// terms (TMA), warps 4-7 codes -> bf16 and the clearing, warps 8-11 epilogue.
 // Every wait is bounded; one that gives up is recorded in the workspace.
 #include <algorithm>
 #include <cstring>
@@ -121,14 +121,16 @@ template <int NB, bool CODES>
 struct GradShape {
   static constexpr int kRanks = NB / 3;
   static constexpr int kAtoms = (NB + 63) / 64;       // 64 terms x 64 tokens, 8 KiB each
-  static constexpr int kA = kTok * kD * 2, kB = kAtoms * 8192, kStage = kA + kB;
+  static constexpr int kA = kTok * kD * 2, kB = kAtoms * 8192;
   // two CTAs per SM up to 32 ranks: a CTA's start and end are then covered by the other
   static constexpr int kPerSm = NB <= 96 ? 2 : 1;
-  static constexpr int kStages = NB <= 48 ? 3 : NB <= 96 ? (CODES ? 2 : 3) : 4;
-  static constexpr int kRaw = CODES ? 3 : 0;          // ring of codes, 8 KiB each
+  // rings: activations in bf16 (filled from the codes, or by TMA), terms, codes
+  static constexpr int kSA = CODES ? (NB <= 96 ? 2 : 3) : NB <= 48 ? 4 : NB <= 96 ? 3 : 4;
+  static constexpr int kSB = NB <= 48 ? (CODES ? 6 : 4) : NB <= 96 ? 3 : 5;
+  static constexpr int kRaw = CODES ? (NB <= 96 ? 3 : 5) : 0;  // 8 KiB each
   static constexpr int kTmem = 2 * NB <= 128 ? 128 : 2 * NB <= 256 ? 256 : 512;
   static constexpr int kCtrl = 512 + kThreads * 2 + kMaxAdapters / 8;
-  static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kTok * kD + kCtrl;
+  static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kTok * kD + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
   static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
   static_assert(kPerSm * kTmem <= 512, "tensor memory");
@@ -167,19 +169,21 @@ template <int NB, bool CODES>
 __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     lora_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs a) {
   using Sh = GradShape<NB, CODES>;
-  constexpr int S_ = Sh::kStages, RW = CODES ? Sh::kRaw : 1;
+  constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = CODES ? Sh::kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  auto stage_a = [&](int st) { return smem + st * Sh::kStage; };
-  auto stage_b = [&](int st) { return smem + st * Sh::kStage + Sh::kA; };
-  auto raw_slot = [&](int s) { return smem + S_ * Sh::kStage + s * kTok * kD; };
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S_ * Sh::kStage + Sh::kRaw * kTok * kD);
+  auto stage_a = [&](int st) { return smem + st * Sh::kA; };
+  auto stage_b = [&](int st) { return smem + SA * Sh::kA + st * Sh::kB; };
+  auto raw_slot = [&](int s) { return smem + SA * Sh::kA + SB * Sh::kB + s * kTok * kD; };
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + SA * Sh::kA + SB * Sh::kB + Sh::kRaw * kTok * kD);
   uint64_t* raw_empty = raw_full + RW;
   uint64_t* a_full = raw_empty + RW;   // transform warps done with the stage
-  uint64_t* b_full = a_full + S_;      // terms (and bf16 activations) landed
-  uint64_t* done = b_full + S_;        // the stage's MMAs are complete
-  uint64_t* acc_full = done + S_;
+  uint64_t* a_tma = a_full + SA;       // bf16 activations landed
+  uint64_t* a_done = a_tma + SA;       // the stage's MMAs are complete
+  uint64_t* b_full = a_done + SA;      // terms landed
+  uint64_t* b_done = b_full + SB;
+  uint64_t* acc_full = b_done + SB;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -211,10 +215,14 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kXf);
     }
-    for (int i = 0; i < S_; ++i) {
+    for (int i = 0; i < SA; ++i) {
       mbar_init(&a_full[i], kXf);
+      mbar_init(&a_tma[i], 1);
+      mbar_init(&a_done[i], 1);
+    }
+    for (int i = 0; i < SB; ++i) {
       mbar_init(&b_full[i], 1);
-      mbar_init(&done[i], 1);
+      mbar_init(&b_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     record_error(a.ws, AQ_ERR_TIMEOUT, info, 0);
   };
 
-  Ring sr{0, 0}, rr{0, 0}, ar{0, 0};  // stage, raw slot, accumulator
+  Ring sr{0, 0}, br{0, 0}, rr{0, 0}, ar{0, 0};  // activations, terms, codes, accumulator
   bool ok = true, issued = false;
 
   for (int l = 0; l < a.L; ++l) {
@@ -275,18 +283,27 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     __syncthreads();
     const int base = c0;
 
-    if (warp == 0 && CODES) {
-      // ------------------------------------------------------------ codes
+    if (warp == 0) {
+      // ------------------------------------------------------------ codes, or bf16 activations
       if (lane == 0) {
         for (int i = 0; ok && i < n; ++i) {
-          if (!mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag)) {
+          const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
+          if (!(CODES ? mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag)
+                      : mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag))) {
             fail(21);
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&raw_full[rr.i], kTok * kD);
-          tma_load_2d(raw_slot(rr.i), &maps.x, d0, (base + (list[i] & 0x7FFF)) * kTok, &raw_full[rr.i]);
-          rr.template next<RW>();
+          if (CODES) {
+            mbar_arrive_expect_tx(&raw_full[rr.i], kTok * kD);
+            tma_load_2d(raw_slot(rr.i), &maps.x, d0, m0, &raw_full[rr.i]);
+            rr.template next<RW>();
+          } else {
+            mbar_arrive_expect_tx(&a_tma[sr.i], Sh::kA);
+            tma_load_2d(stage_a(sr.i), &maps.x, d0, m0, &a_tma[sr.i]);
+            tma_load_2d(stage_a(sr.i) + 8192, &maps.x, d0 + 64, m0, &a_tma[sr.i]);
+            sr.template next<SA>();
+          }
         }
       }
     } else if (warp == 1) {
@@ -299,20 +316,22 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
             ok = false;
             break;
           }
-          if (!mbar_wait(&b_full[sr.i], sr.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
+          if (!mbar_wait(&b_full[br.i], br.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag) ||
+              (!CODES && !mbar_wait(&a_tma[sr.i], sr.ph, abort_flag))) {
             fail(23);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t off = (uint64_t)((sr.i * Sh::kStage) >> 4);
+          const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of eight rows
-            mma_bf16(tmem_base + ar.i * NB, adesc0 + off + 128 * k, bdesc0 + off + 128 * k, Sh::kIdesc,
-                     i % kUnit > 0 || k > 0);
-          mma_commit(&done[sr.i]);
+            mma_bf16(tmem_base + ar.i * NB, ao + 128 * k, bo + 128 * k, Sh::kIdesc, i % kUnit > 0 || k > 0);
+          mma_commit(&a_done[sr.i]);
+          mma_commit(&b_done[br.i]);
           issued = true;
-          sr.template next<S_>();
+          sr.template next<SA>();
+          br.template next<SB>();
           if (i % kUnit == kUnit - 1 || i + 1 == n) {
             mma_commit(&acc_full[ar.i]);
             ar.template next<2>();
@@ -320,24 +339,19 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
         }
       }
     } else if (warp == 2) {
-      // ------------------------------------------------------------ terms, bf16 activations
+      // ------------------------------------------------------------ terms
       if (lane == 0) {
         for (int i = 0; ok && i < n; ++i) {
-          if (!mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag)) {
+          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag)) {
             fail(24);
             ok = false;
             break;
           }
-          const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
-          mbar_arrive_expect_tx(&b_full[sr.i], Sh::kB + (CODES ? 0 : Sh::kA));
+          mbar_arrive_expect_tx(&b_full[br.i], Sh::kB);
 #pragma unroll
           for (int c = 0; c < Sh::kAtoms; ++c)
-            tma_load_2d(stage_b(sr.i) + c * 8192, &maps.terms, 64 * c, m0, &b_full[sr.i]);
-          if (!CODES) {
-            tma_load_2d(stage_a(sr.i), &maps.x, d0, m0, &b_full[sr.i]);
-            tma_load_2d(stage_a(sr.i) + 8192, &maps.x, d0 + 64, m0, &b_full[sr.i]);
-          }
-          sr.template next<S_>();
+            tma_load_2d(stage_b(br.i) + c * 8192, &maps.terms, 64 * c, (base + (list[i] & 0x7FFF)) * kTok, &b_full[br.i]);
+          br.template next<SB>();
         }
       }
     } else if (warp >= 4 && warp < 4 + kXf) {
@@ -346,9 +360,10 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       for (int i = 0; ok && i < n; ++i) {
         const bool mixed = list[i] & 0x8000;
         const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
-        bool got = mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag);
+        bool got = mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag);
         if (CODES) got = got && mbar_wait(&raw_full[rr.i], rr.ph, abort_flag);
-        if (mixed) got = got && mbar_wait(&b_full[sr.i], sr.ph, abort_flag);
+        if (mixed) got = got && mbar_wait(&b_full[br.i], br.ph, abort_flag);
+        if (mixed && !CODES) got = got && mbar_wait(&a_tma[sr.i], sr.ph, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           fail(25);
           ok = false;
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
             const uint4 zero = make_uint4(0, 0, 0, 0);
             for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stage_a(sr.i) + half * 8192 + r * 128 + q * 16) = zero;
             for (int q = half; q < 8 * Sh::kAtoms; q += 2)
-              *reinterpret_cast<uint4*>(stage_b(sr.i) + (q >> 3) * 8192 + r * 128 + (q & 7) * 16) = zero;
+              *reinterpret_cast<uint4*>(stage_b(br.i) + (q >> 3) * 8192 + r * 128 + (q & 7) * 16) = zero;
           }
         }
         if (CODES || mixed) fence_proxy_async_smem();
@@ -382,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
           mbar_arrive(&a_full[sr.i]);
           if (CODES) mbar_arrive(&raw_empty[rr.i]);
         }
-        sr.template next<S_>();
+        sr.template next<SA>();
+        br.template next<SB>();
         if (CODES) rr.template next<RW>();
       }
     } else if (warp >= 4 + kXf) {
@@ -501,7 +517,8 @@ int grad_splits(int M, int D) {
   int best = least;
   long long cost = 0;
   for (int s = least; s <= std::max(least, std::min(chunks, 16)); ++s) {
-    const long long c = (long long)ceil_div((long long)blocks * s, slots) * (ceil_div(chunks, s) + 10);
+    // (a launch for the sum counts as eight)
+    const long long c = (long long)ceil_div((long long)blocks * s, slots) * (ceil_div(chunks, s) + 10) + (s > 1 ? 8 : 0);
     if (cost == 0 || c < cost) {
       cost = c;
       best = s;
