@@ -48,7 +48,6 @@ namespace aq {
 namespace {
 
 constexpr int kStep = 64;       // rows n per step
-constexpr int kRawSlots = 3;    // ring of packed codes and scales
 constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 scales
 constexpr int kXfWarp0 = 4, kXfGroups = 3, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
 constexpr int kEpiWarp0 = kXfWarp0 + kXfGroups * kXfWarps, kEpiWarps = 4;
@@ -57,17 +56,18 @@ constexpr int kMaxBwdSplits = 16;
 
 template <int NT>
 struct BwdShape {
-  static constexpr int kA = kStep * kTileK * 2;  // W' stage: two 64-column halves of 64 rows x 128 bytes
-  static constexpr int kB = NT * kStep * 2;      // dY stage: NT rows x 128 bytes
-  static constexpr int kStage = kA + kB;
-  static constexpr int kStages = 196608 / kStage < 6 ? 196608 / kStage : 6;
+  static constexpr int kA = kStep * kTileK * 2;  // W' slot: two 64-column halves of 64 rows x 128 bytes
+  static constexpr int kB = NT * kStep * 2;      // dY slot: NT rows x 128 bytes
+  // Rings of W', dY and packed codes.  Copies take 1 to 1.5 us to land, as long as two
+  // to four steps: codes and dY each need that many slots on their way.
+  static constexpr int kSA = NT <= 128 ? 4 : 3, kSB = NT <= 128 ? 6 : 4, kRaw = NT <= 128 ? 7 : 6;
   static constexpr int kTmemCols = 2 * NT <= 32 ? 32 : 2 * NT <= 64 ? 64 : 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
   static constexpr int kCtrl = 512;
-  static constexpr int kSmem = 1024 + kStages * kStage + kRawSlots * kRawBytes + kCtrl;
+  static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kRawBytes + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NT, true, false);
   static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
-  static_assert(kStages >= 3 && kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
-  static_assert((2 * kRawSlots + 3 * kStages + 4 + 1) * 8 + kRawSlots * 4 + 3 * 4 <= kCtrl, "control area");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert((2 * kRaw + 2 * kSA + 2 * kSB + 4 + 1) * 8 + kRaw * 4 + 3 * 4 <= kCtrl, "control area");
 };
 
 struct BwdMaps {
@@ -126,36 +126,40 @@ template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_backward_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
   using Sh = BwdShape<NT>;
-  constexpr int S_ = Sh::kStages;
+  constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = Sh::kRaw;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  auto stage_a = [&](int st) { return smem + st * Sh::kStage; };
-  auto stage_b = [&](int st) { return smem + st * Sh::kStage + Sh::kA; };
-  auto raw_slot = [&](int sl) { return smem + S_ * Sh::kStage + sl * kRawBytes; };
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S_ * Sh::kStage + kRawSlots * kRawBytes);
-  uint64_t* raw_empty = raw_full + kRawSlots;
-  uint64_t* a_full = raw_empty + kRawSlots;  // transform warps done with the stage
-  uint64_t* b_full = a_full + S_;            // dY landed
-  uint64_t* done = b_full + S_;              // the stage's MMAs are complete
-  uint64_t* acc_full = done + S_;
+  auto stage_a = [&](int i) { return smem + i * Sh::kA; };
+  auto stage_b = [&](int i) { return smem + SA * Sh::kA + i * Sh::kB; };
+  auto raw_slot = [&](int i) { return smem + SA * Sh::kA + SB * Sh::kB + i * kRawBytes; };
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw_slot(RW));
+  uint64_t* raw_empty = raw_full + RW;
+  uint64_t* a_full = raw_empty + RW;   // transform warps done with the slot
+  uint64_t* a_done = a_full + SA;      // the slot's MMAs are complete
+  uint64_t* b_full = a_done + SA;      // dY landed
+  uint64_t* b_done = b_full + SB;
+  uint64_t* acc_full = b_done + SB;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   volatile uint32_t* raw_int4 = reinterpret_cast<volatile uint32_t*>(drain + 1);
-  uint32_t* tmem_slot = const_cast<uint32_t*>(raw_int4 + kRawSlots);
+  uint32_t* tmem_slot = const_cast<uint32_t*>(raw_int4 + RW);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRawSlots; ++i) {
+    for (int i = 0; i < RW; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kXfWarps);
     }
-    for (int i = 0; i < S_; ++i) {
+    for (int i = 0; i < SA; ++i) {
       mbar_init(&a_full[i], kXfWarps);
+      mbar_init(&a_done[i], 1);
+    }
+    for (int i = 0; i < SB; ++i) {
       mbar_init(&b_full[i], 1);
-      mbar_init(&done[i], 1);
+      mbar_init(&b_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(dst, k ? &maps.w4 : &maps.w8, 0, (int)r, &raw_full[rr.i]);
           bulk_load(dst + kStep * kTileK, a.scales + s, kStep * 2, &raw_full[rr.i]);
         }
-        rr.next<kRawSlots>();
+        rr.template next<RW>();
       }
       row[0] = row[1];
       sc[0] = sc[1];
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kStep * 128), bdesc0 = sw128_desc(smem_u32(stage_b(0)));
-      Ring sr{0, 0};
+      Ring sr{0, 0}, br{0, 0};
       bool ok = true, any = false;
       int ui = 0;
       for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++ui) {
@@ -253,19 +257,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t d = tmem_base + buf * NT;
         for (int i = x.i0; i < x.i1; ++i) {
-          if (!mbar_wait(&b_full[sr.i], sr.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
+          if (!mbar_wait(&b_full[br.i], br.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
             fail(3);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t off = (uint64_t)((sr.i * Sh::kStage) >> 4);
+          const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
 #pragma unroll
           for (int k = 0; k < kStep / 16; ++k)  // 16 rows: two groups of A, 32 bytes of B
-            mma_bf16(d, adesc0 + off + 128 * k, bdesc0 + off + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
-          mma_commit(&done[sr.i]);
+            mma_bf16(d, ao + 128 * k, bo + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
+          mma_commit(&a_done[sr.i]);
+          mma_commit(&b_done[br.i]);
           any = true;
-          sr.template next<S_>();
+          sr.template next<SA>();
+          br.template next<SB>();
         }
         if (ok) mma_commit(&acc_full[buf]);
       }
@@ -278,19 +284,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ dY producer
     if (lane == 0) {
       pdl_wait();
-      Ring sr{0, 0};
+      Ring br{0, 0};
       bool ok = true;
       for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
         const BwdUnit x = bwd_unit(a, u);
         for (int i = x.i0; i < x.i1; ++i) {
-          if (!mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag)) {
+          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag)) {
             fail(4);
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&b_full[sr.i], Sh::kB);
-          tma_load_2d(stage_b(sr.i), &maps.dy, i * kStep, x.tb * NT, &b_full[sr.i]);
-          sr.template next<S_>();
+          mbar_arrive_expect_tx(&b_full[br.i], Sh::kB);
+          tma_load_2d(stage_b(br.i), &maps.dy, i * kStep, x.tb * NT, &b_full[br.i]);
+          br.template next<SB>();
         }
       }
       if (!ok || *abort_flag) grace();
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = x.i0; i < x.i1; ++i) {
         if (turn == group) {
           if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag) &&
-                                           mbar_wait(&done[sr.i], sr.ph ^ 1u, abort_flag))) {
+                                           mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag))) {
             fail(5);
             ok = false;
             break;
@@ -344,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         turn = turn == kXfGroups - 1 ? 0 : turn + 1;
-        sr.template next<S_>();
-        rr.template next<kRawSlots>();
+        sr.template next<SA>();
+        rr.template next<RW>();
       }
     }
   } else if (warp >= kEpiWarp0) {
