@@ -303,10 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kXfWarp0 && warp < kEpiWarp0) {
     // ------------------------------------------------------------ transform
-    // 8 codes of one row per thread and round: 16 threads cover a row, so that
-    // a quarter warp writes the eight 16-byte chunks of one 128-byte row.
+    // 16 codes of one row per thread and round, eight threads a row, rows 16 apart: a
+    // thread's chunks sit at fixed offsets, and its row scale serves 16 codes.  Threads
+    // of the second 64 columns write their two chunks in the other order, so that the
+    // eight threads of a row always write eight different 16-byte columns.
     const int t = (threadIdx.x - 32 * kXfWarp0) % kXfThreads, group = (warp - kXfWarp0) / kXfWarps;
-    const int c = t & 15, r0 = t >> 4;
+    const int c = t & 7, r0 = t >> 3, late = c >> 2;
+    const int first = late * (kStep * 128) + r0 * 128 + (((2 * (c & 3) + late) ^ (r0 & 7)) << 4);
+    const int second = late * (kStep * 128) + r0 * 128 + (((2 * (c & 3) + 1 - late) ^ (r0 & 7)) << 4);
     Ring sr{0, 0}, rr{0, 0};
     bool ok = true;
     int turn = 0;
@@ -322,25 +326,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint8_t* src = raw_slot(rr.i);
           const uint16_t* scl = reinterpret_cast<const uint16_t*>(src + kStep * kTileK);
-          uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kStep * 128);
-          const bool is4 = raw_int4[rr.i];
-#pragma unroll
-          for (int k = 0; k < kStep / 8; ++k) {
-            const int r = r0 + 8 * k;
-            float s = __half2float(__ushort_as_half(scl[r]));
-            uint2 v;
-            if (is4) {  // nibbles as 16 q: see tc_linear.cu
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(src + r * (kTileK / 2) + c * 4);
-              const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;
-              v = make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
-              s *= 0.0625f;
-            } else {
-              v = *reinterpret_cast<const uint2*>(src + r * kTileK + c * 8);
-            }
+          uint8_t* dst = stage_a(sr.i);
+          auto put = [&](int k, uint4 v, float s) {
             const float o = -32896.f * s;
             const float2 s2 = make_float2(s, s), o2 = make_float2(o, o);
-            const uint2 e0 = codes4(v.x, s2, o2), e1 = codes4(v.y, s2, o2);
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(e0.x, e0.y, e1.x, e1.y);
+            const uint2 e0 = codes4(v.x, s2, o2), e1 = codes4(v.y, s2, o2), e2 = codes4(v.z, s2, o2), e3 = codes4(v.w, s2, o2);
+            const uint4 lo = make_uint4(e0.x, e0.y, e1.x, e1.y), hi = make_uint4(e2.x, e2.y, e3.x, e3.y);
+            *reinterpret_cast<uint4*>(dst + first + k * 2048) = late ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + second + k * 2048) = late ? lo : hi;
+          };
+          if (raw_int4[rr.i]) {
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k) {  // nibbles as 16 q: see tc_linear.cu
+              const uint2 w = *reinterpret_cast<const uint2*>(src + (r0 + 16 * k) * (kTileK / 2) + c * 8);
+              const uint32_t l0 = (w.x << 4) & 0xF0F0F0F0u, h0 = w.x & 0xF0F0F0F0u;
+              const uint32_t l1 = (w.y << 4) & 0xF0F0F0F0u, h1 = w.y & 0xF0F0F0F0u;
+              put(k, make_uint4(__byte_perm(l0, h0, 0x5140), __byte_perm(l0, h0, 0x7362), __byte_perm(l1, h1, 0x5140),
+                                __byte_perm(l1, h1, 0x7362)),
+                  __half2float(__ushort_as_half(scl[r0 + 16 * k])) * 0.0625f);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k)
+              put(k, *reinterpret_cast<const uint4*>(src + (r0 + 16 * k) * kTileK + c * 16),
+                  __half2float(__ushort_as_half(scl[r0 + 16 * k])));
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -360,15 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const size_t kcol = 32 * quad + lane;
     pdl_wait();
     int ui = 0;
-    auto put = [&](int m, size_t k, float v) {
-      if (a.f32) {
-        if (a.add) v += static_cast<const float*>(a.add)[(size_t)m * a.ldadd + k];
-        static_cast<float*>(a.dx)[(size_t)m * a.lddx + k] = v;
-      } else {
-        if (a.add) v += bf16_bits_to_float(static_cast<const uint16_t*>(a.add)[(size_t)m * a.ldadd + k]);
-        static_cast<__nv_bfloat16*>(a.dx)[(size_t)m * a.lddx + k] = __float2bfloat16_rn(v);
-      }
-    };
     for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++ui) {
       const BwdUnit x = bwd_unit(a, u);
       const int buf = ui & 1, m0 = x.tb * NT;
@@ -379,20 +379,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT;
-      for (int c0 = 0; c0 < NT; c0 += 16) {
-        if (m0 + c0 >= a.M) break;
+      // a lane holds one column k of every token: a warp's stores cover 32 columns
+      float* fp = x.part >= 0 ? a.partial + (size_t)x.part * NT * kTileK + kcol
+                              : static_cast<float*>(a.dx) + (size_t)m0 * a.lddx + k;
+      __nv_bfloat16* bp = static_cast<__nv_bfloat16*>(a.dx) + (size_t)m0 * a.lddx + k;
+      const size_t fld = x.part >= 0 ? kTileK : a.lddx;
+      const bool f32 = a.f32 || x.part >= 0, add = a.add && x.part < 0;
+      const int cols = min(NT, a.M - m0);
+      for (int c0 = 0; c0 < cols; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(taddr + c0, v);
+        float y[16];
+        if (add)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (c0 + e < cols)
+              y[e] = a.f32 ? static_cast<const float*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]
+                           : bf16_bits_to_float(static_cast<const uint16_t*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           asm volatile("" : "+r"(v[e]));
-          const int m = m0 + c0 + e;
-          if (m < a.M) {
-            if (x.part >= 0) __stcg(a.partial + ((size_t)x.part * NT + c0 + e) * kTileK + kcol, __uint_as_float(v[e]));
-            else put(m, k, __uint_as_float(v[e]));
-          }
+          if (add && c0 + e < cols) v[e] = __float_as_uint(__uint_as_float(v[e]) + y[e]);
         }
+        const int left = cols - c0;
+        if (f32) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < left) fp[(size_t)e * fld] = __uint_as_float(v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < left) bp[(size_t)e * a.lddx] = __float2bfloat16_rn(__uint_as_float(v[e]));
+        }
+        fp += 16 * fld;
+        bp += (size_t)16 * a.lddx;
       }
       tc_fence_before();
       __syncwarp();
