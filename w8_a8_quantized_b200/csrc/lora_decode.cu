@@ -9,7 +9,9 @@
 // of the columns n of B_l^T, whose first rows are loaded before the exchange.
 // The cluster of token m serves it and the next three tokens of the same
 // adapter if an even four of them come before it, and returns otherwise.
-// Sums are fp32, in a fixed order.
+// Sums are fp32, in a fixed order.  Three CTAs fit an SM: 64 tokens of 40 adapters
+// (45 clusters) run in one wave; the code for a single token keeps twice the rows
+// on their way, which the registers of four tokens' sums leave no room for.
 #include <algorithm>
 
 #include "aq_internal.cuh"
@@ -24,7 +26,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kT = 4;          // tokens of a cluster
 constexpr int kVec = 8;        // columns of a 16-byte load
 constexpr int kWide = 32 * kVec;  // columns of a warp's load
-constexpr int kRows = 4;       // table rows in flight per warp
 
 struct DecodeArgs {
   const uint16_t* a;
@@ -91,8 +92,151 @@ __device__ __forceinline__ void put8(const DecodeArgs& a, int m, int n, const fl
   }
 }
 
+// This CTA's columns k0 .. k0 + kn of S for TT tokens: 16 lanes per table row, two
+// rows per warp and load, U loads on their way; sent to every CTA of the cluster.
+template <int TT, int U>
+__device__ __forceinline__ void contract(const DecodeArgs& a, const uint16_t* xs, uint32_t part_addr, int c, int row0,
+                                         int rank, int k0, int kn, float scale, int T) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
+  for (int r0 = 2 * warp; r0 < rank; r0 += 2 * kWarps) {
+    const int r = r0 + (lane >> 4);
+    const uint16_t* row = a.a + (size_t)(row0 + min(r, rank - 1)) * a.K + k0;
+    float acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = 0.f;
+    for (int kb = sub * kVec; kb < kn; kb += U * 16 * kVec) {
+      uint4 w[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int k = kb + i * 16 * kVec;
+        w[i] = k < kn ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int k = kb + i * 16 * kVec;
+        if (k < kn) {
+          float wf[8];
+          widen8(w[i], wf);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            if (t < T) {
+              float xf[8];
+              widen8(*reinterpret_cast<const uint4*>(xs + t * a.kslice + k), xf);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) acc[t] = fmaf(wf[e], xf[e], acc[t]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+      if (t < T && r < rank && sub < kCl)
+        store_peer(peer_smem(part_addr + (uint32_t)(((c * a.max_rank + r) * kT + t) * 4), sub), scale * acc[t]);
+    }
+  }
+}
+
+// Columns n0 .. n1 of the result for TT tokens: warps share them out by 256 columns,
+// then by rows (rgs row groups), ROWS table rows on their way, the first of them
+// during the exchange of the sums.
+template <bool F32, int TT, int ROWS>
+__device__ __forceinline__ void spread(const DecodeArgs& a, const float* part, float* sums, float* red, int row0, int rank,
+                                       int n0, int n1, const int (&tok)[kT], int T, bool keep) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ncg = max(1, (n1 - n0 + kWide - 1) / kWide);
+  const int rgs = ncg >= kWarps ? 1 : kWarps / ncg;
+  const int rg = ncg >= kWarps ? 0 : warp / ncg;
+  const bool works = rg < rgs;
+  int cg = ncg >= kWarps ? warp : warp % ncg;
+  uint4 w[ROWS];
+  auto load = [&](int r0, int n) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + i * rgs;
+      w[i] = r < rank && n < n1 ? __ldg(reinterpret_cast<const uint4*>(a.bt + (size_t)(row0 + r) * a.N + n))
+                                : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (works) load(rg, n0 + cg * kWide + lane * kVec);
+  cluster_barrier();
+  for (int i = tid; i < rank * kT; i += kThreads) {
+    float s = 0.f;
+    if (i % kT < T)
+#pragma unroll
+      for (int k = 0; k < kCl; ++k) s += part[k * a.max_rank * kT + i];
+    sums[i] = s;
+  }
+  __syncthreads();
+  if (keep)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      if (t < T)
+        for (int i = tid; i < a.max_rank; i += kThreads)
+          a.s[(size_t)tok[t] * a.max_rank + i] = i < rank ? sums[i * kT + t] : 0.f;
+  bool head = true;
+  for (; cg < ncg && works; cg += kWarps) {
+    const int n = n0 + cg * kWide + lane * kVec;
+    float acc[TT][8];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[t][e] = 0.f;
+    for (int r0 = rg; r0 < rank; r0 += ROWS * rgs) {
+      if (!head) load(r0, n);
+      head = false;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const int r = r0 + i * rgs;
+        if (r < rank) {
+          float wf[8];
+          widen8(w[i], wf);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const float s = sums[r * kT + t];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[t][e] = fmaf(s, wf[e], acc[t][e]);
+          }
+        }
+      }
+    }
+    if (rgs == 1) {
+      if (n < n1)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t < T) put8<F32>(a, tok[t], n, acc[t]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        if (t < T) {
+          float4* d = reinterpret_cast<float4*>(red + ((rg * kT + t) * ncg + cg) * kWide + lane * kVec);
+          d[0] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+          d[1] = make_float4(acc[t][4], acc[t][5], acc[t][6], acc[t][7]);
+        }
+    }
+  }
+  if (rgs > 1) {
+    __syncthreads();
+    const int vecs = ncg * 32;
+    for (int i = tid; i < T * vecs; i += kThreads) {
+      const int t = i / vecs, n = n0 + (i - t * vecs) * kVec;
+      if (n >= n1) continue;
+      float s[8] = {};
+      for (int g = 0; g < rgs; ++g) {
+        const float4* d = reinterpret_cast<const float4*>(red + (g * kT + t) * ncg * kWide + (n - n0));
+        const float4 p = d[0], q = d[1];
+        s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
+        s[4] += q.x; s[5] += q.y; s[6] += q.z; s[7] += q.w;
+      }
+      put8<F32>(a, t == 0 ? tok[0] : t == 1 ? tok[1] : t == 2 ? tok[2] : tok[3], n, s);
+    }
+  }
+}
+
 template <bool F32>
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) lora_decode_kernel(const DecodeArgs a) {
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads, 3) lora_decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint16_t* xs = reinterpret_cast<uint16_t*>(raw);                      // [kT][kslice]
   float* part = reinterpret_cast<float*>(xs + kT * a.kslice);           // [kCl][max_rank][kT]
@@ -134,8 +278,6 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) lora_dec
     if (mask) ++T;
     mask &= mask - 1;
   }
-
-  // ---- columns k0 .. k1 of A
   const int k0 = c * a.kslice, kn = max(0, min(a.kslice, a.K - k0));
 #pragma unroll
   for (int t = 0; t < kT; ++t)
@@ -145,146 +287,13 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) lora_dec
             __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)tok[t] * a.ldx + k0 + k));
   __syncthreads();
   const float scale = __ldg(a.scale + v);
-  const uint32_t part_addr = smem_u32(part);
-  for (int r0 = warp * kRows; r0 < rank; r0 += kWarps * kRows) {
-    float acc[kRows][kT];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int t = 0; t < kT; ++t) acc[r][t] = 0.f;
-#pragma unroll 2
-    for (int k = lane * kVec; k < kn; k += kWide) {
-      uint4 w[kRows];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        w[r] = r0 + r < rank ? __ldg(reinterpret_cast<const uint4*>(a.a + (size_t)(row0 + r0 + r) * a.K + k0 + k))
-                             : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        if (t < T) {
-          float xf[8];
-          widen8(*reinterpret_cast<const uint4*>(xs + t * a.kslice + k), xf);
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            float wf[8];
-            widen8(w[r], wf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[r][t] = fmaf(wf[e], xf[e], acc[r][t]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        if (t < T && r0 + r < rank) {
-          float s = acc[r][t];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane < kCl)
-            store_peer(peer_smem(part_addr + (uint32_t)(((c * a.max_rank + r0 + r) * kT + t) * 4), lane), scale * s);
-        }
-      }
-  }
-
-  // ---- columns n0 .. n1 of B^T: warps share them out by 256 columns, then by rows
-  const int ncg = max(1, (n1 - n0 + kWide - 1) / kWide);
-  const int rgs = ncg >= kWarps ? 1 : kWarps / ncg;
-  const int rg = ncg >= kWarps ? 0 : warp / ncg;
-  int cg = ncg >= kWarps ? warp : warp % ncg;
-  const bool works = rg < rgs;
-  uint4 first[kRows];  // this warp's first rows, on their way during the exchange
-  {
-    const int n = n0 + cg * kWide + lane * kVec;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int r = rg + i * rgs;
-      first[i] = works && r < rank && n < n1
-                     ? __ldg(reinterpret_cast<const uint4*>(a.bt + (size_t)(row0 + r) * a.N + n))
-                     : make_uint4(0, 0, 0, 0);
-    }
-  }
-  cluster_barrier();
-  for (int i = tid; i < rank * kT; i += kThreads) {
-    float s = 0.f;
-    if (i % kT < T)
-#pragma unroll
-      for (int k = 0; k < kCl; ++k) s += part[k * a.max_rank * kT + i];
-    sums[i] = s;
-  }
-  __syncthreads();
-  if (a.s && c == 0)
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-      if (t < T)
-        for (int i = tid; i < a.max_rank; i += kThreads)
-          a.s[(size_t)tok[t] * a.max_rank + i] = i < rank ? sums[i * kT + t] : 0.f;
-
-  bool head = true;
-  for (; cg < ncg && works; cg += kWarps) {
-    const int n = n0 + cg * kWide + lane * kVec;
-    float acc[kT][8];
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[t][e] = 0.f;
-    for (int r0 = rg; r0 < rank; r0 += kRows * rgs) {
-      uint4 w[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i * rgs;
-        w[i] = head ? first[i]
-                    : r < rank && n < n1 ? __ldg(reinterpret_cast<const uint4*>(a.bt + (size_t)(row0 + r) * a.N + n))
-                                         : make_uint4(0, 0, 0, 0);
-      }
-      head = false;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i * rgs;
-        if (r < rank) {
-          const float4 s = *reinterpret_cast<const float4*>(sums + r * kT);
-          const float sv[kT] = {s.x, s.y, s.z, s.w};
-          float wf[8];
-          widen8(w[i], wf);
-#pragma unroll
-          for (int t = 0; t < kT; ++t)
-            if (t < T)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) acc[t][e] = fmaf(sv[t], wf[e], acc[t][e]);
-        }
-      }
-    }
-    if (rgs == 1) {
-      if (n < n1)
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-          if (t < T) put8<F32>(a, tok[t], n, acc[t]);
-    } else {
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-        if (t < T) {
-          float4* d = reinterpret_cast<float4*>(red + ((rg * kT + t) * ncg + cg) * kWide + lane * kVec);
-          d[0] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-          d[1] = make_float4(acc[t][4], acc[t][5], acc[t][6], acc[t][7]);
-        }
-    }
-  }
-  if (rgs > 1) {
-    __syncthreads();
-    const int vecs = ncg * 32;
-    for (int i = tid; i < T * vecs; i += kThreads) {
-      const int t = i / vecs, n = n0 + (i - t * vecs) * kVec;
-      if (n >= n1) continue;
-      float s[8] = {};
-      for (int g = 0; g < rgs; ++g) {
-        const float4* d = reinterpret_cast<const float4*>(red + (g * kT + t) * ncg * kWide + (n - n0));
-        const float4 p = d[0], q = d[1];
-        s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
-        s[4] += q.x; s[5] += q.y; s[6] += q.z; s[7] += q.w;
-      }
-      put8<F32>(a, t == 0 ? tok[0] : t == 1 ? tok[1] : t == 2 ? tok[2] : tok[3], n, s);
-    }
+  const bool keep = a.s && c == 0;
+  if (T == 1) {
+    contract<1, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    spread<F32, 1, 8>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
+  } else {
+    contract<kT, 4>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    spread<F32, kT, 4>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
   }
 }
 
