@@ -111,6 +111,10 @@ LORA = [  # M, N, K, ranks, ids
     (1000, 1024, 4096, [16, 64, 8, 31], segment_ids(1000, 4, 5)),
     (333, 2048, 896, [24, 40], mixed_ids(333, 2, 6, none=0.5)),
     (77, 128, 128, [9], [-1] * 77),
+    # decode beyond one cluster's columns, beyond one stage of rows, and beyond the decode kernel's widest input
+    (3, 17408, 264, [33, 200], [1, 0, 1]),
+    (9, 520, 40960, [5, 24], mixed_ids(9, 2, 10)),
+    (2, 128, 41024, [12], [0, 0]),
     # many column blocks per tile, tiles of one adapter, of several and of none
     (2000, 8192, 256, [16, 40, 33], [0] * 500 + [-1] * 700 + segment_ids(300, 3, 7) + [2] * 60 + [-1] * 10 + [1] * 430),
     (1300, 4096, 4104, [64, 3, 17, 50, 8], segment_ids(1000, 5, 8) + mixed_ids(300, 5, 9)),

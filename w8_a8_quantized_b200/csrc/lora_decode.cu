@@ -3,15 +3,18 @@
 //
 // A few tokens read each adapter's rows once for next to no arithmetic, so the
 // work is a stream of table rows whose time is the latency of two dependent
-// passes.  Both run here in one cluster of eight CTAs per (adapter, up to four of
+// passes.  Both run here in one cluster of eight CTAs per (adapter, up to two of
 // its tokens): each CTA takes an eighth of the columns k of A_l, the partial sums
 // are exchanged through distributed shared memory, and each CTA takes an eighth
-// of the columns n of B_l^T, whose first rows are loaded before the exchange.
-// The cluster of token m serves it and the next three tokens of the same
-// adapter if an even four of them come before it, and returns otherwise.
-// Sums are fp32, in a fixed order.  Three CTAs fit an SM: 64 tokens of 40 adapters
-// (45 clusters) run in one wave; the code for a single token keeps twice the rows
-// on their way, which the registers of four tokens' sums leave no room for.
+// of the columns n of B_l^T.  The cluster of token m serves it and the next
+// token of the same adapter if an even number of them comes before it, and returns
+// otherwise.  Sums are fp32, in a fixed order.
+//
+// B's columns are cut into as many clusters as the GPU has room for in one wave (each
+// forms S anew, from L2): what a CTA does one row after another is what takes its time
+// (rank 64, N 9728, K 2560, one token: 12 us with one cluster, 7.8 with five).  For the
+// same reason a cluster takes two tokens of an adapter and not four, whose sums would
+// leave registers for half the rows on their way.
 #include <algorithm>
 
 #include "aq_internal.cuh"
@@ -23,9 +26,11 @@ namespace {
 constexpr int kCl = 8;         // CTAs of a cluster
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kT = 4;          // tokens of a cluster
+constexpr int kT = 2;          // tokens of a cluster
 constexpr int kVec = 8;        // columns of a 16-byte load
 constexpr int kWide = 32 * kVec;  // columns of a warp's load
+constexpr int kMaxSlice = 5120;   // columns of A in a CTA
+constexpr int kRedBytes = kWarps * kT * kWide * 4;  // sums of the row groups
 
 struct DecodeArgs {
   const uint16_t* a;
@@ -51,9 +56,8 @@ __device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void store_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -161,7 +165,8 @@ __device__ __forceinline__ void spread(const DecodeArgs& a, const float* part, f
     }
   };
   if (works) load(rg, n0 + cg * kWide + lane * kVec);
-  cluster_barrier();
+  cluster_arrive();
+  cluster_wait();
   for (int i = tid; i < rank * kT; i += kThreads) {
     float s = 0.f;
     if (i % kT < T)
@@ -230,7 +235,7 @@ __device__ __forceinline__ void spread(const DecodeArgs& a, const float* part, f
         s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
         s[4] += q.x; s[5] += q.y; s[6] += q.z; s[7] += q.w;
       }
-      put8<F32>(a, t == 0 ? tok[0] : t == 1 ? tok[1] : t == 2 ? tok[2] : tok[3], n, s);
+      put8<F32>(a, t == 0 ? tok[0] : tok[1], n, s);
     }
   }
 }
@@ -238,10 +243,10 @@ __device__ __forceinline__ void spread(const DecodeArgs& a, const float* part, f
 template <bool F32>
 __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads, 3) lora_decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
-  uint16_t* xs = reinterpret_cast<uint16_t*>(raw);                      // [kT][kslice]
+  uint16_t* xs = reinterpret_cast<uint16_t*>(raw + kRedBytes);          // [kT][kslice]
   float* part = reinterpret_cast<float*>(xs + kT * a.kslice);           // [kCl][max_rank][kT]
   float* sums = part + kCl * a.max_rank * kT;                           // [max_rank][kT]
-  float* red = sums + a.max_rank * kT;                                  // [kWarps][kT][kWide]
+  float* red = reinterpret_cast<float*>(raw);                           // [rgs][kT][ncg * kWide]
   __shared__ unsigned votes[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, m = blockIdx.y;
@@ -257,9 +262,10 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads, 3) lora_
     row0 = min(max(__ldg(a.off + v), 0), a.R);
     rank = min(min(max(__ldg(a.off + v + 1), row0), a.R) - row0, a.max_rank);
   }
-  const int n0 = c * a.nslice, n1 = min(n0 + a.nslice, a.N);
+  const int n0 = min((blockIdx.z * kCl + c) * a.nslice, a.N), n1 = min(n0 + a.nslice, a.N);
+  const bool keep = a.s && c == 0 && blockIdx.z == 0;
   if (rank == 0) {  // no adapter: y itself
-    if (a.s && c == 0)
+    if (keep)
       for (int i = tid; i < a.max_rank; i += kThreads) a.s[(size_t)m * a.max_rank + i] = 0.f;
     if (a.out != a.y) {
       const float zero[8] = {};
@@ -279,45 +285,53 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads, 3) lora_
     mask &= mask - 1;
   }
   const int k0 = c * a.kslice, kn = max(0, min(a.kslice, a.K - k0));
+  cluster_arrive();  // the others' shared memory may be written once all have come this far
 #pragma unroll
   for (int t = 0; t < kT; ++t)
     if (t < T)
       for (int k = tid * kVec; k < kn; k += kThreads * kVec)
         *reinterpret_cast<uint4*>(xs + t * a.kslice + k) =
             __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)tok[t] * a.ldx + k0 + k));
-  __syncthreads();
   const float scale = __ldg(a.scale + v);
-  const bool keep = a.s && c == 0;
+  cluster_wait();
+  __syncthreads();
   if (T == 1) {
     contract<1, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
     spread<F32, 1, 8>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
   } else {
-    contract<kT, 4>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
-    spread<F32, kT, 4>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
+    contract<kT, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    spread<F32, kT, 8>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
   }
 }
 
-int slice(int d) { return ((d + kCl - 1) / kCl + 7) / 8 * 8; }
+// Columns of a CTA where `parts` of them share d.
+int slice(int d, int parts) { return ((d + parts - 1) / parts + 7) / 8 * 8; }
+// Clusters that share the columns of B^T: as many as give one wave of three CTAs per
+// SM, with 256 to 2048 columns of a CTA.
+int column_clusters(int M, int N) {
+  const int least = (N + kCl * kWarps * kWide - 1) / (kCl * kWarps * kWide), most = (N + kCl * kWide - 1) / (kCl * kWide);
+  return std::max(least, std::min(most, 3 * num_sms() / (kCl * M)));
+}
 
 template <bool F32>
 cudaError_t launch(const DecodeArgs& a, size_t smem, cudaStream_t st) {
-  cudaError_t e = ensure_smem_attr<lora_decode_kernel<F32>>(200 * 1024);
+  cudaError_t e = ensure_smem_attr<lora_decode_kernel<F32>>((int)(kRedBytes + kT * kMaxSlice * 2 + (kCl + 1) * 256 * kT * 4));
   if (e != cudaSuccess) return e;
-  return launch_pdl(lora_decode_kernel<F32>, dim3(kCl, a.M), dim3(kThreads), smem, st, a);
+  return launch_pdl(lora_decode_kernel<F32>, dim3(kCl, a.M, column_clusters(a.M, a.N)), dim3(kThreads), smem, st, a);
 }
 
 size_t smem_bytes(int K, int max_rank) {
-  return (size_t)kT * slice(K) * 2 + (size_t)(kCl + 1) * max_rank * kT * 4 + (size_t)kWarps * kT * kWide * 4;
+  return kRedBytes + (size_t)kT * slice(K, kCl) * 2 + (size_t)(kCl + 1) * max_rank * kT * 4;
 }
 
 }  // namespace
 
-bool lora_decode_fits(const aq_lora* ad, int M) { return M <= 64 && smem_bytes(ad->K, ad->max_rank) <= 100 * 1024; }
+bool lora_decode_fits(const aq_lora* ad, int M) { return M <= 64 && slice(ad->K, kCl) <= kMaxSlice; }
 
 cudaError_t launch_lora_decode(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* ids, int M, const void* y,
                                int ldy, void* out, int ldo, bool f32, float* s, cudaStream_t st) {
   const DecodeArgs a{ad->a, ad->bt, ad->off, ad->scale, ad->N, ad->K, ad->L, ad->R, ad->max_rank, x, ldx, M,
-                     ids, y, out, ldy, ldo, s, slice(ad->K), slice(ad->N)};
+                     ids, y, out, ldy, ldo, s, slice(ad->K, kCl), slice(ad->N, kCl * column_clusters(M, ad->N))};
   const size_t smem = smem_bytes(ad->K, ad->max_rank);
   return f32 ? launch<true>(a, smem, st) : launch<false>(a, smem, st);
 }
