@@ -611,14 +611,16 @@ def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int) -> int
     says nothing: its width rounded up stands in)."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must live on {device if device.type == 'cuda' else 'a CUDA device'}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2 and stride[1] == 1 and shape[0] >= M and shape[1] >= width:
-        if shape[0] == 1:
-            return -(-shape[1] // 16) * 16
-        if stride[0] >= width:
-            return stride[0]
+    if t.device != device:
+        raise ValueError(f"{name} must live on {device}")
+    stride = t.stride()
+    if len(stride) == 2 and stride[1] == 1:
+        rows, cols = t.shape
+        if rows >= M and cols >= width:
+            if rows == 1:
+                return -(-cols // 16) * 16
+            if stride[0] >= width:
+                return stride[0]
     raise ValueError(f"{name} must be [>= {M}][>= {width}] with unit inner stride and rows that do not overlap")
 
 
@@ -626,7 +628,24 @@ def _matrix(t: torch.Tensor, name: str):
     """Rows, columns and device of the 2-D tensor that sets a call's sizes."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D torch.bfloat16 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
     return *t.shape, t.device
+
+
+def _exact(t: torch.Tensor, name: str, dtype, device, shape):
+    """_need, with a shape; one pass over what is right, the messages where it is not."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _need(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {list(t.shape)}")
+
+
+def _new(like, rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A [rows][cols] tensor; the cheaper way where `like` has its shape and layout."""
+    if like is not None and like.dtype is dtype and like.shape == (rows, cols) and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty((rows, cols), dtype=dtype, device=device)
 
 
 def _call(fn, name: str, device, *args):
@@ -723,18 +742,6 @@ def _lora_ws(ad: Adapters, M: int, backward: int, ws):
     return _own_ws("lora", need, ad.device)
 
 
-def _lora_ids(ad: Adapters, ids: torch.Tensor, M: int):
-    _need(ids, "ids", torch.int32, ad.device)
-    if ids.dim() != 1 or ids.shape[0] != M:
-        raise ValueError(f"ids must be int32 [{M}], one adapter index per token")
-
-
-def _lora_s(ad: Adapters, s: torch.Tensor, M: int):
-    _need(s, "s", torch.float32, ad.device)
-    if s.shape != (M, ad.max_rank):
-        raise ValueError(f"s must be float32 [{M}][{ad.max_rank}]")
-
-
 def aq_lora_apply(ad: Adapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Tensor = None, s: torch.Tensor = None,
                   out: torch.Tensor = None, out_dtype=torch.float32, ws: torch.Tensor = None) -> torch.Tensor:
     """y + scale_l B_l A_l x per token, l = ids[m] (none outside [0, L)): x bf16 [M][K],
@@ -744,15 +751,18 @@ def aq_lora_apply(ad: Adapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Ten
     M, _, _ = _matrix(x, "x")
     dev, N = ad.device, ad.N
     ldx = _rows(x, "x", (_BF16,), dev, M, ad.K)
-    _lora_ids(ad, ids, M)
+    _exact(ids, "ids", torch.int32, dev, (M,))
     ldy = 0
     if y is not None:
         ldy, out_dtype = _rows(y, "y", (_F32, _BF16), dev, M, N), y.dtype
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    ldo = _rows(out, "out", (_F32, _BF16) if y is None else (out_dtype,), dev, M, N)
+        out, ldo = _new(y, M, N, out_dtype, dev), N
+        if out_dtype not in (_F32, _BF16):
+            raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    else:
+        ldo = _rows(out, "out", (_F32, _BF16) if y is None else (out_dtype,), dev, M, N)
     if s is not None:
-        _lora_s(ad, s, M)
+        _exact(s, "s", _F32, dev, (M, ad.max_rank))
     ws = _lora_ws(ad, M, 0, ws)
     _call(lib().aq_lora_apply, "aq_lora_apply", dev, ad.ref, x.data_ptr(), ldx, ids.data_ptr(), M,
           None if y is None else y.data_ptr(), ldy, out.data_ptr(), ldo, AQ_F32 if out.dtype == _F32 else AQ_BF16,
@@ -772,8 +782,8 @@ def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch
     M, _, _ = _matrix(dy, "dy")
     dev, N, K, R = ad.device, ad.N, ad.K, ad.R
     ldd = _rows(dy, "dy", (_BF16,), dev, M, N)
-    _lora_ids(ad, ids, M)
-    _lora_s(ad, s, M)
+    _exact(ids, "ids", torch.int32, dev, (M,))
+    _exact(s, "s", _F32, dev, (M, ad.max_rank))
     ldx = _rows(x, "x", (_BF16,) if sx is None else (torch.int8,), dev, M, K)
     if sx is not None:
         _need(sx, "sx", torch.float32, dev)
@@ -783,17 +793,19 @@ def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch
     if add is not None:
         ldadd, dx_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if dx is None and (want_dx or add is not None):
-        dx = torch.empty((M, K), dtype=dx_dtype, device=dev)
-    if dx is not None:
+        dx, lddx = _new(add, M, K, dx_dtype, dev), K
+        if dx_dtype not in (_F32, _BF16):
+            raise TypeError("dx_dtype must be torch.float32 or torch.bfloat16")
+    elif dx is not None:
         lddx = _rows(dx, "dx", (_F32, _BF16) if add is None else (dx_dtype,), dev, M, K)
     if da is None:
         da = torch.empty((R, K), dtype=_F32, device=dev)
+    else:
+        _exact(da, "da", _F32, dev, (R, K))
     if dbt is None:
         dbt = torch.empty((R, N), dtype=_F32, device=dev)
-    for t, name, width in ((da, "da", K), (dbt, "dbt", N)):
-        _need(t, name, _F32, dev)
-        if t.shape != (R, width):
-            raise ValueError(f"{name} must be float32 [{R}][{width}]")
+    else:
+        _exact(dbt, "dbt", _F32, dev, (R, N))
     ws = _lora_ws(ad, M, 1, ws)
     _call(lib().aq_lora_backward, "aq_lora_backward", dev, ad.ref, dy.data_ptr(), ldd, ids.data_ptr(), M, s.data_ptr(),
           x.data_ptr(), ldx, None if sx is None else sx.data_ptr(), da.data_ptr(), dbt.data_ptr(),
@@ -815,17 +827,18 @@ def aq_silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, keep: bool = False, 
     ldg, ldu = _rows(gate, "gate", (_BF16,), dev, M, F), _rows(up, "up", (_BF16,), dev, M, F)
     if up.shape != (M, F):
         raise ValueError("gate and up must have one shape")
-    hq = torch.empty((M, F), dtype=torch.int8, device=dev) if hq is None else hq
-    sh = torch.empty((M,), dtype=_F32, device=dev) if sh is None else sh
-    _need(hq, "hq", torch.int8, dev)
-    _need(sh, "sh", _F32, dev)
-    if hq.shape != (M, F) or sh.numel() < M:
-        raise ValueError("hq must be int8 [M][F] and sh hold M scales")
+    if hq is None:
+        hq = torch.empty((M, F), dtype=torch.int8, device=dev)
+    else:
+        _exact(hq, "hq", torch.int8, dev, (M, F))
+    if sh is None:
+        sh = torch.empty((M,), dtype=_F32, device=dev)
+    else:
+        _exact(sh, "sh", _F32, dev, (M,))
     kept, ptrs = (), (None,) * 4
     if keep:
-        groups = -(-F // AQ_GATED_GROUP)
-        kept = tuple(t for _ in range(2) for t in (torch.empty((M, F), dtype=torch.int8, device=dev),
-                                                   torch.empty((M, groups), dtype=_F32, device=dev)))
+        gs = torch.empty((M, -(-F // AQ_GATED_GROUP)), dtype=_F32, device=dev)
+        kept = torch.empty_like(hq), gs, torch.empty_like(hq), torch.empty_like(gs)
         ptrs = tuple(t.data_ptr() for t in kept)
     _call(lib().aq_silu_mul_quant, "aq_silu_mul_quant", dev, gate.data_ptr(), ldg, up.data_ptr(), ldu, M, F,
           hq.data_ptr(), sh.data_ptr(), *ptrs)
@@ -838,14 +851,18 @@ def aq_silu_mul_backward(dh: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, u
     (dgate, dup) bf16 [M][F]."""
     M, F, dev = _matrix(dh, "dh")
     ldd, groups = _rows(dh, "dh", (_BF16,), dev, M, F), -(-F // AQ_GATED_GROUP)
-    for q, s, name in ((gq, gs, "g"), (uq, us, "u")):
-        _need(q, name + "q", torch.int8, dev)
-        _need(s, name + "s", _F32, dev)
-        if q.shape != (M, F) or s.shape != (M, groups):
-            raise ValueError(f"{name}q must be int8 [M][F] and {name}s float32 [M][ceil(F/{AQ_GATED_GROUP})]")
-    dgate = torch.empty((M, F), dtype=_BF16, device=dev) if dgate is None else dgate
-    dup = torch.empty((M, F), dtype=_BF16, device=dev) if dup is None else dup
-    ldg, ldu = _rows(dgate, "dgate", (_BF16,), dev, M, F), _rows(dup, "dup", (_BF16,), dev, M, F)
+    _exact(gq, "gq", torch.int8, dev, (M, F))
+    _exact(uq, "uq", torch.int8, dev, (M, F))
+    _exact(gs, "gs", _F32, dev, (M, groups))
+    _exact(us, "us", _F32, dev, (M, groups))
+    if dgate is None:
+        dgate, ldg = _new(dh, M, F, _BF16, dev), F
+    else:
+        ldg = _rows(dgate, "dgate", (_BF16,), dev, M, F)
+    if dup is None:
+        dup, ldu = _new(dh, M, F, _BF16, dev), F
+    else:
+        ldu = _rows(dup, "dup", (_BF16,), dev, M, F)
     _call(lib().aq_silu_mul_backward, "aq_silu_mul_backward", dev, dh.data_ptr(), ldd, gq.data_ptr(), gs.data_ptr(),
           uq.data_ptr(), us.data_ptr(), M, F, dgate.data_ptr(), ldg, dup.data_ptr(), ldu)
     return dgate, dup
@@ -866,8 +883,11 @@ def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = N
     if add is not None:
         ldadd, out_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype, device=dev)
-    ldo = _rows(out, "out", (_F32, _BF16) if add is None else (out_dtype,), dev, M, K)
+        out, ldo = _new(add, M, K, out_dtype, dev), K
+        if out_dtype not in (_F32, _BF16):
+            raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    else:
+        ldo = _rows(out, "out", (_F32, _BF16) if add is None else (out_dtype,), dev, M, K)
     if ws is not None:
         _need(ws, "ws", torch.uint8, dev)
     else:
