@@ -12,8 +12,9 @@
 // 64 x 128 x 3r multiplications.
 //
 // A CTA takes 128 columns and a range of tokens, whoever's they are, so that
-// unequal adapters do not make unequal CTAs; it goes through the adapters of its
-// range one after another, over the 64s that have a part in each.  Where a 64 holds
+// unequal adapters do not make unequal CTAs.  It lists its steps beforehand, (adapter,
+// 64 tokens) pairs ordered by adapter, and runs through them without a pause at an
+// adapter's end (a pause cost 5 us).  Where a 64 holds
 // other adapters' tokens too, their rows are cleared in shared memory on both sides,
 // so that nothing of them, not even an infinity, reaches the sum.  Tensor memory
 // sums 512 tokens at a time; the epilogue adds those sums in fp32 registers,
@@ -37,6 +38,12 @@ constexpr int kThreads = 384;
 constexpr int kUnit = 8;       // steps summed in tensor memory
 constexpr int kXf = 4, kEpi = 4;  // warps
 constexpr int kMaxAdapters = 16384;
+constexpr int kListCap = 768, kSlotCap = 64;  // steps and adapters listed at once
+
+// A listed step: which 64 tokens of the range, whether others' tokens are among them, the
+// bounds of a unit and of its adapter, and the adapter's slot.
+constexpr uint32_t kMixed = 1u << 9, kUnitStart = 1u << 10, kUnitEnd = 1u << 11, kLast = 1u << 12;
+constexpr int kSlotShift = 13;
 
 // ---------------------------------------------------------------- terms
 struct TermsJob {
@@ -129,7 +136,7 @@ struct GradShape {
   static constexpr int kSB = NB <= 48 ? (CODES ? 6 : 4) : NB <= 96 ? 3 : 5;
   static constexpr int kRaw = CODES ? (NB <= 96 ? 3 : 5) : 0;  // 8 KiB each
   static constexpr int kTmem = 2 * NB <= 128 ? 128 : 2 * NB <= 256 ? 256 : 512;
-  static constexpr int kCtrl = 512 + kThreads * 2 + kMaxAdapters / 8;
+  static constexpr int kCtrl = 512 + kListCap * 4 + 3 * kSlotCap * 4 + kMaxAdapters / 8;
   static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kTok * kD + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
   static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
@@ -189,27 +196,15 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_flag = abort_flag + 1;
-  volatile int* count = abort_flag + 2;  // [12] listed chunks of each warp
-  volatile uint16_t* list = reinterpret_cast<volatile uint16_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512);
-  uint32_t* present = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512 + kThreads * 2);
+  volatile int* count = abort_flag + 2;  // [2][12] steps of each warp
+  volatile uint32_t* list = reinterpret_cast<volatile uint32_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512);
+  volatile int* slot_id = reinterpret_cast<volatile int*>(list + kListCap);  // adapter, first gradient row, ranks
+  volatile int* slot_row = slot_id + kSlotCap;
+  volatile int* slot_nr = slot_row + kSlotCap;
+  uint32_t* present = reinterpret_cast<uint32_t*>(const_cast<int*>(slot_nr + kSlotCap));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int d0 = blockIdx.x * kD, split = blockIdx.y;
-  pdl_wait();
-  const int chunks = (a.M + kTok - 1) / kTok;
-  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
-  // the adapters of this range's (at most 384) 64s, one of which each thread looks after
-  const int words = (a.L + 31) / 32, own = c0 + tid < c1 ? __ldg(a.info + c0 + tid) : -1;
-  const int own_m0 = (c0 + tid) * kTok, own_m1 = min(own_m0 + kTok, a.M);
-  for (int i = tid; i < words; i += kThreads) present[i] = 0;
-  __syncthreads();
-  if (own >= 0) atomicOr(&present[own >> 5], 1u << (own & 31));
-  if (own == -2)
-    for (int m = own_m0; m < own_m1; ++m) {
-      const int v = __ldg(a.ids + m);
-      if (v >= 0 && v < a.L) atomicOr(&present[v >> 5], 1u << (v & 31));
-    }
-
   if (tid == 0) {
     for (int i = 0; i < RW; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -239,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     tmem_alloc(tmem_slot, Sh::kTmem);
     tmem_relinquish();
   }
+  for (int i = tid; i < (a.L + 31) / 32; i += kThreads) present[i] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -252,34 +248,71 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     record_error(a.ws, AQ_ERR_TIMEOUT, info, 0);
   };
 
+  pdl_wait();
+  // the adapters of this range's (at most 384) 64s, one of which each thread looks after
+  const int chunks = (a.M + kTok - 1) / kTok;
+  const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
+  const int own = c0 + tid < c1 ? __ldg(a.info + c0 + tid) : -1;
+  const unsigned mixed_lanes = __ballot_sync(0xffffffffu, own == -2);
+  if (own >= 0) atomicOr(&present[own >> 5], 1u << (own & 31));
+  for (unsigned left = mixed_lanes; left; left &= left - 1) {  // a warp reads a mixed 64 together
+    const int m0 = (c0 + 32 * warp + __ffs(left) - 1) * kTok;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = m0 + 32 * h + lane, v = m < a.M ? __ldg(a.ids + m) : -1;
+      if (v >= 0 && v < a.L) atomicOr(&present[v >> 5], 1u << (v & 31));
+    }
+  }
+  __syncthreads();
+
   Ring sr{0, 0}, br{0, 0}, rr{0, 0}, ar{0, 0};  // activations, terms, codes, accumulator
   bool ok = true, issued = false;
+  float tot[Sh::kRanks];
+#pragma unroll
+  for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
 
-  for (int l = 0; l < a.L; ++l) {
-    const uint32_t bits = present[l >> 5] >> (l & 31);
-    if (bits == 0) {  // none up to the word's end
-      l |= 31;
-      continue;
+  for (int l = 0; l < a.L;) {
+    // list the steps of the next adapters
+    int n = 0, slots = 0, turn = 0;
+    for (; l < a.L && slots < kSlotCap; ++l) {
+      const uint32_t bits = present[l >> 5] >> (l & 31);
+      if (bits == 0) {  // none up to the word's end
+        l |= 31;
+        continue;
+      }
+      l += __ffs(bits) - 1;
+      const int row0 = min(max(__ldg(a.off + l), 0), a.R);
+      const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
+      if (nr <= 0) continue;
+      bool take = own == l;
+      for (unsigned left = mixed_lanes; left; left &= left - 1) {
+        const int m = (c0 + 32 * warp + __ffs(left) - 1) * kTok + lane;
+        const bool has = (m < a.M && __ldg(a.ids + m) == l) || (m + 32 < a.M && __ldg(a.ids + m + 32) == l);
+        if (__any_sync(0xffffffffu, has) && lane == __ffs(left) - 1) take = true;
+      }
+      const unsigned vote = __ballot_sync(0xffffffffu, take);
+      if (lane == 0) count[12 * turn + warp] = __popc(vote);
+      __syncthreads();
+      int at = __popc(vote & ((1u << lane) - 1)), mine = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int c = count[12 * turn + w];
+        if (w < warp) at += c;
+        mine += c;
+      }
+      turn ^= 1;
+      if (n + mine > kListCap) break;  // (at most 384 of one adapter: the list holds two)
+      if (take)
+        list[n + at] = (uint32_t)tid | (own == -2 ? kMixed : 0u) | (at % kUnit == 0 ? kUnitStart : 0u) |
+                       (at % kUnit == kUnit - 1 || at + 1 == mine ? kUnitEnd : 0u) | (at + 1 == mine ? kLast : 0u) |
+                       ((uint32_t)slots << kSlotShift);
+      if (tid == 0) {
+        slot_id[slots] = l;
+        slot_row[slots] = row0 + a.rb0;
+        slot_nr[slots] = nr;
+      }
+      n += mine;
+      ++slots;
     }
-    l += __ffs(bits) - 1;
-    const int row0 = min(max(__ldg(a.off + l), 0), a.R);
-    const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
-    if (nr <= 0) continue;
-    // its 64s, in order; bit 15: others' tokens too
-    __syncthreads();
-    int take = own == l;
-    if (own == -2)
-      for (int m = own_m0; m < own_m1; ++m)
-        if (__ldg(a.ids + m) == l) take = 2;
-    const unsigned vote = __ballot_sync(0xffffffffu, take != 0);
-    if (lane == 0) count[warp] = __popc(vote);
-    __syncthreads();
-    int at = __popc(vote & ((1u << lane) - 1)), n = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += count[w];
-      n += count[w];
-    }
-    if (take) list[at] = (uint16_t)(tid | (take == 2 ? 0x8000 : 0));
     __syncthreads();
     const int base = c0;
 
@@ -287,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       // ------------------------------------------------------------ codes, or bf16 activations
       if (lane == 0) {
         for (int i = 0; ok && i < n; ++i) {
-          const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
+          const int m0 = (base + (int)(list[i] & 0x1FF)) * kTok;
           if (!(CODES ? mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag)
                       : mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag))) {
             fail(21);
@@ -311,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       if (lane == 0) {
         const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kTok * 128), bdesc0 = mn_desc(smem_u32(stage_b(0)), kTok * 128);
         for (int i = 0; ok && i < n; ++i) {
-          if (i % kUnit == 0 && !mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag)) {
+          const uint32_t step = list[i];
+          if ((step & kUnitStart) && !mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag)) {
             fail(22);
             ok = false;
             break;
@@ -326,13 +360,13 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
           const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of eight rows
-            mma_bf16(tmem_base + ar.i * NB, ao + 128 * k, bo + 128 * k, Sh::kIdesc, i % kUnit > 0 || k > 0);
+            mma_bf16(tmem_base + ar.i * NB, ao + 128 * k, bo + 128 * k, Sh::kIdesc, !(step & kUnitStart) || k > 0);
           mma_commit(&a_done[sr.i]);
           mma_commit(&b_done[br.i]);
           issued = true;
           sr.template next<SA>();
           br.template next<SB>();
-          if (i % kUnit == kUnit - 1 || i + 1 == n) {
+          if (step & kUnitEnd) {
             mma_commit(&acc_full[ar.i]);
             ar.template next<2>();
           }
@@ -350,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
           mbar_arrive_expect_tx(&b_full[br.i], Sh::kB);
 #pragma unroll
           for (int c = 0; c < Sh::kAtoms; ++c)
-            tma_load_2d(stage_b(br.i) + c * 8192, &maps.terms, 64 * c, (base + (list[i] & 0x7FFF)) * kTok, &b_full[br.i]);
+            tma_load_2d(stage_b(br.i) + c * 8192, &maps.terms, 64 * c, (base + (int)(list[i] & 0x1FF)) * kTok, &b_full[br.i]);
           br.template next<SB>();
         }
       }
@@ -358,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       // ------------------------------------------------------------ transform
       const int t = tid - 128, c = t & 15, r0 = t >> 4;
       for (int i = 0; ok && i < n; ++i) {
-        const bool mixed = list[i] & 0x8000;
-        const int m0 = (base + (list[i] & 0x7FFF)) * kTok;
+        const bool mixed = list[i] & kMixed;
+        const int m0 = (base + (int)(list[i] & 0x1FF)) * kTok;
         bool got = mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag);
         if (CODES) got = got && mbar_wait(&raw_full[rr.i], rr.ph, abort_flag);
         if (mixed) got = got && mbar_wait(&b_full[br.i], br.ph, abort_flag);
@@ -384,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
           // rows that this warp itself has written
           __syncwarp();
           const int w2 = 2 * (warp - 4), r = w2 + (lane >> 4) + 8 * ((lane & 15) >> 1), half = lane & 1, m = m0 + r;
-          if (m >= a.M || __ldg(a.ids + m) != l) {
+          if (m >= a.M || __ldg(a.ids + m) != slot_id[list[i] >> kSlotShift]) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
             for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stage_a(sr.i) + half * 8192 + r * 128 + q * 16) = zero;
             for (int q = half; q < 8 * Sh::kAtoms; q += 2)
@@ -403,10 +437,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       }
     } else if (warp >= 4 + kXf) {
       // ------------------------------------------------------------ epilogue
-      float tot[Sh::kRanks];
-#pragma unroll
-      for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
-      for (int i = 0; ok && i < n; i += kUnit) {
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t step = list[i];
+        if (!(step & kUnitEnd)) continue;
         if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
           fail(26);
           ok = false;
@@ -432,15 +465,18 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[ar.i]);
         ar.template next<2>();
-      }
-      const int d = d0 + 32 * (warp & 3) + lane;
-      if (d < a.D) {
-        float* g = a.g + ((size_t)split * a.R + row0 + a.rb0) * a.D + d;
+        if (step & kLast) {
+          const int d = d0 + 32 * (warp & 3) + lane, nr = slot_nr[step >> kSlotShift];
+          float* g = a.g + ((size_t)split * a.R + slot_row[step >> kSlotShift]) * a.D + d;
 #pragma unroll
-        for (int r = 0; r < Sh::kRanks; ++r)
-          if (r < nr) g[(size_t)r * a.D] = tot[r];
+          for (int r = 0; r < Sh::kRanks; ++r) {
+            if (r < nr && d < a.D) g[(size_t)r * a.D] = tot[r];
+            tot[r] = 0.f;
+          }
+        }
       }
     }
+    __syncthreads();  // the list may be written anew
   }
 
   // adapters without tokens here: noted for the sum, or zeros where there is none
