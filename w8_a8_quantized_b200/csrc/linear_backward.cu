@@ -23,10 +23,10 @@
 //   warp 1       allocates tensor memory; one lane issues tcgen05.mma (kind::f16,
 //                M = 128, N = NT, K = 16) four times per step
 //   warp 3       dY producer (TMA, 128-byte swizzle), after the previous kernel
-//   warps 4-15   transform: codes -> sw q in bf16 -> the swizzled A stage, in three
-//                groups of four warps that take every third step (one step's chain of
-//                waits and latencies is longer than its MMAs)
-//   warps 16-19  epilogue: tensor memory -> add -> dx, while the next unit runs in
+//   warps 4-11   transform: codes -> sw q in bf16 -> the swizzled A slot, in two groups
+//                of four warps that take every other step (one step's chain of waits and
+//                latencies is longer than its MMAs)
+//   warps 12-15  epilogue: tensor memory -> add -> dx, while the next unit runs in
 //                the other accumulator buffer
 // The weights are read before the previous kernel has finished; dY, add, dx and
 // the workspace are not touched before.
@@ -49,7 +49,7 @@ namespace {
 
 constexpr int kStep = 64;       // rows n per step
 constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 scales
-constexpr int kXfWarp0 = 4, kXfGroups = 3, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
+constexpr int kXfWarp0 = 4, kXfGroups = 2, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
 constexpr int kEpiWarp0 = kXfWarp0 + kXfGroups * kXfWarps, kEpiWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kMaxBwdSplits = 16;
@@ -67,6 +67,10 @@ struct BwdShape {
   static constexpr uint32_t kIdesc = idesc_bf16(NT, true, false);
   static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  // A parity says which of two phases is over, so a waiter must know the one before to be
+  // over.  A group that turns to step i has seen the MMAs of step i - kXfGroups - kSA
+  // complete; that has to cover the last but one use of its slots.
+  static_assert(kXfGroups <= kSA && kXfGroups + kSA <= kRaw, "phases");
   static_assert((2 * kRaw + 2 * kSA + 2 * kSB + 4 + 1) * 8 + kRaw * 4 + 3 * 4 <= kCtrl, "control area");
 };
 

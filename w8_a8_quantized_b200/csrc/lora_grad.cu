@@ -140,6 +140,9 @@ struct GradShape {
   static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kTok * kD + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
   static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  // the transform warps look at the terms' barriers in mixed steps only: the use of a slot
+  // before must be over by then (they have seen the MMAs of step i - kSA complete)
+  static_assert(kSB >= kSA, "phases");
   static_assert(kPerSm * kTmem <= 512, "tensor memory");
 };
 
