@@ -319,8 +319,7 @@ def aq_debug_paper_partials(w: PackedWeights, xq: torch.Tensor, M: int) -> torch
     P = torch.zeros((M, w.N, w.C), dtype=torch.int32, device=dev)
     with torch.cuda.device(dev):
         _check(lib().aq_debug_paper_partials(ctypes.byref(w.struct), xq.data_ptr(), M, P.data_ptr(), _stream(dev)),
-               "aq_debug_paper_partials", "aq_lora_apply", "aq_lora_backward", "aq_lora_workspace_bytes",
-            "aq_silu_mul_quant", "aq_silu_mul_backward", "aq_linear_backward", "aq_linear_backward_workspace_bytes")
+               "aq_debug_paper_partials")
     return P
 
 
