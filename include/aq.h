@@ -438,7 +438,7 @@ typedef struct aq_lora {
  *  ids   int32 [M]
  *  y     the projection's output [M][ldy], fp32 or bf16 (ydtype), or NULL (out = the
  *        adapters' part alone)
- *  out   [M][ldo], same dtype; may be y itself, otherwise must not overlap an input
+ *  out   [M][ldo], same dtype; may be y itself (same pitch), otherwise must not overlap an input
  *  s     fp32 [M][max_rank] or NULL: receives S (zeros behind a token's rank), which
  *        aq_lora_backward takes
  *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned, zero-filled once
@@ -467,7 +467,7 @@ int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* 
  *  x     int8 [M][ldx] (ldx % 16 == 0, K % 16 == 0) with sx fp32 [M], or bf16 [M][ldx] (ldx % 8 == 0)
  *  da    fp32 [R][K], dbt fp32 [R][N], 16-byte aligned, written
  *  add   [M][ldadd] of dxdtype or NULL (zero), e.g. aq_linear_backward's result
- *  dx    [M][lddx], fp32 or bf16 (dxdtype), or NULL (not wanted); may be add itself
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype), or NULL (not wanted); may be add itself (same pitch)
  *  ws    >= aq_lora_workspace_bytes(ad, M, 1) bytes, as for aq_lora_apply; a bounded wait
  *        that gives up is recorded there and reported by aq_workspace_status
  * Alignment, M and errors as for aq_lora_apply.
@@ -517,7 +517,7 @@ int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const fl
  *  dy    bf16 [M][ldd], 16-byte aligned, ldd % 8 == 0, ldd >= N
  *  add   [M][ldadd] of dxdtype or NULL (zero): e.g. the gradient through another
  *        projection of the same input
- *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself (same pitch)
  *  ws    >= aq_linear_backward_workspace_bytes(M, w) bytes, 16-byte aligned,
  *        zero-filled once as for the linear calls; errors by aq_workspace_status
  * 1 <= M <= 2097152.  Asynchronous.

@@ -47,7 +47,8 @@ def test_struct_layout_matches_the_header():
     (dict(x=None), ARG), (dict(x=24), ARG), (dict(ldx=248), ARG), (dict(ldx=260), ARG), (dict(ids=None), ARG),
     (dict(ids=18), ARG), (dict(M=0), ARG), (dict(M=65535 * 64 + 1), ARG), (dict(y=24), ARG), (dict(ldy=130), ARG),
     (dict(out=None), ARG), (dict(ldo=120), ARG), (dict(dtype=1, ldo=132), ARG), (dict(dtype=2), ARG), (dict(s=18), ARG),
-    (dict(ws=None), WORKSPACE), (dict(n=15), WORKSPACE), (dict(M=70, n=64), WORKSPACE), (dict(ws=24), ARG)])
+    (dict(ws=None), WORKSPACE), (dict(n=15), WORKSPACE), (dict(M=70, n=64), WORKSPACE), (dict(ws=24), ARG),
+    (dict(ldo=132), ARG), (dict(ldo=132, y=32, n=15), WORKSPACE)])  # in place with another pitch, and not in place
 def test_lora_apply_refusals(kw, status):
     assert apply(**kw) == status
 
@@ -57,7 +58,8 @@ def test_lora_apply_refusals(kw, status):
     (dict(s=None), ARG), (dict(s=18), ARG), (dict(x=None), ARG), (dict(ldx=264), ARG), (dict(sx=None, ldx=260), ARG),
     (dict(sx=18), ARG), (dict(ad=lora(K=248), ldx=256), SHAPE), (dict(da=None), ARG), (dict(dbt=24), ARG),
     (dict(dx=None), ARG), (dict(dx=24), ARG), (dict(lddx=250), ARG), (dict(ldadd=258), ARG), (dict(dtype=7), ARG),
-    (dict(M=0), ARG), (dict(ids=None), ARG), (dict(ws=None), WORKSPACE), (dict(n=64), WORKSPACE), (dict(ws=20), ARG)])
+    (dict(M=0), ARG), (dict(ids=None), ARG), (dict(ws=None), WORKSPACE), (dict(n=64), WORKSPACE), (dict(ws=20), ARG),
+    (dict(lddx=264), ARG)])
 def test_lora_backward_refusals(kw, status):
     assert backward(**kw) == status
 
@@ -108,7 +110,7 @@ def linear_back(w=None, dy=16, ldd=128, M=4, add=16, ldadd=256, dx=16, lddx=256,
     (dict(dy=None), ARG), (dict(dy=24), ARG), (dict(ldd=120), ARG), (dict(ldd=132), ARG), (dict(M=0), ARG),
     (dict(M=(1 << 21) + 1), ARG), (dict(add=24), ARG), (dict(ldadd=250), ARG), (dict(dx=None), ARG), (dict(dx=8), ARG),
     (dict(lddx=248), ARG), (dict(dtype=1, lddx=260), ARG), (dict(dtype=3), ARG), (dict(ws=None), WORKSPACE),
-    (dict(n=16), WORKSPACE), (dict(ws=24), ARG)])
+    (dict(n=16), WORKSPACE), (dict(ws=24), ARG), (dict(lddx=264), ARG)])
 def test_linear_backward_refusals(kw, status):
     assert linear_back(**kw) == status
 

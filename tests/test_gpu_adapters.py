@@ -283,6 +283,99 @@ def test_lora_gradients_against_differences():
         c.x[m, k] = old
 
 
+@pytest.mark.parametrize("M", [13, 70, 300])
+@pytest.mark.parametrize("ranks", [[8, 5], [8, 90]])
+def test_lora_padded_batch(M, ranks):
+    """Tokens without an adapter may hold anything: NaN in their activations, gradients
+    and products leave the others' results as they are, bit for bit."""
+    N, K = 264, 320
+    ids = np.array(segment_ids(M, 2, M))
+    ids[np.random.default_rng(M).random(M) < 0.3] = -1
+    ids[-5:] = -1
+    c = LoraCase(M, N, K, ranks, ids.tolist(), seed=M)
+    s = torch.empty(M, max(ranks), device="cuda")
+    out0 = aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    want = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, c.x)
+    pad = c.ids == -1
+    c.x[pad], c.dy[pad] = float("nan"), float("nan")
+    out = aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    assert torch.equal(out, out0) and not s[pad].any()
+    s[pad] = float("nan")
+    got = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, c.x)
+    assert all(torch.equal(p, q) for p, q in zip(got, want)) and not got[2][pad].any()
+
+
+SIZES = [  # M, N, K, ranks, ids: the smallest and the longest axes, the most adapters
+    (1, 8, 8, [1], [0]),
+    (70, 8, 8, [1, 2], [m % 2 for m in range(70)]),
+    (70, 8, 16, [3], [0] * 70),
+    (1, 1 << 20, 1 << 20, [2], [0]),
+    (66, 8, 1 << 20, [1, 2], segment_ids(66, 2, 1)),
+    (66, 1 << 20, 16, [2, 1], segment_ids(66, 2, 2)),
+    (100, 64, 48, [1] * 16383, [(m * m * 163) % 16383 for m in range(100)]),
+    (1500, 136, 64, [1 + l % 3 for l in range(500)], mixed_ids(1500, 500, 11)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SIZES)))
+def test_lora_extreme_sizes(case):
+    c = LoraCase(*SIZES[case], seed=70 + case, scales=[0.5 + (l % 7) / 8 for l in range(len(SIZES[case][3]))])
+    s64, d64, ts, td = c.forward()
+    s = torch.empty(c.M, max(c.ranks), device="cuda")
+    out = aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    assert_within(s, s64, ts, "s")
+    assert_within(out, d64, td + 2 * U * d64.abs() + half_step(torch.float32) * (d64.abs() + td), "out")
+    x, sx, x64 = c.x, None, c.x.double()
+    if c.K % 16 == 0:
+        x, sx = aq.aq_quant_act(c.x.contiguous())
+        x64 = x.double() * sx.double()[:, None]
+    add = torch.zeros(c.M, c.K, device="cuda")
+    (da64, ta), (db64, tb), (dx64, tx) = backward_reference(c, s, x64, add)
+    da = torch.full((sum(c.ranks), c.K), float("nan"), device="cuda")
+    db = torch.full((sum(c.ranks), c.N), float("nan"), device="cuda")
+    _, _, dx = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, x, sx=sx, add=add, da=da, dbt=db)
+    assert_within(da, da64, ta, "da")
+    assert_within(db, db64, tb, "dbt")
+    assert_within(dx, dx64, tx + 2 * U * dx64.abs() + half_step(torch.float32) * (dx64.abs() + tx), "dx")
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_rows_past_32_bit_offsets(M):
+    """Pitches so long that the last row lies more than 2^31 elements on."""
+    N = K = 256
+    pitch = (1 << 31) // (M - 1) // 16 * 16 + 64
+    wide = lambda dtype: torch.empty(pitch * (M - 1) + K, dtype=dtype, device="cuda").as_strided((M, K), (pitch, 1))  # noqa: E731
+
+    def moved(t, dtype=None):
+        w = wide(dtype or t.dtype)
+        w.copy_(t)
+        return w
+
+    ids = [m % 2 for m in range(M)]
+    for ranks in ([8, 5], [8, 90]):
+        c = LoraCase(M, N, K, ranks, ids, seed=M)
+        y = normal(rng(M), M, N)
+        s = torch.empty(M, max(ranks), device="cuda")
+        want = aq.aq_lora_apply(c.ad, c.x, c.ids, y, s=s)
+        wx, wy, wo = moved(c.x), moved(y), wide(y.dtype)
+        assert torch.equal(aq.aq_lora_apply(c.ad, wx, c.ids, wy, out=wo), want)
+        want = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, c.x, add=y)
+        wy.copy_(y)
+        got = aq.aq_lora_backward(c.ad, moved(c.dy), c.ids, s, wx, add=wy, dx=wo)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        del wx, wy, wo, got
+    w, _ = packed(N, K, 128, 0.5, 7)
+    dy = normal(rng(8), M, N)
+    want = aq.aq_linear_backward(w, dy, add=y)
+    assert torch.equal(aq.aq_linear_backward(w, moved(dy), add=moved(y), out=wide(y.dtype)), want)
+    want = aq.aq_silu_mul_quant(dy, y, keep=True)
+    got = aq.aq_silu_mul_quant(moved(dy), moved(y), keep=True)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    want = aq.aq_silu_mul_backward(c.x, *want[2:])
+    got = aq.aq_silu_mul_backward(moved(c.x), *got[2:], dgate=wide(y.dtype), dup=wide(y.dtype))
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 # ------------------------------------------------------------------ gated activation
 
 def codes64(v, width):
@@ -605,3 +698,28 @@ def test_two_graphs_replayed_at_once():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert all(torch.equal(p, q) for p, q in zip(o, w))
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads may take turns between one call's launches."""
+    import threading
+    blocks = [Block(66 + 64 * i, 256, 512, mixed_ids(66 + 64 * i, 2, i), seed=30 + i) for i in range(2)]
+    want = [b.step()[0] for b in blocks]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, barrier = [[] for _ in blocks], threading.Barrier(2)
+
+    def run(i):
+        with torch.cuda.stream(stream):
+            barrier.wait(30)
+            for _ in range(20):
+                got[i].append(blocks[i].step()[0])
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 20 and all(torch.equal(p, q) for o in g for p, q in zip(o, w))

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import numpy as np
 import torch
@@ -707,11 +708,13 @@ def aq_lora_workspace_bytes(ad: Adapters, M: int, backward: bool) -> int:
 
 
 def _stream_ws(tag: str, need: int, device) -> torch.Tensor:
-    """A zero-filled workspace of the current stream, cached and grown on demand; a
-    call that is captured into a graph gets its own, so that graphs share none."""
+    """A zero-filled workspace of the current stream and thread, cached and grown on
+    demand (threads may take turns on a stream between one call's launches: autograd
+    runs backward passes in a thread of its own); a call that is captured into a graph
+    gets its own, so that graphs share none."""
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(need, dtype=torch.uint8, device=device)
-    key = (device, tag, _raw_stream(device.index))
+    key = (device, tag, _raw_stream(device.index), threading.get_ident())
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
         ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=device)
@@ -949,7 +952,7 @@ def aq_measure_i8_peak(iters: int = 20000, device=None) -> float:
 
 def check_all_workspaces():
     """Raise if any cached workspace recorded a kernel error."""
-    for ws in _ws_cache.values():
+    for ws in list(_ws_cache.values()):
         rc, info = aq_workspace_status(ws)
         if rc != AQ_OK:
             raise AqError(rc, f"kernel wait gave up (info {info})")

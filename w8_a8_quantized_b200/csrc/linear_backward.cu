@@ -548,6 +548,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   const int per16 = dxdtype == AQ_F32 ? 4 : 8;
   if (lddx < w->K || lddx % per16 || ((uintptr_t)dx & 15)) return AQ_ERR_ARG;
   if (add && (ldadd < w->K || ldadd % per16 || ((uintptr_t)add & 15))) return AQ_ERR_ARG;
+  if (add == dx && ldadd != lddx && M > 1) return AQ_ERR_ARG;  // in place is row by row
   if (!ws || ws_bytes < aq_linear_backward_workspace_bytes(M, w)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
   const BwdPlan p = plan_bwd(M, w->N, w->C);

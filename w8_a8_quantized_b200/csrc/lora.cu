@@ -559,6 +559,8 @@ constexpr int kMaxTokens = 65535 * kTok;  // grid rows of the expand kernel
 
 // Rows read or written as 16-byte vectors.
 bool bad_rows(const void* p, int ld, int width, int per16) { return !p || ((uintptr_t)p & 15) || ld < width || ld % per16; }
+// In place is row by row: the same pointer with another pitch would overwrite rows still to be read.
+bool skewed(const void* in, int ldi, const void* out, int ldo, int M) { return in == out && ldi != ldo && M > 1; }
 
 }  // namespace
 }  // namespace aq
@@ -579,7 +581,8 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
   if (M < 1 || M > kMaxTokens || !ids || ((uintptr_t)ids & 3) || ((uintptr_t)s & 3)) return AQ_ERR_ARG;
   if (ydtype != AQ_F32 && ydtype != AQ_BF16) return AQ_ERR_ARG;
   const int per16 = ydtype == AQ_F32 ? 4 : 8;
-  if (bad_rows(x, ldx, ad->K, 8) || bad_rows(out, ldo, ad->N, per16) || (y && bad_rows(y, ldy, ad->N, per16)))
+  if (bad_rows(x, ldx, ad->K, 8) || bad_rows(out, ldo, ad->N, per16) || (y && bad_rows(y, ldy, ad->N, per16)) ||
+      skewed(y, ldy, out, ldo, M))
     return AQ_ERR_ARG;
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 0)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
@@ -607,7 +610,8 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   if (dx) {
     if (dxdtype != AQ_F32 && dxdtype != AQ_BF16) return AQ_ERR_ARG;
     const int per16 = dxdtype == AQ_F32 ? 4 : 8;
-    if (bad_rows(dx, lddx, ad->K, per16) || (add && bad_rows(add, ldadd, ad->K, per16))) return AQ_ERR_ARG;
+    if (bad_rows(dx, lddx, ad->K, per16) || (add && bad_rows(add, ldadd, ad->K, per16)) || skewed(add, ldadd, dx, lddx, M))
+      return AQ_ERR_ARG;
   }
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 1)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;

@@ -487,13 +487,14 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     if (blockIdx.x == 0 && a.rb0 == 0)
       for (int l = tid; l < a.L; l += kThreads) a.has[(size_t)l * a.splits + split] = (present[l >> 5] >> (l & 31)) & 1u;
   } else {
-    const int width = min(kD, a.D - d0);
-    for (int l = 0; l < a.L; ++l) {
+    // a warp per adapter, four columns a lane (D is a multiple of 8)
+    const int d = d0 + 4 * lane;
+    for (int l = warp; l < a.L; l += kThreads / 32) {
       if ((present[l >> 5] >> (l & 31)) & 1u) continue;
       const int row0 = min(max(__ldg(a.off + l), 0), a.R);
       const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
-      for (int i = tid; i < nr * width; i += kThreads)
-        a.g[(size_t)(row0 + a.rb0 + i / width) * a.D + d0 + i % width] = 0.f;
+      for (int r = 0; d < a.D && r < nr; ++r)
+        *reinterpret_cast<float4*>(a.g + (size_t)(row0 + a.rb0 + r) * a.D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   if (warp == 1 && lane == 0 && issued) {
