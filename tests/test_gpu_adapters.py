@@ -513,7 +513,8 @@ def packed(N, K, bN, frac8, seed):
 BACK = [(1, 64, 128, 64, 0.0), (1, 128, 128, 128, 1.0), (3, 192, 384, 64, 0.5), (16, 640, 256, 128, 0.5),
         (33, 1088, 640, 64, 0.25), (64, 256, 2560, 128, 0.5), (77, 1088, 2560, 64, 0.5), (128, 128, 256, 128, 0.0),
         (129, 384, 512, 128, 0.25), (200, 2048, 384, 128, 1.0), (257, 320, 896, 64, 0.5), (500, 1024, 1280, 128, 0.5),
-        (1111, 704, 640, 64, 0.25), (2, 14336, 256, 128, 0.5)]
+        (1111, 704, 640, 64, 0.25), (2, 14336, 256, 128, 0.5), (900, 2048, 2176, 128, 0.5), (513, 4864, 2560, 128, 0.25),
+        (1030, 2560, 9728, 64, 0.5), (1500, 2560, 4096, 128, 0.5), (2048, 2560, 9728, 128, 0.5), (6000, 512, 640, 64, 0.5)]
 
 
 @pytest.mark.parametrize("M,N,K,bN,frac8", BACK)

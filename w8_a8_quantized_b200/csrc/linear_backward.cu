@@ -13,26 +13,34 @@
 //   D[128 k][NT tokens] += W'[64 n][128 k]^T dY[NT tokens][64 n]^T
 // with W' as the A operand, MN-major, so that the codes keep the packed order
 // (k contiguous) and no transposition is needed, and dY as the B operand,
-// K-major as it lies in memory.
+// K-major as it lies in memory.  Long sequences run in pairs of CTAs (cta_group::2):
+// a tile column each, every CTA holding half of the tokens' dY, which both use.
 //
 // Roles in one CTA (persistent over work units, every role walks the same
 // sequence of steps g = 0, 1, 2, ...):
 //   warp 0       weight producer: labels and tile indices of 32 steps at a time,
 //                one step per lane, the next 32 in flight; codes (TMA) and the 64
 //                row scales (bulk copy) into the raw ring
-//   warp 1       allocates tensor memory; one lane issues tcgen05.mma (kind::f16,
-//                M = 128, N = NT, K = 16) four times per step
+//   warp 1       allocates tensor memory; issues tcgen05.mma (kind::f16, K = 16) four times
+//                per step and 256 tokens, in a pair for both CTAs
 //   warp 3       dY producer (TMA, 128-byte swizzle), after the previous kernel
-//   warps 4-11   transform: codes -> sw q in bf16 -> the swizzled A slot, in two groups
-//                of four warps that take every other step (one step's chain of waits and
-//                latencies is longer than its MMAs)
-//   warps 12-15  epilogue: tensor memory -> add -> dx, while the next unit runs in
-//                the other accumulator buffer
+//   warps 4-     transform: codes -> sw q in bf16 -> the swizzled A slot, in two or three
+//                groups of four warps that take steps in turn (one step's chain of waits and
+//                latencies, 1000 cycles, is longer than its MMAs, 512 for 256 tokens)
+//   the rest     epilogue: tensor memory -> add -> dx, while the next unit runs in
+//                the other accumulator buffer; units of 512 tokens take both, and have a
+//                group of four warps for each
 // The weights are read before the previous kernel has finished; dY, add, dx and
 // the workspace are not touched before.
 //
+// What bounds it: the transform with 256 tokens a unit (step 810 cycles), the tensor pipe
+// with 512 (step 1100 of 1024 cycles; each dequantized tile serves twice the products), and
+// for long calls the power: 8192 x 14336 x 4096 (n x k) takes 1010 us in single CTAs, 910 in
+// pairs with 256 tokens and 740 with 512 (1.3 PFLOP/s; a library product sustains 1.38);
+// 2048 x 2560 x 9728 101, 95 and 85.
+//
 // Whole units go to the CTAs as long as every CTA gets one; the units that are left
-// (all of them for short sequences) are split over n so that they fill the GPU once
+// (all of them for short sequences) may be split over n so that they fill the GPU once
 // more, their partial sums go to the workspace, and a second launch adds them in
 // split order.  (Summed by the unit's
 // last CTA instead, 77 x 2560 x 1088 took 60 us: one CTA's loads wait for one
@@ -49,23 +57,25 @@ namespace {
 
 constexpr int kStep = 64;       // rows n per step
 constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 scales
-constexpr int kXfWarp0 = 4, kXfGroups = 2, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
-constexpr int kEpiWarp0 = kXfWarp0 + kXfGroups * kXfWarps, kEpiWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kXfWarp0 = 4, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
+constexpr int kEpiWarps = 4;
 constexpr int kMaxBwdSplits = 16;
 
-template <int NT>
+template <int NT, int CG>
 struct BwdShape {
+  static constexpr int kHalves = NT > 256 ? 2 : 1, kN = NT / kHalves;  // products of a step, their N
+  static constexpr int kXfGroups = CG == 2 && kHalves == 1 ? 3 : 2, kEpiWarp0 = kXfWarp0 + kXfGroups * kXfWarps;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps * kHalves);
   static constexpr int kA = kStep * kTileK * 2;  // W' slot: two 64-column halves of 64 rows x 128 bytes
-  static constexpr int kB = NT * kStep * 2;      // dY slot: NT rows x 128 bytes
+  static constexpr int kB = NT / CG * kStep * 2;  // dY slot: this CTA's rows x 128 bytes
   // Rings of W', dY and packed codes.  Copies take 1 to 1.5 us to land, as long as two
   // to four steps: codes and dY each need that many slots on their way.
-  static constexpr int kSA = NT <= 128 ? 4 : 3, kSB = NT <= 128 ? 6 : 4, kRaw = NT <= 128 ? 7 : 6;
-  static constexpr int kTmemCols = 2 * NT <= 32 ? 32 : 2 * NT <= 64 ? 64 : 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
+  static constexpr int kSA = NT / CG <= 128 ? 4 : 3, kSB = NT / CG <= 128 ? 6 : 4, kRaw = NT / CG <= 128 ? 7 : 6;
+  static constexpr int kTmemCols = 2 * kN <= 64 ? 64 : 2 * kN <= 128 ? 128 : 2 * kN <= 256 ? 256 : 512;  // two accumulators
   static constexpr int kCtrl = 512;
   static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kRawBytes + kCtrl;
-  static constexpr uint32_t kIdesc = idesc_bf16(NT, true, false);
-  static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N");
+  static constexpr uint32_t kIdesc = idesc_bf16(kN, true, false, 128 * CG);
+  static_assert(kN % 16 == 0 && kN >= 32 && kN <= 256, "MMA N");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // A parity says which of two phases is over, so a waiter must know the one before to be
   // over.  A group that turns to step i has seen the MMAs of step i - kXfGroups - kSA
@@ -93,7 +103,7 @@ struct BwdArgs {
 };
 
 struct BwdUnit {
-  int kb, tb, i0, i1;
+  int kb, tb, i0, i1;  // kb: with pairs, of two tile columns
   int part;  // index among the split work items, or -1
 };
 
@@ -113,6 +123,56 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   return x;
 }
 
+// ---- two CTAs on one tile: the leader (rank 0) issues the products of both
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t lead_addr(const void* p) {  // the same place in the leader's shared memory
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* slot_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot_smem)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Load into this CTA's memory that completes on the leader's barrier.
+__device__ __forceinline__ void tma_load_2d_lead(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(lead_addr(bar))
+      : "memory");
+}
+// Arrive at the leader's barrier.  (The products read each CTA's tiles in that CTA's own
+// memory: what it wrote has to be complete there, by the fence before the arrival.  A
+// release at cluster scope made the transform's step twice as long.)
+template <int CG>
+__device__ __forceinline__ void arrive_lead(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead_addr(bar)) : "memory");
+}
+// Arrive at the barriers of both CTAs when every MMA issued so far is done.
+template <int CG>
+__device__ __forceinline__ void mma_commit_all(uint64_t* bar) {
+  if constexpr (CG == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 // Four codes (two's-complement bytes) times sw, as two bf16 pairs.  The byte
 // b = q + 128 in the middle of a mantissa is 32768 + b, and 32896 sw is exact (9 + 11
 // bits), so one fused multiply-add gives sw q exactly, which is then rounded once.
@@ -126,11 +186,12 @@ __device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw, float2 off) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NT, int CG>
+__global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
     linear_backward_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
-  using Sh = BwdShape<NT>;
-  constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = Sh::kRaw;
+  using Sh = BwdShape<NT, CG>;
+  constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = Sh::kRaw, H = Sh::kHalves;
+  constexpr int kXfGroups = Sh::kXfGroups, kEpiWarp0 = Sh::kEpiWarp0;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -152,13 +213,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* never_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 1 ? 0 : blockIdx.x & 1, first_unit = blockIdx.x / CG, stride = gridDim.x / CG;
   if (threadIdx.x == 0) {
     for (int i = 0; i < RW; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kXfWarps);
     }
     for (int i = 0; i < SA; ++i) {
-      mbar_init(&a_full[i], kXfWarps);
+      mbar_init(&a_full[i], kXfWarps * CG);
       mbar_init(&a_done[i], 1);
     }
     for (int i = 0; i < SB; ++i) {
@@ -167,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kEpiWarps);
+      mbar_init(&acc_empty[i], kEpiWarps * CG);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -178,11 +240,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&maps.dy);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, Sh::kTmemCols);
-    tmem_relinquish();
+    if constexpr (CG == 1) {
+      tmem_alloc(tmem_slot, Sh::kTmemCols);
+      tmem_relinquish();
+    } else {
+      tmem_alloc2(tmem_slot, Sh::kTmemCols);
+      tmem_relinquish2();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();  // the other's barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();
@@ -194,21 +262,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ weight producer
-    int u = blockIdx.x;  // unit that holds this lane's next step, and the step it starts at
+    int u = first_unit;  // unit that holds this lane's next step, and the step it starts at
     uint32_t base = 0, g = lane;
     BwdUnit x = bwd_unit(a, u);
     // first row in its precision's buffer, offset of the scales, INT4 label: 2 = past the end
     auto fetch = [&](uint32_t& row, uint32_t& sc, uint32_t& kind) {
       while (u < a.units && g >= base + (uint32_t)(x.i1 - x.i0)) {
         base += x.i1 - x.i0;
-        u += gridDim.x;
+        u += stride;
         if (u < a.units) x = bwd_unit(a, u);
       }
       kind = 2;
       row = sc = 0;
       if (u < a.units) {
         const int n0 = (x.i0 + (int)(g - base)) * kStep, r = n0 / a.bN, in = n0 - r * a.bN;
-        const int t = r * a.C + x.kb;
+        const int t = r * a.C + x.kb * CG + rank;
         kind = __ldg(a.bitmap + (t >> 3)) >> (t & 7) & 1;
         row = (uint32_t)__ldg(a.tile_idx + t) * a.bN + in;
         sc = (uint32_t)t * a.bN + in;
@@ -247,40 +315,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && (!ok || *abort_flag)) grace();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (rank == 0) {
       const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kStep * 128), bdesc0 = sw128_desc(smem_u32(stage_b(0)));
-      Ring sr{0, 0}, br{0, 0};
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+      Ring sr{0, 0}, br{0, 0}, ar{0, 0};
       bool ok = true, any = false;
-      int ui = 0;
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x, ++ui) {
+      for (int u = first_unit; ok && u < a.units; u += stride) {
         const BwdUnit x = bwd_unit(a, u);
-        const int buf = ui & 1;
-        if (!mbar_wait(&acc_empty[buf], ((ui >> 1) & 1) ^ 1, abort_flag)) {
-          fail(2);
-          break;
-        }
-        const uint32_t d = tmem_base + buf * NT;
-        for (int i = x.i0; i < x.i1; ++i) {
-          if (!mbar_wait(&b_full[br.i], br.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag)) {
+        for (int i = x.i0; ok && i < x.i1; ++i) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag) &&
+                                           mbar_wait(&a_full[sr.i], sr.ph, abort_flag))) {
             fail(3);
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
 #pragma unroll
-          for (int k = 0; k < kStep / 16; ++k)  // 16 rows: two groups of A, 32 bytes of B
-            mma_bf16(d, ao + 128 * k, bo + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
-          mma_commit(&a_done[sr.i]);
-          mma_commit(&b_done[br.i]);
-          any = true;
+          for (int h = 0; h < H; ++h) {
+            const int buf = H == 2 ? h : ar.i;
+            if (i == x.i0 && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
+              fail(2);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * Sh::kN;
+            const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4),
+                           bo = bdesc0 + (uint64_t)((br.i * Sh::kB + h * (Sh::kB / H)) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kStep / 16; ++k)  // 16 rows: two groups of A, 32 bytes of B
+                mma_bf16<CG>(d, ao + 128 * k, bo + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
+              if (h == H - 1) {
+                mma_commit_all<CG>(&a_done[sr.i]);
+                mma_commit_all<CG>(&b_done[br.i]);
+              }
+              if (i + 1 == x.i1) mma_commit_all<CG>(&acc_full[buf]);
+            }
+            __syncwarp();
+            any = true;
+          }
           sr.template next<SA>();
           br.template next<SB>();
         }
-        if (ok) mma_commit(&acc_full[buf]);
+        if (H == 2) ar.ph ^= 1u;
+        else ar.template next<2>();
       }
-      if (any) {  // every MMA issued is complete before tensor memory is freed
-        mma_commit(drain);
+      if (any || CG == 2) {  // every MMA issued is complete before tensor memory is freed
+        if (elect_one()) mma_commit_all<CG>(drain);
+        __syncwarp();
         mbar_wait(drain, 0, never_flag);
       }
     }
@@ -290,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait();
       Ring br{0, 0};
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+      for (int u = first_unit; ok && u < a.units; u += stride) {
         const BwdUnit x = bwd_unit(a, u);
         for (int i = x.i0; i < x.i1; ++i) {
           if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag)) {
@@ -298,8 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&b_full[br.i], Sh::kB);
-          tma_load_2d(stage_b(br.i), &maps.dy, i * kStep, x.tb * NT, &b_full[br.i]);
+          // one barrier, the leader's, for both halves of the tokens
+          if (rank == 0) mbar_arrive_expect_tx(&b_full[br.i], Sh::kB * CG);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            uint8_t* dst = stage_b(br.i) + h * (Sh::kB / H);
+            const int m = x.tb * NT + h * Sh::kN + rank * (Sh::kN / CG);
+            if constexpr (CG == 1) tma_load_2d(dst, &maps.dy, i * kStep, m, &b_full[br.i]);
+            else tma_load_2d_lead(dst, &maps.dy, i * kStep, m, &b_full[br.i]);
+          }
           br.template next<SB>();
         }
       }
@@ -318,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring sr{0, 0}, rr{0, 0};
     bool ok = true;
     int turn = 0;
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+    for (int u = first_unit; ok && u < a.units; u += stride) {
       const BwdUnit x = bwd_unit(a, u);
       for (int i = x.i0; i < x.i1; ++i) {
         if (turn == group) {
@@ -358,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&a_full[sr.i]);
+            arrive_lead<CG>(&a_full[sr.i]);
             mbar_arrive(&raw_empty[rr.i]);
           }
         }
@@ -369,27 +458,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3;
+    // (two halves have a group of four warps each)
+    const int quad = warp & 3, half = (warp - kEpiWarp0) / kEpiWarps;
     const size_t kcol = 32 * quad + lane;
     pdl_wait();
     int ui = 0;
-    for (int u = blockIdx.x; u < a.units; u += gridDim.x, ++ui) {
+    for (int u = first_unit; u < a.units; u += stride, ++ui) {
       const BwdUnit x = bwd_unit(a, u);
-      const int buf = ui & 1, m0 = x.tb * NT;
-      const size_t k = (size_t)x.kb * kTileK + kcol;
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (ui >> 1) & 1, abort_flag))) {
+      const int buf = H == 2 ? half : ui & 1, phase = H == 2 ? ui & 1 : ui >> 1 & 1, m0 = x.tb * NT + half * Sh::kN;
+      const size_t k = (size_t)(x.kb * CG + rank) * kTileK + kcol;
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], phase, abort_flag))) {
         fail(6);
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * NT;
+      const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * Sh::kN;
       // a lane holds one column k of every token: a warp's stores cover 32 columns
-      float* fp = x.part >= 0 ? a.partial + (size_t)x.part * NT * kTileK + kcol
+      float* fp = x.part >= 0 ? a.partial + ((size_t)(x.part * CG + rank) * NT + half * Sh::kN) * kTileK + kcol
                               : static_cast<float*>(a.dx) + (size_t)m0 * a.lddx + k;
       __nv_bfloat16* bp = static_cast<__nv_bfloat16*>(a.dx) + (size_t)m0 * a.lddx + k;
       const size_t fld = x.part >= 0 ? kTileK : a.lddx;
       const bool f32 = a.f32 || x.part >= 0, add = a.add && x.part < 0;
-      const int cols = min(NT, a.M - m0);
+      const int cols = min(Sh::kN, a.M - m0);  // (none: below 0)
       for (int c0 = 0; c0 < cols; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(taddr + c0, v);
@@ -421,28 +511,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (lane == 0) arrive_lead<CG>(&acc_empty[buf]);
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) {
+    if (warp == 1) mbar_wait(drain, 0, never_flag);  // the leader's last arrival has come to this CTA too
+    __syncwarp();
+    cluster_sync();  // the other's products may read this CTA's memory until here
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, Sh::kTmemCols);
+    if constexpr (CG == 1) tmem_dealloc(tmem_base, Sh::kTmemCols);
+    else tmem_dealloc2(tmem_base, Sh::kTmemCols);
   }
 }
 
 // dx = add + the partial sums of the split units, splits in increasing order; four
 // columns of a token per thread, blockIdx.y the split unit.
-__global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs a, int nt) {
-  const int i = blockIdx.x * 256 + threadIdx.x, c = i / (kTileK / 4), u = a.whole + blockIdx.y;
-  const int m = u % a.ntb * nt + c, k = u / a.ntb * kTileK + i % (kTileK / 4) * 4;
+__global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs a, int nt, int cg) {
+  const int i = blockIdx.x * 256 + threadIdx.x, c = i / (kTileK / 4), col = blockIdx.y % cg, j = blockIdx.y / cg,
+            u = a.whole + j;
+  const int m = u % a.ntb * nt + c, k = (u / a.ntb * cg + col) * kTileK + i % (kTileK / 4) * 4;
   pdl_launch_dependents();
   pdl_wait();
   if (c >= nt || m >= a.M) return;
-  const float4* p = reinterpret_cast<const float4*>(a.partial) + (size_t)blockIdx.y * a.S * nt * (kTileK / 4) + i;
-  const size_t step = (size_t)nt * (kTileK / 4);
+  const float4* p = reinterpret_cast<const float4*>(a.partial) + ((size_t)j * a.S * cg + col) * nt * (kTileK / 4) + i;
+  const size_t step = (size_t)cg * nt * (kTileK / 4);
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int s = 0; s < a.S; ++s) {
@@ -477,53 +574,72 @@ __global__ void __launch_bounds__(256) linear_backward_sum_kernel(const BwdArgs 
 
 // ---------------------------------------------------------------- host side
 struct BwdPlan {
-  int nt, ntb;
+  int cg, nt, ntb;  // CTAs and tokens of a unit, units along the tokens
   long long whole;  // units done whole
   int rest, S;      // units that are split, and their splits
 };
 
-// Token-block width and splits.  A step takes the longer of the MMAs (2 NT cycles)
-// and what does not depend on NT (about 400: measured).
+// The forms of a unit, with the time of a step and of a unit's epilogue where the next
+// unit cannot cover it, in 10 ns (a fit over sizes from 64 x 2560 x 2560 to 4096 x 2048 x
+// 2048 to within 10%).
+struct BwdForm {
+  int cg, nt, step, unit;
+};
+constexpr BwdForm kBwdForms[] = {{1, 32, 40, 30},   {1, 64, 40, 40},   {1, 128, 40, 60},
+                                 {1, 256, 45, 120}, {2, 256, 41, 120}, {2, 512, 60, 400}};
+
+// The form and the splits of least time: the steps of the CTA that has most, its units'
+// ends, and for a split the second launch with its 4 bytes written and read per sum.
 BwdPlan plan_bwd(int M, int N, int C) {
-  const int sms = num_sms(), steps = N / kStep;
-  BwdPlan best{0, 0, 0, 0, 1};
+  const int steps = N / kStep;
+  BwdPlan best{0, 0, 0, 0, 0, 1};
   long long best_cost = 0;
-  for (int nt : {32, 64, 128, 192, 256}) {
-    const int ntb = (M + nt - 1) / nt;
-    const long long units = (long long)C * ntb;
-    BwdPlan p{nt, ntb, units / sms * sms, (int)(units % sms), 1};
-    if (p.rest > 0) p.S = std::max(1, std::min({sms / p.rest, steps / 4, kMaxBwdSplits}));
-    long long path = p.whole / sms * (long long)(steps + 2);
-    if (p.rest > 0) path += (steps + p.S - 1) / p.S + 4 + (p.S > 1 ? 6 : 0);
-    if (p.S == 1) {  // nothing to split
-      p.whole = units;
-      p.rest = 0;
-    }
-    const long long cost = path * std::max(2 * nt, 400);
-    if (best.nt == 0 || cost < best_cost) {
-      best = p;
-      best_cost = cost;
+  for (const BwdForm& f : kBwdForms) {
+    if (C % f.cg) continue;
+    const int ntb = (M + f.nt - 1) / f.nt, slots = num_sms() / f.cg;
+    const long long units = (long long)C / f.cg * ntb, rounds = units / slots;
+    const int rest = (int)(units % slots), most = rest ? std::max(1, std::min({slots / rest, steps / 4, kMaxBwdSplits})) : 1;
+    for (int S = 1; S <= most; ++S) {
+      const bool split = S > 1;
+      long long cost = (rounds * steps + (rest ? (steps + S - 1) / S : 0)) * f.step + (rounds + (rest > 0)) * f.unit;
+      if (split) cost += 300 + (rounds ? 500 : 0) + (long long)rest * S * f.cg * f.nt * kTileK * 4 * 30 / 1000000;
+      if (best.nt == 0 || cost < best_cost) {
+        best = split ? BwdPlan{f.cg, f.nt, ntb, rounds * slots, rest, S} : BwdPlan{f.cg, f.nt, ntb, units, 0, 1};
+        best_cost = cost;
+      }
     }
   }
   return best;
 }
 
-template <int NT>
+template <int NT, int CG>
 cudaError_t launch_bwd(const aq_packed* w, const uint16_t* dy, int ldd, const BwdArgs& a, cudaStream_t st) {
-  using Sh = BwdShape<NT>;
-  cudaError_t e = ensure_smem_attr<linear_backward_kernel<NT>>(Sh::kSmem);
+  using Sh = BwdShape<NT, CG>;
+  cudaError_t e = ensure_smem_attr<linear_backward_kernel<NT, CG>>(Sh::kSmem);
   if (e != cudaSuccess) return e;
   BwdMaps maps;
   memset(&maps, 0, sizeof(maps));
-  bool ok = map_2d(&maps.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, a.N, a.M, (uint64_t)ldd * 2, kStep, NT, true);
+  bool ok = map_2d(&maps.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, a.N, a.M, (uint64_t)ldd * 2, kStep, Sh::kN / CG, true);
   if (ok && w->T8 > 0)
     ok = map_2d(&maps.w8, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->w8, kTileK, (uint64_t)w->T8 * w->bN, kTileK, kTileK, kStep, false);
   if (ok && w->T4 > 0)
     ok = map_2d(&maps.w4, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->w4, kTileK / 2, (uint64_t)w->T4 * w->bN, kTileK / 2,
                 kTileK / 2, kStep, false);
   if (!ok) return cudaErrorInvalidValue;
-  return launch_pdl(linear_backward_kernel<NT>, dim3(std::min(a.units, num_sms())), dim3(kThreads), (size_t)Sh::kSmem,
-                    st, maps, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CG * std::min(a.units, num_sms() / CG));
+  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_pdl
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, linear_backward_kernel<NT, CG>, maps, a);
 }
 
 constexpr int kMaxBwdTokens = 1 << 21;
@@ -536,7 +652,7 @@ using namespace aq;
 extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) {
   if (validate_packed(w) != AQ_OK || M < 1 || M > kMaxBwdTokens) return 0;
   const BwdPlan p = plan_bwd(M, w->N, w->C);
-  return kWsHeader + (size_t)p.rest * p.S * p.nt * kTileK * sizeof(float);
+  return kWsHeader + (size_t)p.rest * p.S * p.cg * p.nt * kTileK * sizeof(float);
 }
 
 extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
@@ -565,14 +681,16 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
-  switch (p.nt) {
-    case 32: e = launch_bwd<32>(w, dy, ldd, a, st); break;
-    case 64: e = launch_bwd<64>(w, dy, ldd, a, st); break;
-    case 128: e = launch_bwd<128>(w, dy, ldd, a, st); break;
-    case 192: e = launch_bwd<192>(w, dy, ldd, a, st); break;
-    case 256: e = launch_bwd<256>(w, dy, ldd, a, st); break;
+  switch (p.cg * 1000 + p.nt) {
+    case 1032: e = launch_bwd<32, 1>(w, dy, ldd, a, st); break;
+    case 1064: e = launch_bwd<64, 1>(w, dy, ldd, a, st); break;
+    case 1128: e = launch_bwd<128, 1>(w, dy, ldd, a, st); break;
+    case 1256: e = launch_bwd<256, 1>(w, dy, ldd, a, st); break;
+    case 2256: e = launch_bwd<256, 2>(w, dy, ldd, a, st); break;
+    case 2512: e = launch_bwd<512, 2>(w, dy, ldd, a, st); break;
   }
   if (e == cudaSuccess && p.rest > 0)
-    e = launch_pdl(linear_backward_sum_kernel, dim3((p.nt * (kTileK / 4) + 255) / 256, p.rest), dim3(256), 0, st, a, p.nt);
+    e = launch_pdl(linear_backward_sum_kernel, dim3((p.nt * (kTileK / 4) + 255) / 256, p.rest * p.cg), dim3(256), 0, st, a,
+                   p.nt, p.cg);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

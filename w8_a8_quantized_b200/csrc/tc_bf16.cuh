@@ -7,15 +7,24 @@ namespace aq {
 namespace {
 
 #if defined(__CUDACC__)
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, one CTA.
+// D[tmem] (+)= A[smem] * B[smem]^T, bf16 x bf16 -> fp32, by one CTA or a pair of them.
+template <int CG = 1>
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: groups of 8 rows
@@ -30,10 +39,19 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr, uint32_t lead) {
   return d;
 }
 
-// Instruction descriptor: D fp32, A and B bf16, M = 128; mn_a / mn_b: the operand is MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool mn_a, bool mn_b) {
+// Instruction descriptor: D fp32, A and B bf16, M = 128 (256 for a pair); mn_a / mn_b: the operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool mn_a, bool mn_b, int m = 128) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)mn_a << 15) | ((uint32_t)mn_b << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// One lane of a converged warp.  MMAs and commits issued under it take 130 + 50 cycles per
+// four + two of them; under `lane == 0` in a diverged warp they took 360 + 220, since
+// their operands are then not known to be uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Ring position with its phase parity.
