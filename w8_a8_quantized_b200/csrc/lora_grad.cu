@@ -344,36 +344,37 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA
-      if (lane == 0) {
-        const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kTok * 128), bdesc0 = mn_desc(smem_u32(stage_b(0)), kTok * 128);
-        for (int i = 0; ok && i < n; ++i) {
-          const uint32_t step = list[i];
-          if ((step & kUnitStart) && !mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag)) {
-            fail(22);
-            ok = false;
-            break;
-          }
-          if (!mbar_wait(&b_full[br.i], br.ph, abort_flag) || !mbar_wait(&a_full[sr.i], sr.ph, abort_flag) ||
-              (!CODES && !mbar_wait(&a_tma[sr.i], sr.ph, abort_flag))) {
-            fail(23);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
+      const uint64_t adesc0 = mn_desc(smem_u32(stage_a(0)), kTok * 128), bdesc0 = mn_desc(smem_u32(stage_b(0)), kTok * 128);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t step = __shfl_sync(0xffffffffu, list[i], 0);
+        if ((step & kUnitStart) && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag))) {
+          fail(22);
+          ok = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag) &&
+                                         mbar_wait(&a_full[sr.i], sr.ph, abort_flag) &&
+                                         (CODES || mbar_wait(&a_tma[sr.i], sr.ph, abort_flag)))) {
+          fail(23);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ao = adesc0 + (uint64_t)((sr.i * Sh::kA) >> 4), bo = bdesc0 + (uint64_t)((br.i * Sh::kB) >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTok / 16; ++k)  // 16 tokens: two groups of eight rows
-            mma_bf16(tmem_base + ar.i * NB, ao + 128 * k, bo + 128 * k, Sh::kIdesc, !(step & kUnitStart) || k > 0);
+            mma_bf16(tmem + ar.i * NB, ao + 128 * k, bo + 128 * k, Sh::kIdesc, !(step & kUnitStart) || k > 0);
           mma_commit(&a_done[sr.i]);
           mma_commit(&b_done[br.i]);
-          issued = true;
-          sr.template next<SA>();
-          br.template next<SB>();
-          if (step & kUnitEnd) {
-            mma_commit(&acc_full[ar.i]);
-            ar.template next<2>();
-          }
+          if (step & kUnitEnd) mma_commit(&acc_full[ar.i]);
         }
+        __syncwarp();
+        issued = true;
+        sr.template next<SA>();
+        br.template next<SB>();
+        if (step & kUnitEnd) ar.template next<2>();
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------ terms
@@ -497,8 +498,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
         *reinterpret_cast<float4*>(a.g + (size_t)(row0 + a.rb0 + r) * a.D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  if (warp == 1 && lane == 0 && issued) {
-    mma_commit(drain);
+  if (warp == 1 && issued) {
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
     mbar_wait(drain, 0, never_flag);
   }
   if ((warp == 0 || warp == 2) && lane == 0 && (!ok || *abort_flag)) {

@@ -221,53 +221,58 @@ __global__ void __launch_bounds__(kSThreads, 2)
       if (!ok || *abort_flag) grace();
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(RC, false, false);
-      const uint64_t xdesc = sw128_desc(smem_u32(xbuf(0))), wdesc = sw128_desc(smem_u32(wbuf(0)));
-      Ring xr{0, 0}, wr{0, 0}, ar{0, 0};
-      bool issued = false;
-      for (int p0 = 0; ok && p0 < na; p0 += Sh::kCap) {
-        const int p1 = min(p0 + Sh::kCap, na);
-        for (int s = s0; ok && s < s1; ++s) {
-          const int in_unit = (s - s0) % kSUnit;
-          if (in_unit == 0 && !mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag)) {
-            fail(33);
+    constexpr uint32_t idesc = idesc_bf16(RC, false, false);
+    const uint64_t xdesc = sw128_desc(smem_u32(xbuf(0))), wdesc = sw128_desc(smem_u32(wbuf(0)));
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    Ring xr{0, 0}, wr{0, 0}, ar{0, 0};
+    bool issued = false;
+    for (int p0 = 0; ok && p0 < na; p0 += Sh::kCap) {
+      const int p1 = min(p0 + Sh::kCap, na);
+      for (int s = s0; ok && s < s1; ++s) {
+        const int in_unit = (s - s0) % kSUnit;
+        if (in_unit == 0 && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag))) {
+          fail(33);
+          ok = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&x_full[xr.i], xr.ph, abort_flag))) {
+          fail(34);
+          ok = false;
+          break;
+        }
+        for (int i = p0; i < p1; ++i) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&w_full[wr.i], wr.ph, abort_flag))) {
+            fail(35);
             ok = false;
             break;
           }
-          if (!mbar_wait(&x_full[xr.i], xr.ph, abort_flag)) {
-            fail(34);
-            ok = false;
-            break;
-          }
-          for (int i = p0; i < p1; ++i) {
-            if (!mbar_wait(&w_full[wr.i], wr.ph, abort_flag)) {
-              fail(35);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem_base + ar.i * kSCols + (i - p0) * RC;
-            const uint64_t xo = xdesc + (uint64_t)((xr.i * Sh::kX) >> 4), wo = wdesc + (uint64_t)((wr.i * kMaxTcRank * 128) >> 4);
+          tc_fence_after();
+          const uint32_t d = tmem + ar.i * kSCols + (i - p0) * RC;
+          const uint64_t xo = xdesc + (uint64_t)((xr.i * Sh::kX) >> 4), wo = wdesc + (uint64_t)((wr.i * kMaxTcRank * 128) >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_bf16(d, xo + 2 * k, wo + 2 * k, idesc, in_unit > 0 || k > 0);
             mma_commit(&w_free[wr.i]);
-            issued = true;
-            wr.template next<kSW>();
           }
-          if (!ok) break;
-          mma_commit(&x_free[xr.i]);
-          xr.template next<kSX>();
-          if (in_unit == kSUnit - 1 || s + 1 == s1) {
-            mma_commit(&acc_full[ar.i]);
-            ar.template next<2>();
-          }
+          __syncwarp();
+          issued = true;
+          wr.template next<kSW>();
         }
+        if (!ok) break;
+        const bool last = in_unit == kSUnit - 1 || s + 1 == s1;
+        if (elect_one()) {
+          mma_commit(&x_free[xr.i]);
+          if (last) mma_commit(&acc_full[ar.i]);
+        }
+        __syncwarp();
+        xr.template next<kSX>();
+        if (last) ar.template next<2>();
       }
-      if (issued) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, never_flag);
-      }
+    }
+    if (issued) {
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, never_flag);
     }
   } else if (warp >= 4) {
     const int w = warp & 3, row = 32 * w + lane, mine = q.slot[row];
@@ -511,35 +516,39 @@ __global__ void __launch_bounds__(kEThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(BN, false, true);
-      const uint64_t sdesc = sw128_desc(smem_u32(terms)), wdesc = mn_desc(smem_u32(wbase), t.rp * 128);
-      Ring wr{0, 0}, ar{0, 0};
-      bool issued = false;
-      for (int b = b0; ok && b < b1; ++b)
-        for (int i = 0; i < na; ++i) {
-          if (!mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag) || !mbar_wait(&w_full[wr.i], wr.ph, abort_flag)) {
-            fail(42);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int ks = (q.rank[i] + 15) / 16;
-          const uint64_t wo = wdesc + (uint64_t)((wr.i * wslot) >> 4);
+    constexpr uint32_t idesc = idesc_bf16(BN, false, true);
+    const uint64_t sdesc = sw128_desc(smem_u32(terms)), wdesc = mn_desc(smem_u32(wbase), t.rp * 128);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    Ring wr{0, 0}, ar{0, 0};
+    bool issued = false;
+    for (int b = b0; ok && b < b1; ++b)
+      for (int i = 0; i < na; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag) &&
+                                         mbar_wait(&w_full[wr.i], wr.ph, abort_flag))) {
+          fail(42);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int ks = __shfl_sync(0xffffffffu, (q.rank[i] + 15) / 16, 0);
+        const uint64_t wo = wdesc + (uint64_t)((wr.i * wslot) >> 4);
+        if (elect_one()) {
           for (int sp = Sh::kTerms - 1; sp >= 0; --sp)
             for (int k = 0; k < ks; ++k)
-              mma_bf16(tmem_base + ar.i * BN, sdesc + (uint64_t)((sp * kTok * 128) >> 4) + 2 * k, wo + 128 * k, idesc,
+              mma_bf16(tmem + ar.i * BN, sdesc + (uint64_t)((sp * kTok * 128) >> 4) + 2 * k, wo + 128 * k, idesc,
                        sp < Sh::kTerms - 1 || k > 0);
           mma_commit(&w_free[wr.i]);
           mma_commit(&acc_full[ar.i]);
-          issued = true;
-          wr.template next<kEW>();
-          ar.template next<kEAcc>();
         }
-      if (issued) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, never_flag);
+        __syncwarp();
+        issued = true;
+        wr.template next<kEW>();
+        ar.template next<kEAcc>();
       }
+    if (issued) {
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, never_flag);
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ table rows
