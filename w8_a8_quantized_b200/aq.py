@@ -601,8 +601,10 @@ AQ_LORA_MAX_RANK = 256
 
 
 _F32, _BF16 = torch.float32, torch.bfloat16
-# the current stream's handle without building a stream object (2 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _stream
+# the current stream's handle without building a stream object (2 us a call), and the cheaper forms of two queries
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int) -> int:
@@ -624,13 +626,19 @@ def _rows(t: torch.Tensor, name: str, dtypes, device, M: int, width: int) -> int
     raise ValueError(f"{name} must be [>= {M}][>= {width}] with unit inner stride and rows that do not overlap")
 
 
-def _matrix(t: torch.Tensor, name: str):
-    """Rows, columns and device of the 2-D tensor that sets a call's sizes."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+def _lead(t: torch.Tensor, name: str, device=None, width: int = 0):
+    """_rows of the 2-D bf16 tensor that sets a call's sizes: its rows, columns, leading
+    dimension and device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D torch.bfloat16 tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    return *t.shape, t.device
+    dev = t.device
+    if dev.type != "cuda" or (device is not None and dev != device):
+        raise ValueError(f"{name} must live on {device or 'a CUDA device'}")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 or cols < width or (ld < cols and rows > 1):
+        raise ValueError(f"{name} must be [M][>= {width}] with unit inner stride and rows that do not overlap")
+    return rows, cols, ld if rows > 1 else -(-cols // 16) * 16, dev
 
 
 def _exact(t: torch.Tensor, name: str, dtype, device, shape):
@@ -641,17 +649,28 @@ def _exact(t: torch.Tensor, name: str, dtype, device, shape):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {list(t.shape)}")
 
 
-def _new(like, rows: int, cols: int, dtype, device) -> torch.Tensor:
-    """A [rows][cols] tensor; the cheaper way where `like` has its shape and layout."""
-    if like is not None and like.dtype is dtype and like.shape == (rows, cols) and like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty((rows, cols), dtype=dtype, device=device)
+_shapes = {}
+
+
+def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """An uninitialised [rows][cols] tensor ([rows] for cols 0).  Made like a kept tensor of
+    that shape that has no storage, which is 1 us cheaper than torch.empty."""
+    key = rows, cols, dtype, device.index
+    like = _shapes.get(key)
+    if like is None:
+        if len(_shapes) >= 4096:
+            _shapes.clear()
+        with torch.inference_mode(False):
+            like = torch.empty((rows, cols) if cols else (rows,), dtype=dtype, device=device)
+        like.untyped_storage().resize_(0)
+        _shapes[key] = like
+    return torch.empty_like(like)
 
 
 def _call(fn, name: str, device, *args):
     """fn(*args, stream) with `device` current, on its current stream."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -712,9 +731,9 @@ def _stream_ws(tag: str, need: int, device) -> torch.Tensor:
     demand (threads may take turns on a stream between one call's launches: autograd
     runs backward passes in a thread of its own); a call that is captured into a graph
     gets its own, so that graphs share none."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         return torch.zeros(need, dtype=torch.uint8, device=device)
-    key = (device, tag, _raw_stream(device.index), threading.get_ident())
+    key = device.index, tag, _raw_stream(device.index), threading.get_ident()
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
         ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=device)
@@ -724,7 +743,7 @@ def _stream_ws(tag: str, need: int, device) -> torch.Tensor:
 def _own_ws(tag: str, need: int, device) -> torch.Tensor:
     if need == 0:
         raise ValueError("invalid arguments for a workspace")
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         return _stream_ws(tag, need, device)
     with torch.cuda.device(device):
         return _stream_ws(tag, need, device)
@@ -750,17 +769,16 @@ def aq_lora_apply(ad: Adapters, x: torch.Tensor, ids: torch.Tensor, y: torch.Ten
     ids int32 [M], y float32 or bfloat16 [M][N] (None: the adapters' part alone, in
     out_dtype).  out may be y.  s float32 [M][max_rank] receives the products that
     aq_lora_backward takes."""
-    M, _, _ = _matrix(x, "x")
     dev, N = ad.device, ad.N
-    ldx = _rows(x, "x", (_BF16,), dev, M, ad.K)
+    M, _, ldx, _ = _lead(x, "x", dev, ad.K)
     _exact(ids, "ids", torch.int32, dev, (M,))
     ldy = 0
     if y is not None:
         ldy, out_dtype = _rows(y, "y", (_F32, _BF16), dev, M, N), y.dtype
     if out is None:
-        out, ldo = _new(y, M, N, out_dtype, dev), N
-        if out_dtype not in (_F32, _BF16):
+        if out_dtype is not _F32 and out_dtype is not _BF16:
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+        out, ldo = _new(M, N, out_dtype, dev), N
     else:
         ldo = _rows(out, "out", (_F32, _BF16) if y is None else (out_dtype,), dev, M, N)
     if s is not None:
@@ -781,9 +799,8 @@ def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch
     8-bit checkpoint (int8 codes with token scales sx, as aq_quant_act made them)
     or bf16 (sx None).  dx = add + the adapters' part, in add's dtype (dx_dtype
     without add); dx may be add."""
-    M, _, _ = _matrix(dy, "dy")
     dev, N, K, R = ad.device, ad.N, ad.K, ad.R
-    ldd = _rows(dy, "dy", (_BF16,), dev, M, N)
+    M, _, ldd, _ = _lead(dy, "dy", dev, N)
     _exact(ids, "ids", torch.int32, dev, (M,))
     _exact(s, "s", _F32, dev, (M, ad.max_rank))
     ldx = _rows(x, "x", (_BF16,) if sx is None else (torch.int8,), dev, M, K)
@@ -795,17 +812,17 @@ def aq_lora_backward(ad: Adapters, dy: torch.Tensor, ids: torch.Tensor, s: torch
     if add is not None:
         ldadd, dx_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if dx is None and (want_dx or add is not None):
-        dx, lddx = _new(add, M, K, dx_dtype, dev), K
-        if dx_dtype not in (_F32, _BF16):
+        if dx_dtype is not _F32 and dx_dtype is not _BF16:
             raise TypeError("dx_dtype must be torch.float32 or torch.bfloat16")
+        dx, lddx = _new(M, K, dx_dtype, dev), K
     elif dx is not None:
         lddx = _rows(dx, "dx", (_F32, _BF16) if add is None else (dx_dtype,), dev, M, K)
     if da is None:
-        da = torch.empty((R, K), dtype=_F32, device=dev)
+        da = _new(R, K, _F32, dev)
     else:
         _exact(da, "da", _F32, dev, (R, K))
     if dbt is None:
-        dbt = torch.empty((R, N), dtype=_F32, device=dev)
+        dbt = _new(R, N, _F32, dev)
     else:
         _exact(dbt, "dbt", _F32, dev, (R, N))
     ws = _lora_ws(ad, M, 1, ws)
@@ -825,22 +842,22 @@ def aq_silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, keep: bool = False, 
     -> (hq int8 [M][F], sh float32 [M]), the down projection's input.  keep=True
     appends the 8-bit checkpoints of gate and up for aq_silu_mul_backward: (..., gq
     int8 [M][F], gs float32 [M][ceil(F/128)], uq, us)."""
-    M, F, dev = _matrix(gate, "gate")
-    ldg, ldu = _rows(gate, "gate", (_BF16,), dev, M, F), _rows(up, "up", (_BF16,), dev, M, F)
-    if up.shape != (M, F):
+    M, F, ldg, dev = _lead(gate, "gate")
+    m, f, ldu, _ = _lead(up, "up", dev)
+    if m != M or f != F:
         raise ValueError("gate and up must have one shape")
     if hq is None:
-        hq = torch.empty((M, F), dtype=torch.int8, device=dev)
+        hq = _new(M, F, torch.int8, dev)
     else:
         _exact(hq, "hq", torch.int8, dev, (M, F))
     if sh is None:
-        sh = torch.empty((M,), dtype=_F32, device=dev)
+        sh = _new(M, 0, _F32, dev)
     else:
         _exact(sh, "sh", _F32, dev, (M,))
     kept, ptrs = (), (None,) * 4
     if keep:
-        gs = torch.empty((M, -(-F // AQ_GATED_GROUP)), dtype=_F32, device=dev)
-        kept = torch.empty_like(hq), gs, torch.empty_like(hq), torch.empty_like(gs)
+        groups = -(-F // AQ_GATED_GROUP)
+        kept = tuple(_new(M, n, t, dev) for n, t in ((F, torch.int8), (groups, _F32)) * 2)
         ptrs = tuple(t.data_ptr() for t in kept)
     _call(lib().aq_silu_mul_quant, "aq_silu_mul_quant", dev, gate.data_ptr(), ldg, up.data_ptr(), ldu, M, F,
           hq.data_ptr(), sh.data_ptr(), *ptrs)
@@ -851,18 +868,18 @@ def aq_silu_mul_backward(dh: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, u
                          dgate: torch.Tensor = None, dup: torch.Tensor = None):
     """Gradients of silu(gate) * up from its 8-bit checkpoints: dh bf16 [M][F] ->
     (dgate, dup) bf16 [M][F]."""
-    M, F, dev = _matrix(dh, "dh")
-    ldd, groups = _rows(dh, "dh", (_BF16,), dev, M, F), -(-F // AQ_GATED_GROUP)
+    M, F, ldd, dev = _lead(dh, "dh")
+    groups = -(-F // AQ_GATED_GROUP)
     _exact(gq, "gq", torch.int8, dev, (M, F))
     _exact(uq, "uq", torch.int8, dev, (M, F))
     _exact(gs, "gs", _F32, dev, (M, groups))
     _exact(us, "us", _F32, dev, (M, groups))
     if dgate is None:
-        dgate, ldg = _new(dh, M, F, _BF16, dev), F
+        dgate, ldg = _new(M, F, _BF16, dev), F
     else:
         ldg = _rows(dgate, "dgate", (_BF16,), dev, M, F)
     if dup is None:
-        dup, ldu = _new(dh, M, F, _BF16, dev), F
+        dup, ldu = _new(M, F, _BF16, dev), F
     else:
         ldu = _rows(dup, "dup", (_BF16,), dev, M, F)
     _call(lib().aq_silu_mul_backward, "aq_silu_mul_backward", dev, dh.data_ptr(), ldd, gq.data_ptr(), gs.data_ptr(),
@@ -878,16 +895,15 @@ def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = N
                        out_dtype=torch.bfloat16, ws: torch.Tensor = None) -> torch.Tensor:
     """Input gradient of a packed projection: dx = add + dy W (W dequantized), dy bf16
     [M][N] -> [M][K] in add's dtype (out_dtype without add).  out may be add."""
-    M, _, _ = _matrix(dy, "dy")
     dev, K = w.device, w.K
-    ldd = _rows(dy, "dy", (_BF16,), dev, M, w.N)
+    M, _, ldd, _ = _lead(dy, "dy", dev, w.N)
     ldadd = 0
     if add is not None:
         ldadd, out_dtype = _rows(add, "add", (_F32, _BF16), dev, M, K), add.dtype
     if out is None:
-        out, ldo = _new(add, M, K, out_dtype, dev), K
-        if out_dtype not in (_F32, _BF16):
+        if out_dtype is not _F32 and out_dtype is not _BF16:
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+        out, ldo = _new(M, K, out_dtype, dev), K
     else:
         ldo = _rows(out, "out", (_F32, _BF16) if add is None else (out_dtype,), dev, M, K)
     if ws is not None:
