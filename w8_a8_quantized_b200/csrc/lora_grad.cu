@@ -514,27 +514,49 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   }
 }
 
-// g = the sum of the ranges' partial sums in range order, for one adapter and 1024 columns.
-__global__ void __launch_bounds__(256)
-    lora_sum_kernel(const float* __restrict__ p, const uint8_t* __restrict__ has, const int32_t* __restrict__ off,
-                    int splits, int R, int D, int max_rank, float* __restrict__ g) {
+// g = the sum of the ranges' partial sums in range order, for one adapter and 1024 columns
+// of one of the two gradients.
+struct SumJob {
+  const float* p;       // [splits][R][D]
+  const uint8_t* has;   // [L][splits]
+  float* g;
+  int splits, D, blocks;  // blocks of 1024 columns; 0: nothing to sum
+};
+struct SumArgs {
+  SumJob job[2];
+  const int32_t* off;
+  int R, max_rank;
+};
+
+__global__ void __launch_bounds__(256) lora_sum_kernel(const __grid_constant__ SumArgs a) {
+  const bool second = blockIdx.x >= a.job[0].blocks;
+  const SumJob& j = a.job[second];
+  const int l = blockIdx.y, d = ((blockIdx.x - (second ? a.job[0].blocks : 0)) * 256 + threadIdx.x) * 4;
   pdl_launch_dependents();
   pdl_wait();
-  const int l = blockIdx.y, d = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (d >= D) return;
-  const int row0 = min(max(__ldg(off + l), 0), R), row1 = min(row0 + max_rank, min(max(__ldg(off + l + 1), row0), R));
-  const uint8_t* mine = has + (size_t)l * splits;
+  if (d >= j.D) return;
+  const int row0 = min(max(__ldg(a.off + l), 0), a.R),
+            row1 = min(row0 + a.max_rank, min(max(__ldg(a.off + l + 1), row0), a.R));
+  const uint8_t* mine = j.has + (size_t)l * j.splits;
+  const size_t step = (size_t)a.R * j.D;
   for (int r = row0 + blockIdx.z; r < row1; r += gridDim.z) {
+    const float* p = j.p + (size_t)r * j.D + d;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < splits; ++k) {
-      if (!mine[k]) continue;
-      const float4 w = *reinterpret_cast<const float4*>(p + ((size_t)k * R + r) * D + d);
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
+    for (int k0 = 0; k0 < j.splits; k0 += 8) {  // eight loads on their way
+      float4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = k0 + i < j.splits && mine[k0 + i] ? __ldcg(reinterpret_cast<const float4*>(p + (k0 + i) * step))
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v.x += w[i].x;
+        v.y += w[i].y;
+        v.z += w[i].z;
+        v.w += w[i].w;
+      }
     }
-    *reinterpret_cast<float4*>(g + (size_t)r * D + d) = v;
+    *reinterpret_cast<float4*>(j.g + (size_t)r * j.D + d) = v;
   }
 }
 
@@ -598,7 +620,7 @@ cudaError_t launch_ranks(int ranks, const GradMaps& maps, const GradArgs& a, cud
 
 size_t lora_grad_ws_bytes(const aq_lora* ad, int M) {
   return align256((size_t)ceil_div(M, kTok) * 4) + 2 * terms_bytes(M, ad->max_rank) +
-         std::max(part_bytes(ad, M, ad->K), part_bytes(ad, M, ad->N));
+         part_bytes(ad, M, ad->K) + part_bytes(ad, M, ad->N);
 }
 
 cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
@@ -608,7 +630,9 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
   int32_t* info = reinterpret_cast<int32_t*>(at);
   at += align256((size_t)ceil_div(M, kTok) * 4);
   char* terms[2] = {at, at + terms_bytes(M, ad->max_rank)};
-  float* part = reinterpret_cast<float*>(at + 2 * terms_bytes(M, ad->max_rank));
+  at += 2 * terms_bytes(M, ad->max_rank);
+  SumArgs sum;
+  memset(&sum, 0, sizeof(sum));
   cudaError_t e = cudaSuccess;
   size_t off = 0;
   for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
@@ -624,7 +648,10 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
     const bool codes = !side && sx;
     float* out = side ? dbt : da;
     const int splits = grad_splits(M, D);
-    uint8_t* has = reinterpret_cast<uint8_t*>(part) + align256((size_t)splits * ad->R * D * sizeof(float));
+    float* part = reinterpret_cast<float*>(at);
+    uint8_t* has = reinterpret_cast<uint8_t*>(at) + align256((size_t)splits * ad->R * D * sizeof(float));
+    at += part_bytes(ad, M, D);
+    if (splits > 1) sum.job[side] = {part, has, out, splits, D, ceil_div(D, 1024)};
     off = 0;
     for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
       const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
@@ -640,10 +667,13 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
       e = codes ? launch_ranks<true>(rc, maps, a, st) : launch_ranks<false>(rc, maps, a, st);
       off += align256((size_t)M * npad * 2);
     }
-    if (e == cudaSuccess && splits > 1) {
-      e = launch_pdl(lora_sum_kernel, dim3(ceil_div(D, 1024), ad->L, std::min(ad->max_rank, 16)), dim3(256), 0, st, part, has, ad->off, splits, ad->R,
-                     D, ad->max_rank, out);
-    }
+  }
+  if (e == cudaSuccess && sum.job[0].blocks + sum.job[1].blocks > 0) {
+    sum.off = ad->off;
+    sum.R = ad->R;
+    sum.max_rank = ad->max_rank;
+    e = launch_pdl(lora_sum_kernel, dim3(sum.job[0].blocks + sum.job[1].blocks, ad->L, std::min(ad->max_rank, 16)), dim3(256),
+                   0, st, sum);
   }
   return e;
 }
