@@ -465,6 +465,28 @@ def test_gated_ties_round_to_even():
     assert list(rq[0]) == [127, 2, -2, 4, 0, 2, 0, -126, 4, -127, 0, 100, 100, -2, 8, 8]
 
 
+@pytest.mark.parametrize("exponent", [0, -20, 30, -33, -34, -40])
+def test_gated_checkpoints_of_every_ratio(exponent):
+    """Every bf16 mantissa as a group's largest with every value from it down to 2^-9 of
+    it: among them all quotients that are half-integers.  2^-33 and less: around the
+    scale's floor and below it."""
+    rest = np.concatenate([np.arange(128, 256) * 2.0 ** -d for d in range(10)])
+    groups = []
+    for a in range(128, 256):
+        x = rest[rest <= a]
+        x = np.concatenate([x, np.full(-len(x) % 126, float(a))]).reshape(-1, 126)
+        x[:, ::3] *= -1
+        groups.append(np.concatenate([np.full((len(x), 1), -float(a)), x, np.full((len(x), 1), a / 2)], 1))
+    v = np.concatenate(groups) * 2.0 ** (exponent - 7)
+    v = np.concatenate([v, np.zeros((-len(v) % 16, 128))]).reshape(-1, 16 * 128)
+    gate = torch.from_numpy(v).to("cuda").to(torch.bfloat16)
+    assert np.array_equal(host(gate), v)
+    _, _, gq, gs, uq, us = aq.aq_silu_mul_quant(gate, -gate, keep=True)
+    rq, rs = codes64(v, 128)
+    assert np.array_equal(gq.cpu().numpy(), rq) and np.array_equal(gs.cpu().numpy(), rs)
+    assert np.array_equal(uq.cpu().numpy(), -rq) and np.array_equal(us.cpu().numpy(), rs)
+
+
 @pytest.mark.parametrize("M,F", GATED)
 def test_gated_backward(M, F):
     g = rng(7 * M + F)

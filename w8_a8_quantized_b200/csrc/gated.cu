@@ -25,7 +25,7 @@
 // Then 1 + e: 1, rcp.approx 2, two products 2: h within 13.  The row's maximum
 // likewise, its product with R 2, the reciprocal 2: a quotient within 30,
 // 127 * 30 * 2^-24 < 2.3e-4.
-// Checkpoint quotients (x is exact): 127 * 3 * 2^-24 < 4e-5.
+// The checkpoints' codes need no test: see biased_inverse.
 #include <algorithm>
 
 #include "aq_internal.cuh"
@@ -36,7 +36,7 @@ namespace {
 constexpr int kGroup = 128;  // features per scale of a checkpoint: 16 threads x 8
 constexpr float kHMaxFast = 1e37f;  // rows with a larger |h| take fp64 throughout
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: see quantize8
-constexpr float kNearH = 0.5f - 2.5e-4f, kNearX = 0.5f - 4.5e-5f;
+constexpr float kNearH = 0.5f - 2.5e-4f;
 
 __device__ __forceinline__ double gated64(float g, float u) {
   const double gd = g;
@@ -82,21 +82,16 @@ __device__ __forceinline__ int code64(double x, double s) {
   return static_cast<int>(fmin(fmax(rint(x / s), -127.0), 127.0));
 }
 
-// clamp(rint(fl64(x / s))) of a bf16 x whose quotient t (fp32) is all but a
-// half-integer b, without the division: with r = b s - |x| (one rounding, so its
-// sign is right), the quotient rounds to b itself, and then to even, when |r| is
-// within half a unit of b times s (half of that below a power of two: b = 1/2).
-// Equal to the division for every pair of bf16 mantissas (checked).
-__device__ __forceinline__ int tie_code(float x, float t, double s) {
-  const float k = floorf(fabsf(t)), bf = k + 0.5f;
-  const double r = fma(static_cast<double>(bf), s, -static_cast<double>(fabsf(x)));
-  const int e = (__float_as_int(bf) >> 23) - 127;  // half a unit of b: 2^(e - 53)
-  const double half = s * __hiloint2double((e - 53 + 1023) << 20, 0);
-  const int ki = static_cast<int>(k);
-  int c = ki + (ki & 1);
-  if (r > (bf == 0.5f ? 0.5 * half : half)) c = ki;
-  if (-r > half) c = ki + 1;
-  return x < 0.f ? -c : c;
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint2 pack_codes(const uint32_t (&c)[8]) {
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
 // Codes of eight values; bit e of the result: element e is too near a half-integer.
@@ -111,12 +106,11 @@ __device__ __forceinline__ uint32_t codes8(const float2 (&x)[4], float r32, floa
     const float2 r = __ffma2_rn(x[i], r2, round2);
     const float2 k = __fadd2_rn(r, back2);
     d[i] = __ffma2_rn(x[i], r2, make_float2(-k.x, -k.y));
-    far = fmaxf(far, fmaxf(fabsf(d[i].x), fabsf(d[i].y)));
+    far = max3(far, fabsf(d[i].x), fabsf(d[i].y));
     c[2 * i] = __float_as_uint(r.x);
     c[2 * i + 1] = __float_as_uint(r.y);
   }
-  out = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
-                   __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+  out = pack_codes(c);
   uint32_t slow = 0;
   if (!(far <= limit)) {
 #pragma unroll
@@ -124,12 +118,6 @@ __device__ __forceinline__ uint32_t codes8(const float2 (&x)[4], float r32, floa
       slow |= (fabsf(d[i].x) <= limit ? 0u : 1u << (2 * i)) | (fabsf(d[i].y) <= limit ? 0u : 2u << (2 * i));
   }
   return slow;
-}
-
-__device__ __forceinline__ void put_code(uint2& out, int e, int code) {
-  const uint32_t sel = 0x3210u ^ ((4u ^ (e & 3)) << (4 * (e & 3)));  // byte e & 3 from the second operand
-  if (e < 4) out.x = __byte_perm(out.x, code, sel);
-  else out.y = __byte_perm(out.y, code, sel);
 }
 
 // Scale of a checkpoint group: fp32 of max(amax R, 1e-12) in fp64.  R1 has 16
@@ -140,40 +128,53 @@ __device__ __forceinline__ float scale32(float amax) {
   return fmaxf(fmaf(amax, kR2, amax * kR1), 1e-12f);
 }
 
+// Reciprocal of a checkpoint's scale `s` (fp32) that decides every code without a test.
+// With 8-bit mantissas the quotient x / s, about 127 x / amax, is either a half-integer
+// b up to the roundings of s and of the quotient, or 2^-16 b away from it.  127 is prime, so
+// the half-integers are b = 63.5, x = amax / 2, and all of them where amax has the mantissa
+// 254 / 128.  There s is a power of two and the quotients are exact: ties go to even by
+// themselves.  For the other mantissas the fp64 quotient at amax / 2 is below 63.5 for six
+// and not for the rest, so 1 / s is made 2^-19 smaller or larger: more than its own
+// error, 2^-22, and less than what would move any other quotient over a half-integer.  (Where
+// s is at its floor, 1e-12, none comes nearer than 8e-6 b.)
+__device__ __forceinline__ float biased_inverse(float s, float amax) {
+  constexpr uint32_t kBelow0 = 1u << 9 | 1u << 10 | 1u << 24 | 1u << 25;  // mantissas 128 + 9, 10, 24, 25
+  constexpr uint32_t kBelow1 = 1u << (41 - 32) | 1u << (56 - 32);        // 128 + 41, 56
+  const uint32_t bits = __float_as_uint(amax) >> 16, i = bits & 127;
+  const uint32_t below = (i < 32 ? kBelow0 : i < 64 ? kBelow1 : 0u) >> (i & 31) & 1u;
+  const float r = rcp_approx(s) * (below ? 1.f - 0x1p-19f : 1.f + 0x1p-19f);
+  return (__float_as_uint(s) & 0x7FFFFFu) == 0 ? __uint_as_float(0x7F000000u - __float_as_uint(s)) : r;  // 2^-e of 2^e
+}
+
+// Codes of eight values by a reciprocal that decides them.
+__device__ __forceinline__ uint2 decided8(const float2 (&x)[4], float r) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __ffma2_rn(x[i], make_float2(r, r), make_float2(kRound, kRound));
+    c[2 * i] = __float_as_uint(t.x);
+    c[2 * i + 1] = __float_as_uint(t.y);
+  }
+  return pack_codes(c);
+}
+
+// The largest |bf16| patterns of eight values, in two halves (they order as integers).
+__device__ __forceinline__ uint32_t max_pattern(const uint4& v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+
 // Checkpoints of g and u: codes and scales of one 128-feature group of each,
 // held by 16 neighbouring lanes.
-__device__ __forceinline__ void checkpoint8(const uint4& gv, const uint4& uv, const float2 (&g)[4],
-                                            const float2 (&u)[4], bool in, int8_t* gq, float* gs, int8_t* uq, float* us,
-                                            size_t qi, size_t si) {
-  // |bf16| patterns order as integers: both maxima in the halves of one word
-  const uint32_t a = __vmaxu2(__vmaxu2(gv.x & 0x7FFF7FFFu, gv.y & 0x7FFF7FFFu),
-                              __vmaxu2(gv.z & 0x7FFF7FFFu, gv.w & 0x7FFF7FFFu));
-  const uint32_t b = __vmaxu2(__vmaxu2(uv.x & 0x7FFF7FFFu, uv.y & 0x7FFF7FFFu),
-                              __vmaxu2(uv.z & 0x7FFF7FFFu, uv.w & 0x7FFF7FFFu));
-  uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+__device__ __forceinline__ void checkpoint8(uint32_t gmax, uint32_t umax, const float2 (&g)[4], const float2 (&u)[4],
+                                            bool in, int8_t* gq, float* gs, int8_t* uq, float* us, size_t qi, size_t si) {
+  uint32_t m = __vmaxu2(__byte_perm(gmax, umax, 0x5410), __byte_perm(gmax, umax, 0x7632));  // both maxima in one word
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ga = __uint_as_float(m << 16), ua = __uint_as_float(m & 0xFFFF0000u);
   const float sg = scale32(ga), su = scale32(ua);
-  uint2 cg, cu;
-  const float rg = rcp_approx(sg), ru = rcp_approx(su);
-  uint32_t slow = codes8(g, rg, kNearX, cg) | (codes8(u, ru, kNearX, cu) << 8);
-  if (!in) slow = 0;
-  // ties are common (0.3% of the elements: ratios of 8-bit mantissas times 127);
-  // one element per lane and round
-  while (__any_sync(0xffffffffu, slow != 0)) {
-    if (slow) {
-      const int i = __ffs(slow) - 1, e = i & 7;
-      slow &= slow - 1;
-      const float x = pick(i < 8 ? gv : uv, e);
-      const int code = tie_code(x, x * (i < 8 ? rg : ru), scale64(i < 8 ? ga : ua));
-      if (i < 8) put_code(cg, e, code);
-      else put_code(cu, e, code);
-    }
-  }
   if (in) {
-    *reinterpret_cast<uint2*>(gq + qi) = cg;
-    *reinterpret_cast<uint2*>(uq + qi) = cu;
+    *reinterpret_cast<uint2*>(gq + qi) = decided8(g, biased_inverse(sg, ga));
+    *reinterpret_cast<uint2*>(uq + qi) = decided8(u, biased_inverse(su, ua));
     if ((threadIdx.x & 15) == 0) {
       gs[si] = sg;
       us[si] = su;
@@ -215,14 +216,13 @@ __global__ void __launch_bounds__(MAXT, MINB)
     const uint4 gv = gl[i], uv = ul[i];
     const float2 g[4] = {widen2(gv.x), widen2(gv.y), widen2(gv.z), widen2(gv.w)};
     const float2 u[4] = {widen2(uv.x), widen2(uv.y), widen2(uv.z), widen2(uv.w)};
-    float low = 0.f;
+    const uint32_t gmax = max_pattern(gv);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = __fadd2_rn(exp_neg2(g[e]), make_float2(1.f, 1.f));
       h[i][e] = __fmul2_rn(__fmul2_rn(g[e], make_float2(rcp_approx(x.x), rcp_approx(x.y))), u[e]);
-      low = fminf(low, fminf(g[e].x, g[e].y));
     }
-    if (low < -80.f) {  // exp leaves fp32's range: the fp64 value, rounded
+    if ((gmax & 0xFFFFu) > 0x42A0u || gmax > 0x42A0FFFFu) {  // |g| > 80: exp may leave fp32's range: the fp64 value, rounded
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (g[e].x < -80.f) h[i][e].x = static_cast<float>(gated64(g[e].x, u[e].x));
@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(MAXT, MINB)
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(h[i][e].x), fabsf(h[i][e].y)));
+    for (int e = 0; e < 4; ++e) amax = max3(amax, fabsf(h[i][e].x), fabsf(h[i][e].y));
     if (KEEP)
-      checkpoint8(gv, uv, g, u, in, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
+      checkpoint8(gmax, max_pattern(uv), g, u, in, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
       const int v = threadIdx.x + i * threads;
       float big = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(h[i][e].x), fabsf(h[i][e].y)));
+      for (int e = 0; e < 4; ++e) big = max3(big, fabsf(h[i][e].x), fabsf(h[i][e].y));
       if (v < nvec && !(big < near)) {
         const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v);
         for (int e = 0; e < 8; ++e) {
