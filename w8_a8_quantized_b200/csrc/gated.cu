@@ -23,8 +23,7 @@
 // leading 16 bits of log2 e (with a bf16 g an exact product) and c = (log2 e - L1)
 // ln 2: ex2.approx 4, the dropped (c g)^2 / 2 below 2 for |g| <= 88, two roundings.
 // Then 1 + e: 1, rcp.approx 2, two products 2: h within 13.  The row's maximum
-// likewise, its product with R 2, the reciprocal 2: a quotient within 30,
-// 127 * 30 * 2^-24 < 2.3e-4.
+// likewise, its product with R 2, the reciprocal 2: a quotient within 30, 1.8e-6.
 // The checkpoints' codes need no test: see biased_inverse.
 #include <algorithm>
 
@@ -36,7 +35,7 @@ namespace {
 constexpr int kGroup = 128;  // features per scale of a checkpoint: 16 threads x 8
 constexpr float kHMaxFast = 1e37f;  // rows with a larger |h| take fp64 throughout
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: see quantize8
-constexpr float kNearH = 0.5f - 2.5e-4f;
+constexpr float kNearH = 1.85e-6f;  // relative error of a quotient of h
 
 __device__ __forceinline__ double gated64(float g, float u) {
   const double gd = g;
@@ -128,6 +127,13 @@ __device__ __forceinline__ float scale32(float amax) {
   return fmaxf(fmaf(amax, kR2, amax * kR1), 1e-12f);
 }
 
+// v >> n, 0 for any n above 31.
+__device__ __forceinline__ uint32_t shr_clamped(uint32_t v, uint32_t n) {
+  uint32_t r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+  return r;
+}
+
 // Reciprocal of a checkpoint's scale `s` (fp32) that decides every code without a test.
 // With 8-bit mantissas the quotient x / s, about 127 x / amax, is either a half-integer
 // b up to the roundings of s and of the quotient, or 2^-16 b away from it.  127 is prime, so
@@ -140,8 +146,8 @@ __device__ __forceinline__ float scale32(float amax) {
 __device__ __forceinline__ float biased_inverse(float s, float amax) {
   constexpr uint32_t kBelow0 = 1u << 9 | 1u << 10 | 1u << 24 | 1u << 25;  // mantissas 128 + 9, 10, 24, 25
   constexpr uint32_t kBelow1 = 1u << (41 - 32) | 1u << (56 - 32);        // 128 + 41, 56
-  const uint32_t bits = __float_as_uint(amax) >> 16, i = bits & 127;
-  const uint32_t below = (i < 32 ? kBelow0 : i < 64 ? kBelow1 : 0u) >> (i & 31) & 1u;
+  const uint32_t i = __float_as_uint(amax) >> 16 & 127;
+  const uint32_t below = (shr_clamped(kBelow0, i) | shr_clamped(kBelow1, i - 32u)) & 1u;
   const float r = rcp_approx(s) * (below ? 1.f - 0x1p-19f : 1.f + 0x1p-19f);
   return (__float_as_uint(s) & 0x7FFFFFu) == 0 ? __uint_as_float(0x7F000000u - __float_as_uint(s)) : r;  // 2^-e of 2^e
 }
@@ -158,28 +164,31 @@ __device__ __forceinline__ uint2 decided8(const float2 (&x)[4], float r) {
   return pack_codes(c);
 }
 
-// The largest |bf16| patterns of eight values, in two halves (they order as integers).
-__device__ __forceinline__ uint32_t max_pattern(const uint4& v) {
-  return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+// The largest |x| of eight bf16 values, one of each half.
+__device__ __forceinline__ uint32_t max_abs2(const uint4& v) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // Checkpoints of g and u: codes and scales of one 128-feature group of each,
 // held by 16 neighbouring lanes.
 __device__ __forceinline__ void checkpoint8(uint32_t gmax, uint32_t umax, const float2 (&g)[4], const float2 (&u)[4],
-                                            bool in, int8_t* gq, float* gs, int8_t* uq, float* us, size_t qi, size_t si) {
+                                            bool in, bool group_in, int8_t* gq, float* gs, int8_t* uq, float* us, size_t qi,
+                                            size_t si) {
   uint32_t m = __vmaxu2(__byte_perm(gmax, umax, 0x5410), __byte_perm(gmax, umax, 0x7632));  // both maxima in one word
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ga = __uint_as_float(m << 16), ua = __uint_as_float(m & 0xFFFF0000u);
-  const float sg = scale32(ga), su = scale32(ua);
+  // the first eight lanes see to g's scale, the others to u's
+  const bool us_half = threadIdx.x & 8;
+  const float amax = __uint_as_float(us_half ? m & 0xFFFF0000u : m << 16), scale = scale32(amax);
+  const float r = biased_inverse(scale, amax);
+  const float rg = __shfl_sync(0xffffffffu, r, 0, 16), ru = __shfl_sync(0xffffffffu, r, 8, 16);
   if (in) {
-    *reinterpret_cast<uint2*>(gq + qi) = decided8(g, biased_inverse(sg, ga));
-    *reinterpret_cast<uint2*>(uq + qi) = decided8(u, biased_inverse(su, ua));
-    if ((threadIdx.x & 15) == 0) {
-      gs[si] = sg;
-      us[si] = su;
-    }
+    *reinterpret_cast<uint2*>(gq + qi) = decided8(g, rg);
+    *reinterpret_cast<uint2*>(uq + qi) = decided8(u, ru);
   }
+  if ((threadIdx.x & 7) == 0 && group_in) *(us_half ? us + si : gs + si) = scale;
 }
 
 // One CTA per row; a thread holds CV vectors of 8 h values in registers.  The
@@ -208,7 +217,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     ul[i] = v < nvec ? __ldg(urow + v) : make_uint4(0, 0, 0, 0);
   }
   float2 h[CV][4];
-  float amax = 0.f;
+  float big[CV], amax = 0.f;  // the vectors' largest |h|, the row's
 #pragma unroll
   for (int i = 0; i < CV; ++i) {
     const int v = threadIdx.x + i * threads;
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     const uint4 gv = gl[i], uv = ul[i];
     const float2 g[4] = {widen2(gv.x), widen2(gv.y), widen2(gv.z), widen2(gv.w)};
     const float2 u[4] = {widen2(uv.x), widen2(uv.y), widen2(uv.z), widen2(uv.w)};
-    const uint32_t gmax = max_pattern(gv);
+    const uint32_t gmax = max_abs2(gv);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = __fadd2_rn(exp_neg2(g[e]), make_float2(1.f, 1.f));
@@ -230,9 +239,10 @@ __global__ void __launch_bounds__(MAXT, MINB)
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = max3(amax, fabsf(h[i][e].x), fabsf(h[i][e].y));
+    for (int e = 0; e < 4; ++e) big[i] = max3(e ? big[i] : 0.f, fabsf(h[i][e].x), fabsf(h[i][e].y));
+    amax = fmaxf(amax, big[i]);
     if (KEEP)
-      checkpoint8(gmax, max_pattern(uv), g, u, in, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
+      checkpoint8(gmax, max_abs2(uv), g, u, in, (v & ~15) < nvec, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -250,10 +260,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
     for (int i = 0; i < CV; ++i) {
       const int v = threadIdx.x + i * threads;
-      float big = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) big = max3(big, fabsf(h[i][e].x), fabsf(h[i][e].y));
-      if (v < nvec && !(big < near)) {
+      if (v < nvec && !(big[i] < near)) {
         const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v);
         for (int e = 0; e < 8; ++e) {
           const float2 p = e < 4 ? (e < 2 ? h[i][0] : h[i][1]) : (e < 6 ? h[i][2] : h[i][3]);
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     const int v = threadIdx.x + i * threads;
     if (v < nvec) {
       uint2 c;
-      const uint32_t slow = codes8(h[i], r32, kNearH, c);
+      const uint32_t slow = codes8(h[i], r32, fmaf(big[i] * r32, -kNearH, 0.5f - 1e-6f), c);
       undecided[i / 4] |= (wide ? 0xFFu : slow) << (8 * (i & 3));
       reinterpret_cast<uint2*>(hq + (size_t)m * F)[v] = c;
     }
