@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     silu_mul_quant_kernel(const uint16_t* __restrict__ gate, int ldg, const uint16_t* __restrict__ up, int ldu, int F,
                           int8_t* __restrict__ hq, float* __restrict__ sh, int8_t* __restrict__ gq,
                           float* __restrict__ gs, int8_t* __restrict__ uq, float* __restrict__ us) {
-  __shared__ float red[MAXT / 32];
+  __shared__ uint32_t red[MAXT / 32];  // the warps' largest |h|
   __shared__ unsigned long long top;  // bits of the row's largest fp64 |h| (non-negative doubles order as integers)
   const int m = blockIdx.x, threads = blockDim.x;
   const uint4* grow = reinterpret_cast<const uint4*>(gate + (size_t)m * ldg);
@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(MAXT, MINB)
   uint4 gl[CV], ul[CV];
 #pragma unroll
   for (int i = 0; i < CV; ++i) {
-    const int v = threadIdx.x + i * threads;
-    gl[i] = v < nvec ? __ldg(grow + v) : make_uint4(0, 0, 0, 0);
-    ul[i] = v < nvec ? __ldg(urow + v) : make_uint4(0, 0, 0, 0);
+    const int v = min(threadIdx.x + i * threads, nvec - 1);  // behind the end: the last again, in its own group
+    gl[i] = __ldg(grow + v);
+    ul[i] = __ldg(urow + v);
   }
   float2 h[CV][4];
   float big[CV], amax = 0.f;  // the vectors' largest |h|, the row's
@@ -244,12 +244,12 @@ __global__ void __launch_bounds__(MAXT, MINB)
     if (KEEP)
       checkpoint8(gmax, max_abs2(uv), g, u, in, (v & ~15) < nvec, gq, gs, uq, us, (size_t)m * F + (size_t)v * 8, (size_t)m * groups + v / 16);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+  // (non-negative floats order as integers)
+  const uint32_t of_warp = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = of_warp;
   __syncthreads();
-  amax = red[0];
-  for (int w = 1; w < threads / 32; ++w) amax = fmaxf(amax, red[w]);
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < threads / 32 ? red[lane] : 0u));
   const bool wide = !(amax < kHMaxFast);
 
   // the exact maximum: redo every element that may be it (none where the scale
