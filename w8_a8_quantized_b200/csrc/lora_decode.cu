@@ -96,50 +96,63 @@ __device__ __forceinline__ void put8(const DecodeArgs& a, int m, int n, const fl
   }
 }
 
-// This CTA's columns k0 .. k0 + kn of S for TT tokens: 16 lanes per table row, two
-// rows per warp and load, U loads on their way; sent to every CTA of the cluster.
-template <int TT, int U>
+// This CTA's columns k0 .. k0 + kn of S for TT tokens: 16 lanes per table row, RP rows
+// per half warp with U loads each on their way; sent to every CTA of the cluster.
+template <int TT, int RP, int U>
 __device__ __forceinline__ void contract(const DecodeArgs& a, const uint16_t* xs, uint32_t part_addr, int c, int row0,
                                          int rank, int k0, int kn, float scale, int T) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
-  for (int r0 = 2 * warp; r0 < rank; r0 += 2 * kWarps) {
+  for (int r0 = 2 * warp; r0 < rank; r0 += 2 * kWarps * RP) {
     const int r = r0 + (lane >> 4);
-    const uint16_t* row = a.a + (size_t)(row0 + min(r, rank - 1)) * a.K + k0;
-    float acc[TT];
+    const uint16_t* row = a.a + (size_t)(row0 + r) * a.K + k0;
+    float acc[RP][TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = 0.f;
+    for (int j = 0; j < RP; ++j)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[j][t] = 0.f;
     for (int kb = sub * kVec; kb < kn; kb += U * 16 * kVec) {
-      uint4 w[U];
+      uint4 w[RP][U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = kb + i * 16 * kVec;
-        w[i] = k < kn ? __ldg(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
-      }
+      for (int j = 0; j < RP; ++j)
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int k = kb + i * 16 * kVec;
+          w[j][i] = k < kn && r + 2 * kWarps * j < rank
+                        ? __ldg(reinterpret_cast<const uint4*>(row + (size_t)(2 * kWarps * j) * a.K + k))
+                        : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int k = kb + i * 16 * kVec;
         if (k < kn) {
-          float wf[8];
-          widen8(w[i], wf);
 #pragma unroll
           for (int t = 0; t < TT; ++t) {
             if (t < T) {
               float xf[8];
               widen8(*reinterpret_cast<const uint4*>(xs + t * a.kslice + k), xf);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[t] = fmaf(wf[e], xf[e], acc[t]);
+              for (int j = 0; j < RP; ++j) {
+                float wf[8];
+                widen8(w[j][i], wf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[j][t] = fmaf(wf[e], xf[e], acc[j][t]);
+              }
             }
           }
         }
       }
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
+    for (int j = 0; j < RP; ++j)
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-      if (t < T && r < rank && sub < kCl)
-        store_peer(peer_smem(part_addr + (uint32_t)(((c * a.max_rank + r) * kT + t) * 4), sub), scale * acc[t]);
-    }
+      for (int t = 0; t < TT; ++t) {
+        const int rj = r + 2 * kWarps * j;
+        if (r0 + 2 * kWarps * j >= rank) continue;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) acc[j][t] += __shfl_xor_sync(0xffffffffu, acc[j][t], o);
+        if (t < T && rj < rank && sub < kCl)
+          store_peer(peer_smem(part_addr + (uint32_t)(((c * a.max_rank + rj) * kT + t) * 4), sub), scale * acc[j][t]);
+      }
   }
 }
 
@@ -295,11 +308,15 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads, 3) lora_
   const float scale = __ldg(a.scale + v);
   cluster_wait();
   __syncthreads();
+  // as many rows on their way as a row's columns leave room for (64 tokens of 40 adapters, K
+  // 2560: 17.9 us with two rows of four loads, 20.4 with one of eight)
   if (T == 1) {
-    contract<1, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    if (a.kslice <= 512) contract<1, 2, 4>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    else contract<1, 1, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
     spread<F32, 1, 8>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
   } else {
-    contract<kT, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    if (a.kslice <= 512) contract<kT, 2, 4>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
+    else contract<kT, 1, 8>(a, xs, smem_u32(part), c, row0, rank, k0, kn, scale, T);
     spread<F32, kT, 8>(a, part, sums, red, row0, rank, n0, n1, tok, T, keep);
   }
 }
