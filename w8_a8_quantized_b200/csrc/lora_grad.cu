@@ -394,7 +394,12 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
       }
     } else if (warp >= 4 && warp < 4 + kXf) {
       // ------------------------------------------------------------ transform
-      const int t = tid - 128, c = t & 15, r0 = t >> 4;
+      // 16 codes of a row per thread and round, rows 16 apart: two chunks at fixed offsets.
+      // Threads of the second 64 columns write theirs in the other order, so that the
+      // eight threads of a row always write eight different 16-byte columns.
+      const int t = tid - 128, c = t & 7, r0 = t >> 3, late = c >> 2;
+      const int first = late * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + late) ^ (r0 & 7)) << 4);
+      const int second = late * (kTok * 128) + r0 * 128 + (((2 * (c & 3) + 1 - late) ^ (r0 & 7)) << 4);
       for (int i = 0; ok && i < n; ++i) {
         const bool mixed = list[i] & kMixed;
         const int m0 = (base + (int)(list[i] & 0x1FF)) * kTok;
@@ -408,20 +413,23 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
           break;
         }
         if (CODES) {
-          const uint8_t* src = raw_slot(rr.i);
-          uint8_t* dst = stage_a(sr.i) + (c >> 3) * (kTok * 128);
+          const uint8_t* src = raw_slot(rr.i) + r0 * kD + c * 16;
+          uint8_t* dst = stage_a(sr.i);
+          uint4 v[kTok / 16];
 #pragma unroll
-          for (int k = 0; k < kTok / 8; ++k) {
-            const int r = r0 + 8 * k;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                widen_codes8(*reinterpret_cast<const uint2*>(src + r * kD + c * 8));
+          for (int k = 0; k < kTok / 16; ++k) v[k] = *reinterpret_cast<const uint4*>(src + k * 16 * kD);
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k) {
+            const uint4 lo = widen_codes8(make_uint2(v[k].x, v[k].y)), hi = widen_codes8(make_uint2(v[k].z, v[k].w));
+            *reinterpret_cast<uint4*>(dst + first + k * 2048) = late ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + second + k * 2048) = late ? lo : hi;
           }
         }
         if (mixed) {
           // rows of tokens that this adapter does not have: two lanes per row, the
           // rows that this warp itself has written
           __syncwarp();
-          const int w2 = 2 * (warp - 4), r = w2 + (lane >> 4) + 8 * ((lane & 15) >> 1), half = lane & 1, m = m0 + r;
+          const int r = 4 * (warp - 4) + (lane >> 1 & 3) + 16 * (lane >> 3), half = lane & 1, m = m0 + r;
           if (m >= a.M || __ldg(a.ids + m) != slot_id[list[i] >> kSlotShift]) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
             for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stage_a(sr.i) + half * 8192 + r * 128 + q * 16) = zero;
