@@ -499,9 +499,13 @@ Products products(const aq_lora* ad, int M, bool b_side) {
   return lora_tc_fits(ad, M) ? Products{lora_tc_splits(M, t.D), (t.max_rank + 15) / 16 * 16}
                              : Products{shrink_splits(M, t), t.max_rank};
 }
-size_t p_bytes(const aq_lora* ad, int M, bool b_side) {
+size_t sum_bytes(const aq_lora* ad, int M, bool b_side) {
   const Products p = products(ad, M, b_side);
   return align256((size_t)p.splits * M * p.ld * sizeof(float));
+}
+// with the tiles' adapter counts behind them
+size_t p_bytes(const aq_lora* ad, int M, bool b_side) {
+  return sum_bytes(ad, M, b_side) + (lora_tc_fits(ad, M) ? align256(lora_tc_count_bytes(M)) : 0);
 }
 
 cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p, cudaStream_t st) {
@@ -534,14 +538,16 @@ cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, in
 // p = the products of x with the a (or b) side; out = y + p's sums times the other side.
 cudaError_t shrink_any(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p,
                        void* header, cudaStream_t st) {
-  return lora_tc_fits(ad, M) ? launch_lora_shrink_tc(ad, b_side, x, ldx, ids, M, p, header, st)
+  int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(p) + sum_bytes(ad, M, b_side));
+  return lora_tc_fits(ad, M) ? launch_lora_shrink_tc(ad, b_side, x, ldx, ids, M, p, counts, header, st)
                              : shrink(b_side ? table_b(ad) : table_a(ad), x, ldx, ids, M, p, st);
 }
 cudaError_t expand_any(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, const void* y, int ldy,
                        void* out, int ldo, int dtype, float* s, void* header, cudaStream_t st) {
   const int splits = products(ad, M, !b_side).splits;
+  const int32_t* counts = reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(p) + sum_bytes(ad, M, !b_side));
   return lora_tc_fits(ad, M)
-             ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, y, ldy, out, ldo, dtype == AQ_F32, s, header, st)
+             ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, counts, y, ldy, out, ldo, dtype == AQ_F32, s, header, st)
              : expand(b_side ? table_b(ad) : table_a(ad), ids, M, p, splits, y, ldy, out, ldo, dtype, s, st);
 }
 

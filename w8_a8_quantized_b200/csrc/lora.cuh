@@ -12,15 +12,16 @@ cudaError_t launch_lora_decode(const aq_lora* ad, const uint16_t* x, int ldx, co
 
 // More than 64 tokens, ranks up to 64 (lora_tc.cu).  Shrink: p [splits][M][rp] (rp =
 // max_rank rounded up to 16) from the a side or the b side of the tables; expand:
-// out = y + p's sums times the other side.  `header`: the error word of the call's
-// workspace.
+// out = y + p's sums times the other side.  `counts`: lora_tc_count_bytes, written by the
+// one for the other.  `header`: the error word of the call's workspace.
 bool lora_tc_fits(const aq_lora* ad, int M);
 int lora_tc_splits(int M, int D);
+size_t lora_tc_count_bytes(int M);
 cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M,
-                                  float* p, void* header, cudaStream_t st);
+                                  float* p, int32_t* counts, void* header, cudaStream_t st);
 cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
-                                  const void* y, int ldy, void* out, int ldo, bool f32, float* s, void* header,
-                                  cudaStream_t st);
+                                  const int32_t* counts, const void* y, int ldy, void* out, int ldo, bool f32, float* s,
+                                  void* header, cudaStream_t st);
 
 // Weight gradients (lora_grad.cu): t [tsplits][M][ldt] partial sums of the
 // output's gradient times B, s [M][max_rank] the forward products.  `header`: the

@@ -107,6 +107,7 @@ struct ShrinkTcArgs {
   const int32_t* ids;
   int M, splits;
   float* p;
+  int32_t* counts;  // [tiles]: adapters of a tile, for the expansion
   void* ws;
 };
 
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
   pdl_wait();
   list_tile(t, a.ids, m0, a.M, q);
   const int na = q.n;
+  if (tid == 0 && split == 0) a.counts[blockIdx.x] = na;
   if (na == 0) return;
   if (warp == 1) {
     tmem_alloc(tmem_slot, 2 * kSCols);
@@ -346,7 +348,9 @@ struct ExpandMaps {
 struct ExpandTcArgs {
   TcTable t;
   const int32_t* ids;
+  const int32_t* counts;
   int M, splits, has_y, in_place;
+  int tiles, g, extra;  // CTAs of a tile, and those left for tiles of several adapters
   const float* p;  // [splits][M][rp]
   float* s;        // [M][max_rank] or null
   void* ws;
@@ -411,10 +415,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
   TcList& q = *reinterpret_cast<TcList*>(ctrl + Sh::kCtrl);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int m0 = blockIdx.y * kTok;
-  const int blocks = (t.D + BN - 1) / BN;
-  const int b0 = (int)((long long)blocks * blockIdx.x / gridDim.x);
-  const int b1 = (int)((long long)blocks * (blockIdx.x + 1) / gridDim.x);
+  __shared__ int place[3], sums[2][kEThreads / 32];
   if (tid == 0) {
     for (int i = 0; i < kEY; ++i) {
       mbar_init(&y_full[i], 1);
@@ -441,14 +442,52 @@ __global__ void __launch_bounds__(kEThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  list_tile(t, a.ids, m0, a.M, q);
+  // This CTA's tile and its part of the tile's columns.  A block of columns takes as much
+  // again for every further adapter of the tile, so the CTAs that g per tile leave go to
+  // tiles of several adapters, in proportion to those beyond the first.  (4001 tokens of six
+  // requests, 4096 -> 14336, five of 32 tiles with two: 66 us, 77 without.)
+  int tile = (int)blockIdx.x < a.tiles * a.g ? (int)blockIdx.x / a.g : -1, part = (int)blockIdx.x % a.g, parts = a.g;
+  if (a.extra > 0) {
+    const int more = tid < a.tiles ? max(__ldcg(a.counts + tid) - 1, 0) : 0;
+    const int of_warp = __reduce_add_sync(0xffffffffu, more);
+    if (lane == 0) sums[0][warp] = of_warp;
+    if (tid == 0) place[0] = -1;
+    __syncthreads();
+    int total = 0;
+    for (int i = 0; i < kEThreads / 32; ++i) total += sums[0][i];
+    const int share = total > 0 ? a.extra * more / total : 0;
+    int end = share;  // of the tiles up to this thread's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    if (lane == 31) sums[1][warp] = end;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) end += sums[1][i];
+    const int j = (int)blockIdx.x - a.tiles * a.g;
+    if (tile >= 0 ? tid == tile : j >= end - share && j < end) {
+      place[0] = tid;
+      place[1] = tile >= 0 ? part : a.g + j - (end - share);
+      place[2] = a.g + share;
+    }
+    __syncthreads();
+    tile = place[0];
+    part = place[1];
+    parts = place[2];
+  }
+  const int M = tile >= 0 ? a.M : 0;  // (a CTA without a part has no tokens and no columns)
+  const int m0 = max(tile, 0) * kTok, blocks = tile >= 0 ? (t.D + BN - 1) / BN : 0;
+  const int b0 = tile >= 0 ? (int)((long long)blocks * part / parts) : 0;
+  const int b1 = tile >= 0 ? (int)((long long)blocks * (part + 1) / parts) : 0;
+  list_tile(t, a.ids, m0, M, q);
   const int na = q.n;
 
   // S as bf16 terms in the 128-byte swizzle, eight ranks per thread and round
   const int per_row = t.rp / 8;
   for (int i = tid; i < kTok * per_row; i += kEThreads) {
     const int r = i / per_row, c8 = i - r * per_row, m = m0 + r;
-    if (m >= a.M) continue;
+    if (m >= M) continue;
     const int mine = q.slot[r], rank = mine >= 0 ? q.rank[mine] : 0;
     float v[8] = {};
     if (8 * c8 < rank) {
@@ -466,7 +505,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     for (int e = 0; e < 8; ++e) {
       if (8 * c8 + e >= rank) v[e] = 0.f;
       split3(v[e], h[0][e], h[1][e], h[2][e]);
-      if (a.s && blockIdx.x == 0 && 8 * c8 + e < t.max_rank) a.s[(size_t)m * t.max_rank + 8 * c8 + e] = v[e];
+      if (a.s && part == 0 && 8 * c8 + e < t.max_rank) a.s[(size_t)m * t.max_rank + 8 * c8 + e] = v[e];
     }
 #pragma unroll
     for (int k = 0; k < Sh::kTerms; ++k) {
@@ -704,24 +743,28 @@ cudaError_t launch_shrink(const ShrinkMaps& maps, const ShrinkTcArgs& a, cudaStr
 }
 
 template <bool F32, int EW>
-cudaError_t launch_expand(const ExpandMaps& maps, const ExpandTcArgs& a, cudaStream_t st) {
+cudaError_t launch_expand(const ExpandMaps& maps, ExpandTcArgs a, cudaStream_t st) {
   using Sh = ExpandTcShape<F32, EW>;
   cudaError_t e = ensure_smem_attr<lora_expand_tc_kernel<F32, EW>>(Sh::smem(EW == 3 ? kMaxTcRank : 32));
   if (e != cudaSuccess) return e;
   // column ranges per tile: the fewest blocks on the longest path, counting the
   // start of a CTA (list, terms, first copies) as four blocks
   const int tiles = ceil_div(a.M, kTok), blocks = ceil_div(a.t.D, Sh::kBN), sms = num_sms();
-  int best = 1;
+  a.tiles = tiles;
+  a.g = 1;
   long long cost = 0;
   for (int waves = 1; waves <= 6; ++waves) {
     const int g = std::max(1, std::min(blocks, waves * sms / tiles));
     const long long c = (long long)ceil_div((long long)tiles * g, sms) * (ceil_div(blocks, g) + 4);
     if (cost == 0 || c < cost) {
       cost = c;
-      best = g;
+      a.g = g;
     }
   }
-  return launch_pdl(lora_expand_tc_kernel<F32, EW>, dim3(best, tiles), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st, maps, a);
+  // the rest of the last wave (a thread of the kernel looks after each tile)
+  a.extra = a.t.L > 1 && tiles <= kEThreads && a.g < blocks ? ceil_div((long long)tiles * a.g, sms) * sms - tiles * a.g : 0;
+  return launch_pdl(lora_expand_tc_kernel<F32, EW>, dim3(tiles * a.g + a.extra), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st,
+                    maps, a);
 }
 
 }  // namespace
@@ -734,15 +777,17 @@ int lora_tc_splits(int M, int D) {
   return std::max(1, std::min({2 * num_sms() / tiles, steps / 8, 16}));
 }
 
+size_t lora_tc_count_bytes(int M) { return (size_t)ceil_div(M, kTok) * 4; }
+
 cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M,
-                                  float* p, void* header, cudaStream_t st) {
+                                  float* p, int32_t* counts, void* header, cudaStream_t st) {
   const TcTable t = table(ad, b_side);
   ShrinkMaps maps;
   memset(&maps, 0, sizeof(maps));
   if (!map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, t.D, M, (uint64_t)ldx * 2, 64, kTok, true) ||
       !map_2d(&maps.w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t.w, t.D, t.R, (uint64_t)t.D * 2, 64, t.rp, true))
     return cudaErrorInvalidValue;
-  const ShrinkTcArgs a{t, ids, M, lora_tc_splits(M, t.D), p, header};
+  const ShrinkTcArgs a{t, ids, M, lora_tc_splits(M, t.D), p, counts, header};
   switch (t.rp) {
     case 16: return launch_shrink<16>(maps, a, st);
     case 32: return launch_shrink<32>(maps, a, st);
@@ -753,8 +798,8 @@ cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t
 }
 
 cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
-                                  const void* y, int ldy, void* out, int ldo, bool f32, float* s, void* header,
-                                  cudaStream_t st) {
+                                  const int32_t* counts, const void* y, int ldy, void* out, int ldo, bool f32, float* s,
+                                  void* header, cudaStream_t st) {
   const TcTable t = table(ad, b_side);
   ExpandMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -763,7 +808,7 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
   if (!map_2d(&maps.out, type, out, t.D, M, (uint64_t)ldo * elt, 128 / elt, kTok, true) ||
       (y && !map_2d(&maps.y, type, y, t.D, M, (uint64_t)ldy * elt, 128 / elt, kTok, true)))
     return cudaErrorInvalidValue;
-  const ExpandTcArgs a{t, ids, M, splits, y != nullptr, y == out, p, s, header};
+  const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, p, s, header};
   if (t.rp <= 32) return f32 ? launch_expand<true, 5>(maps, a, st) : launch_expand<false, 5>(maps, a, st);
   return f32 ? launch_expand<true, 3>(maps, a, st) : launch_expand<false, 3>(maps, a, st);
 }
