@@ -12,7 +12,8 @@
 // 64 x 128 x 3r multiplications.
 //
 // A CTA takes 128 columns and a range of tokens, whoever's they are, so that
-// unequal adapters do not make unequal CTAs.  It lists its steps beforehand, (adapter,
+// unequal adapters do not make unequal CTAs; where that leaves room on the GPU (short
+// batches), several share a range's adapters.  It lists its steps beforehand, (adapter,
 // 64 tokens) pairs ordered by adapter, and runs through them without a pause at an
 // adapter's end (a pause cost 5 us).  Where a 64 holds
 // other adapters' tokens too, their rows are cleared in shared memory on both sides,
@@ -38,7 +39,7 @@ constexpr int kThreads = 384;
 constexpr int kUnit = 8;       // steps summed in tensor memory
 constexpr int kXf = 4, kEpi = 4;  // warps
 constexpr int kMaxAdapters = 16384;
-constexpr int kListCap = 768, kSlotCap = 64;  // steps and adapters listed at once
+constexpr int kListCap = 512, kSlotCap = 64;  // steps and adapters listed at once
 
 // A listed step: which 64 tokens of the range, whether others' tokens are among them, the
 // bounds of a unit and of its adapter, and the adapter's slot.
@@ -136,7 +137,7 @@ struct GradShape {
   static constexpr int kSB = NB <= 48 ? (CODES ? 6 : 4) : NB <= 96 ? 3 : 5;
   static constexpr int kRaw = CODES ? (NB <= 96 ? 3 : 5) : 0;  // 8 KiB each
   static constexpr int kTmem = 2 * NB <= 128 ? 128 : 2 * NB <= 256 ? 256 : 512;
-  static constexpr int kCtrl = 512 + kListCap * 4 + 3 * kSlotCap * 4 + kMaxAdapters / 8;
+  static constexpr int kCtrl = 512 + kListCap * 4 + 4 * kSlotCap * 4 + kThreads * 4 + kMaxAdapters / 8;
   static constexpr int kSmem = 1024 + kSA * kA + kSB * kB + kRaw * kTok * kD + kCtrl;
   static constexpr uint32_t kIdesc = idesc_bf16(NB, true, true);
   static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory");
@@ -199,15 +200,16 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_flag = abort_flag + 1;
-  volatile int* count = abort_flag + 2;  // [2][12] steps of each warp
   volatile uint32_t* list = reinterpret_cast<volatile uint32_t*>(reinterpret_cast<uint8_t*>(raw_full) + 512);
   volatile int* slot_id = reinterpret_cast<volatile int*>(list + kListCap);  // adapter, first gradient row, ranks
   volatile int* slot_row = slot_id + kSlotCap;
   volatile int* slot_nr = slot_row + kSlotCap;
-  uint32_t* present = reinterpret_cast<uint32_t*>(const_cast<int*>(slot_nr + kSlotCap));
+  volatile int* slot_steps = slot_nr + kSlotCap;
+  volatile int* kinds = slot_steps + kSlotCap;  // `info` of the range's 64s
+  uint32_t* present = reinterpret_cast<uint32_t*>(const_cast<int*>(kinds + kThreads));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int d0 = blockIdx.x * kD, split = blockIdx.y;
+  const int d0 = blockIdx.x * kD, split = blockIdx.y, share = blockIdx.z, shares = gridDim.z;
   if (tid == 0) {
     for (int i = 0; i < RW; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -256,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   const int chunks = (a.M + kTok - 1) / kTok;
   const int c0 = (int)((long long)chunks * split / a.splits), c1 = (int)((long long)chunks * (split + 1) / a.splits);
   const int own = c0 + tid < c1 ? __ldg(a.info + c0 + tid) : -1;
-  const unsigned mixed_lanes = __ballot_sync(0xffffffffu, own == -2);
+  kinds[tid] = own;
   if (own >= 0) atomicOr(&present[own >> 5], 1u << (own & 31));
-  for (unsigned left = mixed_lanes; left; left &= left - 1) {  // a warp reads a mixed 64 together
+  for (unsigned left = __ballot_sync(0xffffffffu, own == -2); left; left &= left - 1) {  // a warp reads a mixed 64 together
     const int m0 = (c0 + 32 * warp + __ffs(left) - 1) * kTok;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -267,6 +269,17 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     }
   }
   __syncthreads();
+  // which of the 64s base .. base + 31 have tokens of adapter l
+  auto steps_of = [&](int l, int base) {
+    const int kind = kinds[base + lane];
+    bool take = kind == l;
+    for (unsigned left = __ballot_sync(0xffffffffu, kind == -2); left; left &= left - 1) {
+      const int m = (c0 + base + __ffs(left) - 1) * kTok + lane;
+      const bool has = (m < a.M && __ldg(a.ids + m) == l) || (m + 32 < a.M && __ldg(a.ids + m + 32) == l);
+      if (__any_sync(0xffffffffu, has) && lane == __ffs(left) - 1) take = true;
+    }
+    return __ballot_sync(0xffffffffu, take);
+  };
 
   Ring sr{0, 0}, br{0, 0}, rr{0, 0}, ar{0, 0};  // activations, terms, codes, accumulator
   bool ok = true, issued = false;
@@ -274,49 +287,103 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
 #pragma unroll
   for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
 
-  for (int l = 0; l < a.L;) {
-    // list the steps of the next adapters
-    int n = 0, slots = 0, turn = 0;
-    for (; l < a.L && slots < kSlotCap; ++l) {
-      const uint32_t bits = present[l >> 5] >> (l & 31);
-      if (bits == 0) {  // none up to the word's end
-        l |= 31;
-        continue;
+  for (int done = 0;;) {
+    // The next of this CTA's adapters (every shares-th of the present ones); each warp finds
+    // them for itself ...
+    int seen = 0;
+    for (int w0 = 0; w0 < (a.L + 31) / 32; w0 += 32) {
+      uint32_t bits = w0 + lane < (a.L + 31) / 32 ? present[w0 + lane] : 0u;
+      const int mine = __popc(bits);
+      int upto = mine;
+      if (a.L > 32) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
       }
-      l += __ffs(bits) - 1;
-      const int row0 = min(max(__ldg(a.off + l), 0), a.R);
-      const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
-      if (nr <= 0) continue;
-      bool take = own == l;
-      for (unsigned left = mixed_lanes; left; left &= left - 1) {
-        const int m = (c0 + 32 * warp + __ffs(left) - 1) * kTok + lane;
-        const bool has = (m < a.M && __ldg(a.ids + m) == l) || (m + 32 < a.M && __ldg(a.ids + m + 32) == l);
-        if (__any_sync(0xffffffffu, has) && lane == __ffs(left) - 1) take = true;
+      for (int i = seen + upto - mine; bits; bits &= bits - 1, ++i) {
+        const int slot = i / shares - done;
+        if (i % shares == share && slot >= 0 && slot < kSlotCap) slot_id[slot] = 32 * (w0 + lane) + __ffs(bits) - 1;
       }
-      const unsigned vote = __ballot_sync(0xffffffffu, take);
-      if (lane == 0) count[12 * turn + warp] = __popc(vote);
-      __syncthreads();
-      int at = __popc(vote & ((1u << lane) - 1)), mine = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const int c = count[12 * turn + w];
-        if (w < warp) at += c;
-        mine += c;
+      seen += __shfl_sync(0xffffffffu, upto, a.L > 32 ? 31 : 0);
+    }
+    __syncwarp();
+    const int left = (seen > share ? (seen - share + shares - 1) / shares : 0) - done, named = min(left, kSlotCap);
+    if (left <= 0) break;
+    auto ranks_of = [&](int l, int& row0) {
+      row0 = min(max(__ldg(a.off + l), 0), a.R);
+      return min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
+    };
+    // lane's 64, the at-th of an adapter with `steps`
+    auto put = [&](int first, int at, int steps, int slot, int k) {
+      list[first + at] = (uint32_t)k | (kinds[k] == -2 ? kMixed : 0u) | (at % kUnit == 0 ? kUnitStart : 0u) |
+                         (at % kUnit == kUnit - 1 || at + 1 == steps ? kUnitEnd : 0u) | (at + 1 == steps ? kLast : 0u) |
+                         ((uint32_t)slot << kSlotShift);
+    };
+    const unsigned below = (1u << lane) - 1;
+    int slots = 1, n = 0;
+    if (named == 1) {
+      // ... one: each warp counts its steps and lists those of 32 64s ...
+      const int l = slot_id[0];
+      int row0, before = 0;
+      unsigned which = 0;
+      const int nr = ranks_of(l, row0);
+      for (int base = 0; base < c1 - c0; base += 32) {
+        const unsigned steps = nr > 0 ? steps_of(l, base) : 0u;
+        if (base == 32 * warp) {
+          which = steps;
+          before = n;
+        }
+        n += __popc(steps);
       }
-      turn ^= 1;
-      if (n + mine > kListCap) break;  // (at most 384 of one adapter: the list holds two)
-      if (take)
-        list[n + at] = (uint32_t)tid | (own == -2 ? kMixed : 0u) | (at % kUnit == 0 ? kUnitStart : 0u) |
-                       (at % kUnit == kUnit - 1 || at + 1 == mine ? kUnitEnd : 0u) | (at + 1 == mine ? kLast : 0u) |
-                       ((uint32_t)slots << kSlotShift);
+      if (which >> lane & 1u) put(0, before + __popc(which & below), n, 0, 32 * warp + lane);
       if (tid == 0) {
-        slot_id[slots] = l;
-        slot_row[slots] = row0 + a.rb0;
-        slot_nr[slots] = nr;
+        slot_row[0] = row0 + a.rb0;
+        slot_nr[0] = nr;
       }
-      n += mine;
-      ++slots;
+    } else {
+      // ... several: their rows and the number of their steps, an adapter per warp ...
+      for (int i = warp; i < named; i += kThreads / 32) {
+        const int l = slot_id[i];
+        int row0, steps = 0;
+        const int nr = ranks_of(l, row0);
+        if (nr > 0)
+          for (int base = 0; base < c1 - c0; base += 32) steps += __popc(steps_of(l, base));
+        if (lane == 0) {
+          slot_row[i] = row0 + a.rb0;
+          slot_nr[i] = nr;
+          slot_steps[i] = steps;
+        }
+      }
+      __syncthreads();
+      // ... and the steps, of as many adapters as the list holds (384 steps of one at most)
+      int end0 = lane < named ? slot_steps[lane] : 0, end1 = lane + 32 < named ? slot_steps[lane + 32] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v0 = __shfl_up_sync(0xffffffffu, end0, o), v1 = __shfl_up_sync(0xffffffffu, end1, o);
+        if (lane >= o) {
+          end0 += v0;
+          end1 += v1;
+        }
+      }
+      end1 += __shfl_sync(0xffffffffu, end0, 31);
+      slots = __popc(__ballot_sync(0xffffffffu, lane < named && end0 <= kListCap)) +
+              __popc(__ballot_sync(0xffffffffu, lane + 32 < named && end1 <= kListCap));
+      n = __shfl_sync(0xffffffffu, slots > 32 ? end1 : end0, (slots - 1) & 31);
+      for (int i = warp; i < slots; i += kThreads / 32) {
+        const int l = slot_id[i], steps = slot_steps[i];
+        const int first = __shfl_sync(0xffffffffu, i < 32 ? end0 : end1, i & 31) - steps;
+        int before = 0;
+        for (int base = 0; before < steps && base < c1 - c0; base += 32) {
+          const unsigned which = steps_of(l, base);
+          if (which >> lane & 1u) put(first, before + __popc(which & below), steps, i, base + lane);
+          before += __popc(which);
+        }
+      }
     }
     __syncthreads();
+    done += slots;
     const int base = c0;
 
     if (warp == 0) {
@@ -493,12 +560,12 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
 
   // adapters without tokens here: noted for the sum, or zeros where there is none
   if (a.splits > 1) {
-    if (blockIdx.x == 0 && a.rb0 == 0)
+    if (blockIdx.x == 0 && share == 0 && a.rb0 == 0)
       for (int l = tid; l < a.L; l += kThreads) a.has[(size_t)l * a.splits + split] = (present[l >> 5] >> (l & 31)) & 1u;
   } else {
     // a warp per adapter, four columns a lane (D is a multiple of 8)
     const int d = d0 + 4 * lane;
-    for (int l = warp; l < a.L; l += kThreads / 32) {
+    for (int l = warp + share * (kThreads / 32); l < a.L; l += shares * (kThreads / 32)) {
       if ((present[l >> 5] >> (l & 31)) & 1u) continue;
       const int row0 = min(max(__ldg(a.off + l), 0), a.R);
       const int nr = min(min(min(max(__ldg(a.off + l + 1), row0), a.R) - row0, a.max_rank) - a.rb0, Sh::kRanks);
@@ -581,10 +648,12 @@ size_t terms_bytes(int M, int max_rank) {
   return b;
 }
 
-// Token ranges: at most 384 64s each; the fewest steps on the longest path over two
-// CTAs per SM, counting a CTA's start and end as ten.
-int grad_splits(int M, int D) {
-  const int chunks = ceil_div(M, kTok), blocks = ceil_div(D, kD), slots = 2 * num_sms();
+int grad_slots(int max_rank) { return (max_rank <= 32 ? 2 : 1) * num_sms(); }  // see GradShape
+
+// Token ranges: at most 384 64s each; the fewest steps on the longest path, counting a
+// CTA's start and end as ten.
+int grad_splits(int M, int D, int max_rank) {
+  const int chunks = ceil_div(M, kTok), blocks = ceil_div(D, kD), slots = grad_slots(max_rank);
   const int least = ceil_div(chunks, kThreads);
   int best = least;
   long long cost = 0;
@@ -599,27 +668,33 @@ int grad_splits(int M, int D) {
   return best;
 }
 
+// CTAs that share the adapters of one range and column block: as many as fit in one wave.
+// (Rows of the gradients are an adapter's own, so there is nothing to sum.)
+int grad_shares(const aq_lora* ad, int D, int splits) {
+  return std::max(1, std::min(ad->L, grad_slots(ad->max_rank) / (ceil_div(D, kD) * splits)));
+}
+
 size_t part_bytes(const aq_lora* ad, int M, int D) {
-  const int s = grad_splits(M, D);
+  const int s = grad_splits(M, D, ad->max_rank);
   return s > 1 ? align256((size_t)s * ad->R * D * sizeof(float)) + align256((size_t)ad->L * s) : 0;
 }
 
 template <int NB, bool CODES>
-cudaError_t launch_shape(const GradMaps& maps, const GradArgs& a, cudaStream_t st) {
+cudaError_t launch_shape(const GradMaps& maps, const GradArgs& a, int shares, cudaStream_t st) {
   using Sh = GradShape<NB, CODES>;
   cudaError_t e = ensure_smem_attr<lora_grad_kernel<NB, CODES>>(Sh::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.splits), dim3(kThreads),
+  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.splits, shares), dim3(kThreads),
                     (size_t)Sh::kSmem, st, maps, a);
 }
 
 template <bool CODES>
-cudaError_t launch_ranks(int ranks, const GradMaps& maps, const GradArgs& a, cudaStream_t st) {
+cudaError_t launch_ranks(int ranks, const GradMaps& maps, const GradArgs& a, int shares, cudaStream_t st) {
   switch (ranks) {
-    case 16: return launch_shape<48, CODES>(maps, a, st);
-    case 32: return launch_shape<96, CODES>(maps, a, st);
-    case 48: return launch_shape<144, CODES>(maps, a, st);
-    case 64: return launch_shape<192, CODES>(maps, a, st);
+    case 16: return launch_shape<48, CODES>(maps, a, shares, st);
+    case 32: return launch_shape<96, CODES>(maps, a, shares, st);
+    case 48: return launch_shape<144, CODES>(maps, a, shares, st);
+    case 64: return launch_shape<192, CODES>(maps, a, shares, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -655,7 +730,7 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
     const int D = side ? ad->N : ad->K;
     const bool codes = !side && sx;
     float* out = side ? dbt : da;
-    const int splits = grad_splits(M, D);
+    const int splits = grad_splits(M, D, ad->max_rank), shares = grad_shares(ad, D, splits);
     float* part = reinterpret_cast<float*>(at);
     uint8_t* has = reinterpret_cast<uint8_t*>(at) + align256((size_t)splits * ad->R * D * sizeof(float));
     at += part_bytes(ad, M, D);
@@ -672,7 +747,7 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
                          : map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, D, M, (uint64_t)ldx * 2, 64, kTok, true));
       if (!ok) return cudaErrorInvalidValue;
       const GradArgs a{ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb, splits > 1 ? part : out, splits, has, header};
-      e = codes ? launch_ranks<true>(rc, maps, a, st) : launch_ranks<false>(rc, maps, a, st);
+      e = codes ? launch_ranks<true>(rc, maps, a, shares, st) : launch_ranks<false>(rc, maps, a, shares, st);
       off += align256((size_t)M * npad * 2);
     }
   }
