@@ -13,8 +13,8 @@
 //   D[128 k][NT tokens] += W'[64 n][128 k]^T dY[NT tokens][64 n]^T
 // with W' as the A operand, MN-major, so that the codes keep the packed order
 // (k contiguous) and no transposition is needed, and dY as the B operand,
-// K-major as it lies in memory.  Long sequences run in pairs of CTAs (cta_group::2):
-// a tile column each, every CTA holding half of the tokens' dY, which both use.
+// K-major as it lies in memory.  Long sequences run in pairs of CTAs (cta_group::2),
+// a tile column each and half of the tokens' dY, which both use.
 //
 // Roles in one CTA (persistent over work units, every role walks the same
 // sequence of steps g = 0, 1, 2, ...):
@@ -28,16 +28,16 @@
 //                groups of four warps that take steps in turn (one step's chain of waits and
 //                latencies, 1000 cycles, is longer than its MMAs, 512 for 256 tokens)
 //   the rest     epilogue: tensor memory -> add -> dx, while the next unit runs in
-//                the other accumulator buffer; units of 512 tokens take both, and have a
-//                group of four warps for each
+//                the other accumulator buffer; units of 384 or 512 tokens take both, and
+//                have a group of four warps for each
 // The weights are read before the previous kernel has finished; dY, add, dx and
 // the workspace are not touched before.
 //
 // What bounds it: the transform with 256 tokens a unit (step 810 cycles), the tensor pipe
 // with 512 (step 1100 of 1024 cycles; each dequantized tile serves twice the products), and
-// for long calls the power: 8192 x 14336 x 4096 (n x k) takes 1010 us in single CTAs, 910 in
-// pairs with 256 tokens and 740 with 512 (1.3 PFLOP/s; a library product sustains 1.38);
-// 2048 x 2560 x 9728 101, 95 and 85.
+// for long calls the power: 8192 tokens x 14336 n x 4096 k take 1010 us in single CTAs, 910
+// in pairs with 256 tokens and 740 with 512 (1.3 PFLOP/s; a library product sustains 1.38);
+// 2048 x 2560 x 9728 101, 95 and 84; 2048 x 9728 x 2560 102, 92 and 98, and 87 with 384.
 //
 // Whole units go to the CTAs as long as every CTA gets one; the units that are left
 // (all of them for short sequences) may be split over n so that they fill the GPU once
@@ -586,7 +586,7 @@ struct BwdForm {
   int cg, nt, step, unit;
 };
 constexpr BwdForm kBwdForms[] = {{1, 32, 40, 30},   {1, 64, 40, 40},   {1, 128, 40, 60},
-                                 {1, 256, 45, 120}, {2, 256, 41, 120}, {2, 512, 60, 400}};
+                                 {1, 256, 45, 120}, {2, 256, 41, 120}, {2, 384, 50, 300}, {2, 512, 60, 400}};
 
 // The form and the splits of least time: the steps of the CTA that has most, its units'
 // ends, and for a split the second launch with its 4 bytes written and read per sum.
@@ -687,6 +687,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
     case 1128: e = launch_bwd<128, 1>(w, dy, ldd, a, st); break;
     case 1256: e = launch_bwd<256, 1>(w, dy, ldd, a, st); break;
     case 2256: e = launch_bwd<256, 2>(w, dy, ldd, a, st); break;
+    case 2384: e = launch_bwd<384, 2>(w, dy, ldd, a, st); break;
     case 2512: e = launch_bwd<512, 2>(w, dy, ldd, a, st); break;
   }
   if (e == cudaSuccess && p.rest > 0)

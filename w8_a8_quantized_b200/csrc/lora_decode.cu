@@ -12,7 +12,7 @@
 //
 // B's columns are cut into as many clusters as the GPU has room for in one wave (each
 // forms S anew, from L2): what a CTA does one row after another is what takes its time
-// (rank 64, N 9728, K 2560, one token: 12 us with one cluster, 7.8 with five).  For the
+// (rank 64, N 9728, K 2560, one token: 12 us with one cluster, 7.8 with five, 6.3 with two rows of a half warp at once).  For the
 // same reason a cluster takes two tokens of an adapter and not four, whose sums would
 // leave registers for half the rows on their way.
 #include <algorithm>

@@ -8,8 +8,9 @@
 // so one pass over x serves all three; codes are exact in bf16.  Both operands are
 // MN-major, that is, as they lie in memory.  A first kernel writes the terms
 // (zeros behind a token's rank) and says of each 64 tokens whether one adapter has
-// them all.  It is bound by the bytes of x: 64 x 128 of them per step against
-// 64 x 128 x 3r multiplications.
+// them all.  On paper the bytes of x bound it, 64 x 128 of them per step against 64 x 128 x 3r
+// multiplications; in practice a step's chain of waits and its conversion (940 of 2000 cycles,
+// two CTAs per SM): 8192 x 14336 codes, ranks 16 to 32, take 60 us, 30% of the copy rate.
 //
 // A CTA takes 128 columns and a range of tokens, whoever's they are, so that
 // unequal adapters do not make unequal CTAs; where that leaves room on the GPU (short

@@ -1,7 +1,8 @@
 // Adapters of more than 64 tokens (prefill, training) on the 5th-generation tensor
 // cores, ranks up to 64: the two contractions of lora.cu over tiles of 128 tokens.
 // Both are bound by the bytes of the long axis (x; y and out), so everything around
-// the products is there to keep TMA copies in flight.
+// the products is there to keep TMA copies in flight.  Expanding 8192 tokens to 14336 columns
+// (bf16) takes 90 us: at the copy rate while it runs, after 8 us of waiting, list and terms.
 //
 // A tile's adapters are listed once.  Products of each adapter go to accumulator
 // columns of its own and a token's row takes those of its adapter: a row is never
