@@ -314,6 +314,10 @@ SIZES = [  # M, N, K, ranks, ids: the smallest and the longest axes, the most ad
     (66, 1 << 20, 16, [2, 1], segment_ids(66, 2, 2)),
     (100, 64, 48, [1] * 16383, [(m * m * 163) % 16383 for m in range(100)]),
     (1500, 136, 64, [1 + l % 3 for l in range(500)], mixed_ids(1500, 500, 11)),
+    (66100, 64, 80, [3, 5, 2], segment_ids(66100, 3, 3)),
+    # three of twelve tiles have two to four adapters; 5 tokens and as many adapters
+    (1500, 4096, 2048, [16, 8, 30, 24, 12, 5], [0] * 140 + [1] * 20 + [2] * 30 + [3] * 500 + [4] * 500 + [5] * 310),
+    (5, 192, 1152, [16 + l for l in range(35)], [3, 17, 34, 9, 3]),
 ]
 
 
@@ -746,3 +750,34 @@ def test_two_threads_on_one_stream():
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert len(g) == 20 and all(torch.equal(p, q) for o in g for p, q in zip(o, w))
+
+
+@pytest.mark.parametrize("M,N,K", [(1500, 2560, 4096), (1030, 2560, 9728), (2048, 9728, 2560), (2048, 2560, 9728)])
+def test_linear_backward_in_graphs_on_two_streams(M, N, K):
+    """Captured and replayed on new gradients, beside eager calls of another stream and an
+    adapter's backward pass of a third."""
+    w, _ = packed(N, K, 128, 0.5, 1)
+    dy, other = normal(rng(1), M, N), normal(rng(2), M, N)
+    aq.aq_linear_backward(w, dy)
+    want_other = aq.aq_linear_backward(w, other)
+    c = LoraCase(300, 512, 640, [12, 40], segment_ids(300, 2, 6), seed=6)
+    s = torch.empty(300, 40, device="cuda")
+    aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    want_lora = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, c.x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = aq.aq_linear_backward(w, dy)
+    side, third = torch.cuda.Stream(), torch.cuda.Stream()
+    for seed in (3, 4):
+        dy.copy_(normal(rng(seed), M, N))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            graph.replay()
+            with torch.cuda.stream(side):
+                got_other = aq.aq_linear_backward(w, other)
+            with torch.cuda.stream(third):
+                got_lora = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, c.x)
+        torch.cuda.synchronize()
+        assert torch.equal(got, aq.aq_linear_backward(w, dy)) and torch.equal(got_other, want_other)
+        assert all(torch.equal(p, q) for p, q in zip(got_lora, want_lora))
