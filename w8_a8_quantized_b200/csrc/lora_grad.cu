@@ -159,6 +159,7 @@ struct GradArgs {
   int M, D, L, R, max_rank, rb0;
   float* g;       // [splits][R][D]
   int splits;
+  int blocks, shares;  // CTAs along the columns, and those that share a range's adapters
   uint8_t* has;   // [L][splits]: whether the range has tokens of the adapter
   void* ws;
 };
@@ -178,8 +179,7 @@ __device__ __forceinline__ uint4 widen_codes8(uint2 w) {
 }
 
 template <int NB, bool CODES>
-__global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
-    lora_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs a) {
+__device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a, int index) {
   using Sh = GradShape<NB, CODES>;
   constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = CODES ? Sh::kRaw : 1;
   extern __shared__ uint8_t smem_raw[];
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
   uint32_t* present = reinterpret_cast<uint32_t*>(const_cast<int*>(kinds + kThreads));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int d0 = blockIdx.x * kD, split = blockIdx.y, share = blockIdx.z, shares = gridDim.z;
+  const int block = index % a.blocks, share = index / a.blocks % a.shares, split = index / a.blocks / a.shares;
+  const int d0 = block * kD, shares = a.shares;
   if (tid == 0) {
     for (int i = 0; i < RW; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
 
   // adapters without tokens here: noted for the sum, or zeros where there is none
   if (a.splits > 1) {
-    if (blockIdx.x == 0 && share == 0 && a.rb0 == 0)
+    if (block == 0 && share == 0 && a.rb0 == 0)
       for (int l = tid; l < a.L; l += kThreads) a.has[(size_t)l * a.splits + split] = (present[l >> 5] >> (l & 31)) & 1u;
   } else {
     // a warp per adapter, four columns a lane (D is a multiple of 8)
@@ -588,6 +589,21 @@ __global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
     tc_fence_after();
     tmem_dealloc(tmem_base, Sh::kTmem);
   }
+}
+
+// Both gradients in one launch, that of A first.
+struct GradJobs {
+  GradMaps maps[2];
+  GradArgs args[2];
+};
+template <int NB, bool CODES>
+__global__ void __launch_bounds__(kThreads, GradShape<NB, CODES>::kPerSm)
+    lora_grad_kernel(const __grid_constant__ GradJobs j) {
+  const int first = j.args[0].blocks * j.args[0].shares * j.args[0].splits, side = (int)blockIdx.x >= first;
+  if (CODES && side == 0)
+    grad_cta<NB, CODES>(j.maps[0], j.args[0], blockIdx.x);
+  else
+    grad_cta<NB, false>(j.maps[side], j.args[side], blockIdx.x - (side ? first : 0));
 }
 
 // g = the sum of the ranges' partial sums in range order, for one adapter and 1024 columns
@@ -651,10 +667,10 @@ size_t terms_bytes(int M, int max_rank) {
 
 int grad_slots(int max_rank) { return (max_rank <= 32 ? 2 : 1) * num_sms(); }  // see GradShape
 
-// Token ranges: at most 384 64s each; the fewest steps on the longest path, counting a
-// CTA's start and end as ten.
-int grad_splits(int M, int D, int max_rank) {
-  const int chunks = ceil_div(M, kTok), blocks = ceil_div(D, kD), slots = grad_slots(max_rank);
+// Token ranges, the same for both gradients: at most 384 64s each; the fewest steps on the
+// longest path, counting a CTA's start and end as ten.
+int grad_splits(const aq_lora* ad, int M) {
+  const int chunks = ceil_div(M, kTok), blocks = ceil_div(ad->K, kD) + ceil_div(ad->N, kD), slots = grad_slots(ad->max_rank);
   const int least = ceil_div(chunks, kThreads);
   int best = least;
   long long cost = 0;
@@ -671,31 +687,33 @@ int grad_splits(int M, int D, int max_rank) {
 
 // CTAs that share the adapters of one range and column block: as many as fit in one wave.
 // (Rows of the gradients are an adapter's own, so there is nothing to sum.)
-int grad_shares(const aq_lora* ad, int D, int splits) {
-  return std::max(1, std::min(ad->L, grad_slots(ad->max_rank) / (ceil_div(D, kD) * splits)));
+int grad_shares(const aq_lora* ad, int splits) {
+  const int blocks = ceil_div(ad->K, kD) + ceil_div(ad->N, kD);
+  return std::max(1, std::min(ad->L, grad_slots(ad->max_rank) / std::max(1, blocks * splits)));
 }
 
 size_t part_bytes(const aq_lora* ad, int M, int D) {
-  const int s = grad_splits(M, D, ad->max_rank);
+  const int s = grad_splits(ad, M);
   return s > 1 ? align256((size_t)s * ad->R * D * sizeof(float)) + align256((size_t)ad->L * s) : 0;
 }
 
 template <int NB, bool CODES>
-cudaError_t launch_shape(const GradMaps& maps, const GradArgs& a, int shares, cudaStream_t st) {
-  using Sh = GradShape<NB, CODES>;
-  cudaError_t e = ensure_smem_attr<lora_grad_kernel<NB, CODES>>(Sh::kSmem);
+cudaError_t launch_shape(const GradJobs& j, cudaStream_t st) {
+  constexpr int smem = std::max(GradShape<NB, CODES>::kSmem, GradShape<NB, false>::kSmem);
+  cudaError_t e = ensure_smem_attr<lora_grad_kernel<NB, CODES>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ceil_div(a.D, kD), a.splits, shares), dim3(kThreads),
-                    (size_t)Sh::kSmem, st, maps, a);
+  int ctas = 0;
+  for (const GradArgs& a : j.args) ctas += a.blocks * a.shares * a.splits;
+  return launch_pdl(lora_grad_kernel<NB, CODES>, dim3(ctas), dim3(kThreads), (size_t)smem, st, j);
 }
 
 template <bool CODES>
-cudaError_t launch_ranks(int ranks, const GradMaps& maps, const GradArgs& a, int shares, cudaStream_t st) {
+cudaError_t launch_ranks(int ranks, const GradJobs& j, cudaStream_t st) {
   switch (ranks) {
-    case 16: return launch_shape<48, CODES>(maps, a, shares, st);
-    case 32: return launch_shape<96, CODES>(maps, a, shares, st);
-    case 48: return launch_shape<144, CODES>(maps, a, shares, st);
-    case 64: return launch_shape<192, CODES>(maps, a, shares, st);
+    case 16: return launch_shape<48, CODES>(j, st);
+    case 32: return launch_shape<96, CODES>(j, st);
+    case 48: return launch_shape<144, CODES>(j, st);
+    case 64: return launch_shape<192, CODES>(j, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -727,30 +745,32 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
     e = launch_pdl(lora_terms_kernel, dim3(ceil_div(M, kTok), 2), dim3(256), 0, st, a);
     off += align256((size_t)M * npad * 2);
   }
-  for (int side = 0; side < 2 && e == cudaSuccess; ++side) {
-    const int D = side ? ad->N : ad->K;
-    const bool codes = !side && sx;
-    float* out = side ? dbt : da;
-    const int splits = grad_splits(M, D, ad->max_rank), shares = grad_shares(ad, D, splits);
-    float* part = reinterpret_cast<float*>(at);
-    uint8_t* has = reinterpret_cast<uint8_t*>(at) + align256((size_t)splits * ad->R * D * sizeof(float));
-    at += part_bytes(ad, M, D);
-    if (splits > 1) sum.job[side] = {part, has, out, splits, D, ceil_div(D, 1024)};
-    off = 0;
-    for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
-      const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
-      GradMaps maps;
-      memset(&maps, 0, sizeof(maps));
+  const int splits = grad_splits(ad, M), shares = grad_shares(ad, splits);
+  off = 0;
+  for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
+    const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
+    GradJobs j;
+    memset(&j, 0, sizeof(j));
+    char* part = at;
+    for (int side = 0; side < 2; ++side) {
+      const int D = side ? ad->N : ad->K;
+      const bool codes = !side && sx;
+      float* out = side ? dbt : da;
+      uint8_t* has = reinterpret_cast<uint8_t*>(part) + align256((size_t)splits * ad->R * D * sizeof(float));
+      if (splits > 1) sum.job[side] = {reinterpret_cast<float*>(part), has, out, splits, D, ceil_div(D, 1024)};
+      GradMaps& maps = j.maps[side];
       bool ok = map_2d(&maps.terms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, terms[side] + off, npad, M, (uint64_t)npad * 2,
                        64, kTok, true);
       ok = ok && (codes ? map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, D, M, ldx, kD, kTok, false)
                   : side ? map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, D, M, (uint64_t)ldd * 2, 64, kTok, true)
                          : map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, D, M, (uint64_t)ldx * 2, 64, kTok, true));
       if (!ok) return cudaErrorInvalidValue;
-      const GradArgs a{ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb, splits > 1 ? part : out, splits, has, header};
-      e = codes ? launch_ranks<true>(rc, maps, a, shares, st) : launch_ranks<false>(rc, maps, a, shares, st);
-      off += align256((size_t)M * npad * 2);
+      j.args[side] = {ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb,
+                      splits > 1 ? reinterpret_cast<float*>(part) : out, splits, ceil_div(D, kD), shares, has, header};
+      part += part_bytes(ad, M, D);
     }
+    e = sx ? launch_ranks<true>(rc, j, st) : launch_ranks<false>(rc, j, st);
+    off += align256((size_t)M * npad * 2);
   }
   if (e == cudaSuccess && sum.job[0].blocks + sum.job[1].blocks > 0) {
     sum.off = ad->off;
