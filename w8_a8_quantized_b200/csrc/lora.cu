@@ -543,11 +543,12 @@ cudaError_t shrink_any(const aq_lora* ad, bool b_side, const uint16_t* x, int ld
                              : shrink(b_side ? table_b(ad) : table_a(ad), x, ldx, ids, M, p, st);
 }
 cudaError_t expand_any(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, const void* y, int ldy,
-                       void* out, int ldo, int dtype, float* s, void* header, cudaStream_t st) {
+                       void* out, int ldo, int dtype, float* s, const TermsArgs* terms, void* header, cudaStream_t st) {
   const int splits = products(ad, M, !b_side).splits;
   const int32_t* counts = reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(p) + sum_bytes(ad, M, !b_side));
   return lora_tc_fits(ad, M)
-             ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, counts, y, ldy, out, ldo, dtype == AQ_F32, s, header, st)
+             ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, counts, y, ldy, out, ldo, dtype == AQ_F32, s, terms, header,
+                                                   st)
              : expand(b_side ? table_b(ad) : table_a(ad), ids, M, p, splits, y, ldy, out, ldo, dtype, s, st);
 }
 
@@ -598,7 +599,7 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
                                                                                                             : AQ_ERR_CUDA;
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaError_t e = shrink_any(ad, false, x, ldx, ids, M, p, ws, st);
-  if (e == cudaSuccess) e = expand_any(ad, true, ids, M, p, y, ldy, out, ldo, ydtype, s, ws, st);
+  if (e == cudaSuccess) e = expand_any(ad, true, ids, M, p, y, ldy, out, ldo, ydtype, s, nullptr, ws, st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }
 
@@ -625,9 +626,12 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   const Products t = products(ad, M, true);
   cudaError_t e = shrink_any(ad, true, dy, ldd, ids, M, p, ws, st);
-  if (e == cudaSuccess && dx) e = expand_any(ad, false, ids, M, p, add, ldadd, dx, lddx, dxdtype, nullptr, ws, st);
+  char* rest = reinterpret_cast<char*>(p) + p_bytes(ad, M, true);
+  const bool beside = dx && lora_tc_fits(ad, M);
+  const TermsArgs terms = lora_grad_terms(ad, ids, M, 0, p, t.splits, t.ld, sx, s, rest);
+  if (e == cudaSuccess && dx)
+    e = expand_any(ad, false, ids, M, p, add, ldadd, dx, lddx, dxdtype, nullptr, beside ? &terms : nullptr, ws, st);
   if (e == cudaSuccess)
-    e = launch_lora_grad(ad, ids, M, p, t.splits, t.ld, x, ldx, sx, da, s, dy, ldd, dbt, ws,
-                         reinterpret_cast<char*>(p) + p_bytes(ad, M, true), st);
+    e = launch_lora_grad(ad, ids, M, p, t.splits, t.ld, x, ldx, sx, da, s, dy, ldd, dbt, beside, ws, rest, st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }

@@ -6,9 +6,9 @@
 // T is fp32 and enters as three bf16 terms, 24 bits, side by side along N:
 //   D[128 d][hi | mid | lo] += x[64 tokens][128 d]^T [T_hi | T_mid | T_lo][64 tokens]
 // so one pass over x serves all three; codes are exact in bf16.  Both operands are
-// MN-major, that is, as they lie in memory.  A first kernel writes the terms
-// (zeros behind a token's rank) and says of each 64 tokens whether one adapter has
-// them all.  On paper the bytes of x bound it, 64 x 128 of them per step against 64 x 128 x 3r
+// MN-major, that is, as they lie in memory.  A first kernel, or the expansion of dx beside
+// its own work, writes the terms (zeros behind a token's rank) and says of each 64 tokens
+// whether one adapter has them all.  On paper the bytes of x bound it, 64 x 128 of them per step against 64 x 128 x 3r
 // multiplications; in practice a step's chain of waits and its conversion (940 of 2000 cycles,
 // two CTAs per SM): 8192 x 14336 codes, ranks 16 to 32, take 60 us, 30% of the copy rate.
 //
@@ -48,21 +48,6 @@ constexpr uint32_t kMixed = 1u << 9, kUnitStart = 1u << 10, kUnitEnd = 1u << 11,
 constexpr int kSlotShift = 13;
 
 // ---------------------------------------------------------------- terms
-struct TermsJob {
-  const float* p;     // [splits][M][ld]
-  int splits, ld;
-  const float* sx;    // [M] or null
-  uint16_t* terms;    // [M][npad]: hi, mid, lo of `rc` ranks each
-};
-struct TermsArgs {
-  TermsJob job[2];
-  const int32_t* ids;
-  const int32_t* off;
-  int M, L, R, max_rank;
-  int rb0, rc, npad;
-  int32_t* info;      // per 64 tokens: the adapter that has them all, -1 none has any, -2 mixed
-};
-
 __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsArgs a) {
   __shared__ int rank[kTok];
   const int tid = threadIdx.x, m0 = blockIdx.x * kTok;
@@ -95,33 +80,7 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(const TermsArgs a) {
   for (int i = tid; i < kTok * per_row; i += 256) {
     const int t = i / per_row, c = (i - t * per_row) * 8, m = m0 + t;
     if (m >= a.M) break;
-    const int left = rank[t] - c;
-    float v[8] = {};
-    if (left > 0) {
-      const float* src = j.p + (size_t)m * j.ld + a.rb0 + c;
-      const size_t step = (size_t)a.M * j.ld;
-#pragma unroll 4
-      for (int k = 0; k < j.splits; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < left) v[e] += __ldg(src + k * step + e);
-      if (j.sx) {
-        const float scale = __ldg(j.sx + m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= scale;
-      }
-    }
-    uint16_t h[3][8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) split3(v[e], h[0][e], h[1][e], h[2][e]);
-    uint16_t* d = j.terms + (size_t)m * a.npad + c;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = h[k][2 * e] | ((uint32_t)h[k][2 * e + 1] << 16);
-      *reinterpret_cast<uint4*>(d + k * a.rc) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    write_terms(a, j, m, c, rank[t]);
   }
 }
 
@@ -725,9 +684,20 @@ size_t lora_grad_ws_bytes(const aq_lora* ad, int M) {
          part_bytes(ad, M, ad->K) + part_bytes(ad, M, ad->N);
 }
 
+TermsArgs lora_grad_terms(const aq_lora* ad, const int32_t* ids, int M, int rb, const float* t, int tsplits, int ldt,
+                          const float* sx, const float* s, void* ws) {
+  char* at = static_cast<char*>(ws);
+  int32_t* info = reinterpret_cast<int32_t*>(at);
+  at += align256((size_t)ceil_div(M, kTok) * 4);
+  for (int i = 0; i < rb; ++i) at += align256((size_t)M * block_pad(ad->max_rank, i) * 2);
+  return {{{t, tsplits, ldt, sx, reinterpret_cast<uint16_t*>(at)},
+           {s, 1, ad->max_rank, nullptr, reinterpret_cast<uint16_t*>(at + terms_bytes(M, ad->max_rank))}},
+          ids, ad->off, M, ad->L, ad->R, ad->max_rank, 64 * rb, block_ranks(ad->max_rank, rb), block_pad(ad->max_rank, rb), info};
+}
+
 cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
                              int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
-                             float* dbt, void* header, void* ws, cudaStream_t st) {
+                             float* dbt, bool have_terms, void* header, void* ws, cudaStream_t st) {
   char* at = static_cast<char*>(ws);
   int32_t* info = reinterpret_cast<int32_t*>(at);
   at += align256((size_t)ceil_div(M, kTok) * 4);
@@ -736,17 +706,11 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
   SumArgs sum;
   memset(&sum, 0, sizeof(sum));
   cudaError_t e = cudaSuccess;
-  size_t off = 0;
-  for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
-    const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
-    TermsArgs a{{{t, tsplits, ldt, sx, reinterpret_cast<uint16_t*>(terms[0] + off)},
-                 {s, 1, ad->max_rank, nullptr, reinterpret_cast<uint16_t*>(terms[1] + off)}},
-                ids, ad->off, M, ad->L, ad->R, ad->max_rank, 64 * rb, rc, npad, info};
-    e = launch_pdl(lora_terms_kernel, dim3(ceil_div(M, kTok), 2), dim3(256), 0, st, a);
-    off += align256((size_t)M * npad * 2);
-  }
+  for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess && !have_terms; ++rb)
+    e = launch_pdl(lora_terms_kernel, dim3(ceil_div(M, kTok), 2), dim3(256), 0, st,
+                   lora_grad_terms(ad, ids, M, rb, t, tsplits, ldt, sx, s, ws));
   const int splits = grad_splits(ad, M), shares = grad_shares(ad, splits);
-  off = 0;
+  size_t off = 0;
   for (int rb = 0; rb < rank_blocks(ad->max_rank) && e == cudaSuccess; ++rb) {
     const int rc = block_ranks(ad->max_rank, rb), npad = block_pad(ad->max_rank, rb);
     GradJobs j;

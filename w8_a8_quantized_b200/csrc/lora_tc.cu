@@ -352,6 +352,7 @@ struct ExpandTcArgs {
   const int32_t* counts;
   int M, splits, has_y, in_place;
   int tiles, g, extra;  // CTAs of a tile, and those left for tiles of several adapters
+  TermsArgs terms;      // rc 0: not wanted
   const float* p;  // [splits][M][rp]
   float* s;        // [M][max_rank] or null
   void* ws;
@@ -530,6 +531,24 @@ __global__ void __launch_bounds__(kEThreads, 1)
   bool ok = true;
   const bool idle = na == 0 && a.in_place;  // nothing changes
 
+  if ((warp == 2 || warp == 3) && a.terms.rc > 0 && tile >= 0) {
+    // ------------------------------------------------------------ terms of the weight gradients, shared by the tile's CTAs
+    const int ranks8 = a.terms.rc / 8;
+    for (int i = 64 * part + tid - 64; i < 2 * kTok * ranks8; i += 64 * parts) {
+      const int job = i / (kTok * ranks8), k = i - job * kTok * ranks8, r = k / ranks8, m = m0 + r;
+      if (m < M) write_terms(a.terms, a.terms.job[job], m, (k - r * ranks8) * 8, q.slot[r] >= 0 ? q.rank[q.slot[r]] : 0);
+    }
+    const int first = m0 + 64 * (warp - 2), n = min(64, M - first);
+    if (n > 0 && part == 0) {
+      auto id = [&](int i) {
+        const int v = i < n ? __ldg(a.ids + first + i) : -1;
+        return v >= 0 && v < t.L ? v : -1;
+      };
+      const int lead = id(0), v0 = id(lane), v1 = id(lane + 32);
+      const bool same = __all_sync(0xffffffffu, (lane >= n || v0 == lead) && (lane + 32 >= n || v1 == lead));
+      if (lane == 0) a.terms.info[first / 64] = same ? lead : -2;
+    }
+  }
   if (idle) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ y
@@ -800,7 +819,7 @@ cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t
 
 cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
                                   const int32_t* counts, const void* y, int ldy, void* out, int ldo, bool f32, float* s,
-                                  void* header, cudaStream_t st) {
+                                  const TermsArgs* terms, void* header, cudaStream_t st) {
   const TcTable t = table(ad, b_side);
   ExpandMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -809,7 +828,7 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
   if (!map_2d(&maps.out, type, out, t.D, M, (uint64_t)ldo * elt, 128 / elt, kTok, true) ||
       (y && !map_2d(&maps.y, type, y, t.D, M, (uint64_t)ldy * elt, 128 / elt, kTok, true)))
     return cudaErrorInvalidValue;
-  const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, p, s, header};
+  const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, terms ? *terms : TermsArgs{}, p, s, header};
   if (t.rp <= 32) return f32 ? launch_expand<true, 5>(maps, a, st) : launch_expand<false, 5>(maps, a, st);
   return f32 ? launch_expand<true, 3>(maps, a, st) : launch_expand<false, 3>(maps, a, st);
 }
