@@ -482,8 +482,10 @@ size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 Table table_a(const aq_lora* ad) { return {ad->a, ad->off, ad->scale, ad->K, ad->L, ad->R, ad->max_rank}; }
 Table table_b(const aq_lora* ad) { return {ad->bt, ad->off, ad->scale, ad->N, ad->L, ad->R, ad->max_rank}; }
 
-// CTAs that share the adapters of one tile: a single tile may hold 64.
-int share(int M, const Table& t) { return M <= kTok && t.L > 1 ? std::min(4, t.L) : 1; }
+// CTAs that share the adapters of one tile: a single tile may hold 64.  An expanding CTA
+// makes the terms of all its tokens first, so fewer share there (30 tokens of 22 adapters with
+// gradients: 82 us with 8 contracting and 4 expanding, 84 with 4 and 4, 91 with 8 and 8).
+int share(int M, const Table& t, int most) { return M <= kTok && t.L > 1 ? std::min(most, t.L) : 1; }
 
 int shrink_splits(int M, const Table& t) {
   const int tiles = ceil_div(M, kTok), chunks = ceil_div(t.D, kDC);
@@ -511,7 +513,7 @@ size_t p_bytes(const aq_lora* ad, int M, bool b_side) {
 }
 
 cudaError_t shrink(const Table& t, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p, cudaStream_t st) {
-  ShrinkArgs a{t, x, ldx, M, ids, p, shrink_splits(M, t), share(M, t)};
+  ShrinkArgs a{t, x, ldx, M, ids, p, shrink_splits(M, t), share(M, t, 8)};
   cudaError_t e = ensure_smem_attr<lora_shrink_kernel>(sizeof(ShrinkSmem));
   if (e != cudaSuccess) return e;
   const dim3 grid(ceil_div(M, kTok), a.splits, a.kz * ceil_div(t.max_rank, kRank));
@@ -533,7 +535,7 @@ cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t st) {
 cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, int splits, const void* y, int ldy,
                    void* out, int ldo, int dtype, float* s, cudaStream_t st) {
   const int rp = (t.max_rank + 15) / 16 * 16;
-  const ExpandArgs a{t, ids, M, p, splits, share(M, t), y, out, ldy, ldo, s, rp, std::min(rp, kRank)};
+  const ExpandArgs a{t, ids, M, p, splits, share(M, t, 4), y, out, ldy, ldo, s, rp, std::min(rp, kRank)};
   return dtype == AQ_F32 ? launch_expand<true>(a, st) : launch_expand<false>(a, st);
 }
 
