@@ -438,9 +438,11 @@ typedef struct aq_lora {
  *  ids   int32 [M]
  *  y     the projection's output [M][ldy], fp32 or bf16 (ydtype), or NULL (out = the
  *        adapters' part alone)
- *  out   [M][ldo], same dtype; may be y itself (same pitch), otherwise must not overlap an input
+ *  out   [M][ldo], same dtype; may be y itself (same pitch)
  *  s     fp32 [M][max_rank] or NULL: receives S (zeros behind a token's rank), which
  *        aq_lora_backward takes
+ *  out and s must not overlap an input (but y as said) or each other: AQ_ERR_ARG.  Rows of one
+ *  pitch that lie side by side in one buffer do not overlap.
  *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned, zero-filled once
  *        when allocated; calls that share it must not run concurrently (one of 16
  *        bytes is not touched: decode batches need none)
@@ -468,6 +470,8 @@ int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, const int32_t* 
  *  da    fp32 [R][K], dbt fp32 [R][N], 16-byte aligned, written
  *  add   [M][ldadd] of dxdtype or NULL (zero), e.g. aq_linear_backward's result
  *  dx    [M][lddx], fp32 or bf16 (dxdtype), or NULL (not wanted); may be add itself (same pitch)
+ *  da, dbt and dx must not overlap an input (but add as said; add may not be dy or x then: the
+ *  weight gradients are formed after dx) or each other: AQ_ERR_ARG.
  *  ws    >= aq_lora_workspace_bytes(ad, M, 1) bytes, as for aq_lora_apply; a bounded wait
  *        that gives up is recorded there and reported by aq_workspace_status
  * Alignment, M and errors as for aq_lora_apply.
@@ -492,7 +496,8 @@ size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward);
  *  gate, up  bf16 [M][ldg], [M][ldu], 16-byte aligned, ld % 8 == 0
  *  hq, gq, uq  int8 [M][F], 16-byte aligned;  sh fp32 [M];  gs, us fp32 [M][ceil(F/128)]
  * 1 <= M, 16 <= F <= 65536 with F % 16 == 0.  A row that holds an infinity or NaN
- * gets unspecified codes; other rows are not touched by it.  Asynchronous, no
+ * gets unspecified codes; other rows are not touched by it.  Outputs must not overlap
+ * gate, up or each other (AQ_ERR_ARG).  Asynchronous, no
  * workspace.  Errors: AQ_ERR_ARG, AQ_ERR_CUDA.
  */
 int aq_silu_mul_quant(const uint16_t* gate, int ldg, const uint16_t* up, int ldu, int M, int F, int8_t* hq, float* sh,
@@ -503,7 +508,8 @@ int aq_silu_mul_quant(const uint16_t* gate, int ldg, const uint16_t* up, int ldu
  * u = us uq, p = 1 / (1 + exp(-g)),
  *   dgate = dh u p (1 + g (1 - p)),   dup = dh g p        (fp32, rounded once to bf16)
  *  dh  bf16 [M][ldd];  dgate, dup bf16 [M][ldg], [M][ldu]; 16-byte aligned, ld % 8 == 0
- * The rounding of h to its codes is passed through.  Limits and errors as for
+ * The rounding of h to its codes is passed through.  dgate and dup must not overlap an
+ * input or each other (side by side in one buffer they do not).  Limits and errors as for
  * aq_silu_mul_quant.
  */
 int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const float* gs, const int8_t* uq,
@@ -517,7 +523,8 @@ int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const fl
  *  dy    bf16 [M][ldd], 16-byte aligned, ldd % 8 == 0, ldd >= N
  *  add   [M][ldadd] of dxdtype or NULL (zero): e.g. the gradient through another
  *        projection of the same input
- *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself (same pitch)
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself (same pitch),
+ *        and must not overlap dy, or add otherwise: AQ_ERR_ARG
  *  ws    >= aq_linear_backward_workspace_bytes(M, w) bytes, 16-byte aligned,
  *        zero-filled once as for the linear calls; errors by aq_workspace_status
  * 1 <= M <= 2097152.  Asynchronous.

@@ -64,6 +64,47 @@ def test_lora_backward_refusals(kw, status):
     assert backward(**kw) == status
 
 
+M_, N_, K_ = 70, 128, 256
+MIB = 1 << 20
+
+
+def places(**kw):
+    """Pointers a MiB apart, some of them moved onto others: 'name' or 'name+bytes'."""
+    names = ("x", "ids", "y", "out", "s", "dy", "sx", "da", "dbt", "add", "dx", "ws", "a", "bt", "off", "scale")
+    at = {n: (i + 1) * MIB for i, n in enumerate(names)}
+    for n, where in kw.items():
+        base, _, plus = where.partition("+")
+        at[n] = at[base] + int(plus or 0)
+    return at
+
+
+# out over an input, over s, over y a row lower, next to nothing; s over an input
+@pytest.mark.parametrize("kw", [
+    dict(out="x"), dict(out="x+16"), dict(out="ids"), dict(out="s"), dict(out=f"y+{4 * N_}"), dict(out="y+16"),
+    dict(out="a"), dict(out="bt+64"), dict(out="off"), dict(s="x+4"), dict(s="y"), dict(s="ids"), dict(s="scale"),
+    dict(x=f"out+{4 * N_ * (M_ - 1)}"), dict(s="y", out="y")])
+def test_lora_apply_refuses_overlaps(kw):
+    p = places(**kw)
+    assert apply(ad=lora(a=p["a"], bt=p["bt"], off=p["off"], scale=p["scale"]), x=p["x"], ids=p["ids"], M=M_, y=p["y"],
+                 out=p["out"], s=p["s"], ws=p["ws"]) == ARG
+
+
+# dx over dy, in place over a residual gradient that is dy itself, over x, and each gradient over what is read or written
+@pytest.mark.parametrize("kw", [
+    dict(dx="dy"), dict(add="dy", dx="dy"), dict(dy="dx+16"), dict(dx="x"), dict(add="x", dx="x"), dict(dx="x+32"),
+    dict(dx="sx"), dict(dx="s"), dict(dx="ids"), dict(dx="add+16"), dict(add=f"dx+{4 * K_}"), dict(dx="a"), dict(dx="bt"),
+    dict(da="x"), dict(da="dy+16"), dict(da="s"), dict(da="add"), dict(dbt="dy"), dict(dbt="x+16"), dict(dbt="sx"),
+    dict(da="dbt"), dict(da="dx+16"), dict(dbt="dx"), dict(dbt="bt"), dict(da="a"), dict(da="off"), dict(dbt="scale")])
+@pytest.mark.parametrize("codes", [True, False])
+def test_lora_backward_refuses_overlaps(kw, codes):
+    p = places(**kw)
+    if not codes and "sx" in kw.values():
+        pytest.skip("no token scales")
+    assert backward(ad=lora(a=p["a"], bt=p["bt"], off=p["off"], scale=p["scale"]), dy=p["dy"], ids=p["ids"], M=M_,
+                    s=p["s"], x=p["x"], sx=p["sx"] if codes else None, da=p["da"], dbt=p["dbt"], add=p["add"],
+                    dx=p["dx"], ws=p["ws"]) == ARG
+
+
 def test_lora_workspace_sizes():
     f = aq.lib().aq_lora_workspace_bytes
     assert f(lora(N=100), 4, 0) == 0 and f(lora(), 0, 0) == 0 and f(None, 4, 0) == 0
@@ -94,6 +135,26 @@ def test_gated_backward_refusals(kw):
     assert gated_back(**kw) == ARG
 
 
+@pytest.mark.parametrize("kw", [
+    dict(hq="gate"), dict(hq="up+16"), dict(gq="gate+16"), dict(uq="up"), dict(sh="gate+4"), dict(gs="up"), dict(us="gate"),
+    dict(hq="gq"), dict(gq="uq+16"), dict(sh="hq"), dict(gs="us+4"), dict(up="hq+512")])
+def test_gated_refuses_overlaps(kw):
+    at = {n: (i + 1) * MIB for i, n in enumerate(("gate", "up", "hq", "sh", "gq", "gs", "uq", "us"))}
+    for n, where in kw.items():
+        at[n] = at[where.split("+")[0]] + int((where.split("+") + ["0"])[1])
+    assert gated(M=70, **at) == ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dg="dh"), dict(du="dh"), dict(du="dh+512"), dict(dg="gq"), dict(du="uq+16"), dict(dg="us"), dict(du="gs"),
+    dict(dg="du"), dict(du="dg+16"), dict(dh="dg+35328")])
+def test_gated_backward_refuses_overlaps(kw):
+    at = {n: (i + 1) * MIB for i, n in enumerate(("dh", "gq", "gs", "uq", "us", "dg", "du"))}
+    for n, where in kw.items():
+        at[n] = at[where.split("+")[0]] + int((where.split("+") + ["0"])[1])
+    assert gated_back(M=70, **at) == ARG
+
+
 def packed(**kw):
     v = dict(N=128, K=256, bN=128, bK=128, R=1, C=2, T4=0, T8=2, bitmap=16, row_off4=16, row_off8=16, tile_idx=16, w4=16,
              w8=16, scales=16)
@@ -113,6 +174,18 @@ def linear_back(w=None, dy=16, ldd=128, M=4, add=16, ldadd=256, dx=16, lddx=256,
     (dict(n=16), WORKSPACE), (dict(ws=24), ARG), (dict(lddx=264), ARG)])
 def test_linear_backward_refusals(kw, status):
     assert linear_back(**kw) == status
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx="dy"), dict(add="dy", dx="dy"), dict(dx="dy+16"), dict(dy=f"dx+{4 * 256 * 69}"), dict(dx="add+16"),
+    dict(add="dx+1024"), dict(dx="add+64", ldadd=512)])
+def test_linear_backward_refuses_overlaps(kw):
+    kw = dict(kw)
+    at = {n: (i + 1) * MIB for i, n in enumerate(("dy", "add", "dx", "ws"))}
+    for n in [n for n in kw if n in at]:
+        base, _, plus = kw.pop(n).partition("+")
+        at[n] = at[base] + int(plus or 0)
+    assert linear_back(M=70, **at, **kw) == ARG
 
 
 def test_linear_backward_workspace_sizes():

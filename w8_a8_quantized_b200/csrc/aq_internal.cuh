@@ -122,6 +122,38 @@ cudaError_t launch_tc_group(const aq_packed* const* w, int G, const float* const
 cudaError_t launch_tc_stalled(const aq_packed* w, const int8_t* xq, const float* sx, int M, void* y, int ldy,
                               void* ws, int phase, unsigned long long wait_ns, int stop_after, cudaStream_t st);
 
+// Memory that a call reads or writes: `rows` rows of `width` bytes, `pitch` bytes apart.  A null
+// pointer touches nothing.
+struct Span {
+  const void* p;
+  size_t pitch, width;
+  long long rows;
+};
+inline Span flat(const void* p, size_t bytes) { return {p, bytes, bytes, 1}; }
+// Whether two spans share a byte.  Exact for rows of one pitch (which may lie side by side in
+// one buffer) and for single rows; rows of different pitches share one where their ranges do.
+inline bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1) return false;
+  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+  const uintptr_t a1 = a0 + (size_t)(a.rows - 1) * a.pitch + a.width, b1 = b0 + (size_t)(b.rows - 1) * b.pitch + b.width;
+  if (a0 >= b1 || b0 >= a1) return false;
+  const size_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if ((a.rows == 1 && b.rows == 1) || (b.rows > 1 && b.pitch != pitch)) return true;
+  const size_t d = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;  // b's first column in a's rows
+  return d < a.width || d + b.width > pitch;
+}
+// Whether an output shares a byte with an input or with another output.
+template <int NO, int NI>
+bool outputs_overlap(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(out[i], out[j])) return true;
+    for (const Span& s : in)
+      if (overlap(out[i], s)) return true;
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------- device helpers
 #if defined(__CUDACC__)
 

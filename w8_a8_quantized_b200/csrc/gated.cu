@@ -407,6 +407,11 @@ extern "C" int aq_silu_mul_quant(const uint16_t* gate, int ldg, const uint16_t* 
   if (keep && (!gq || !gs || !uq || !us)) return AQ_ERR_ARG;
   if (((uintptr_t)gate | (uintptr_t)up | (uintptr_t)hq | (uintptr_t)gq | (uintptr_t)uq) & 15) return AQ_ERR_ARG;
   if (((uintptr_t)sh | (uintptr_t)gs | (uintptr_t)us) & 3) return AQ_ERR_ARG;
+  const size_t codes = (size_t)M * F, scales = (size_t)M * ((F + kGroup - 1) / kGroup) * 4;
+  const Span outs[] = {flat(hq, codes), flat(sh, (size_t)M * 4), flat(gq, codes), flat(gs, scales), flat(uq, codes),
+                       flat(us, scales)};
+  const Span ins[] = {{gate, (size_t)ldg * 2, (size_t)F * 2, M}, {up, (size_t)ldu * 2, (size_t)F * 2, M}};
+  if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = keep ? launch_fwd<true>(gate, ldg, up, ldu, M, F, hq, sh, gq, gs, uq, us, st)
                              : launch_fwd<false>(gate, ldg, up, ldu, M, F, hq, sh, gq, gs, uq, us, st);
@@ -421,6 +426,10 @@ extern "C" int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* g
   if (ldd < F || ldg < F || ldu < F || ldd % 8 || ldg % 8 || ldu % 8) return AQ_ERR_ARG;
   if (((uintptr_t)dh | (uintptr_t)gq | (uintptr_t)uq | (uintptr_t)dgate | (uintptr_t)dup) & 15) return AQ_ERR_ARG;
   if (((uintptr_t)gs | (uintptr_t)us) & 3) return AQ_ERR_ARG;
+  const size_t codes = (size_t)M * F, scales = (size_t)M * ((F + kGroup - 1) / kGroup) * 4, width = (size_t)F * 2;
+  const Span outs[] = {{dgate, (size_t)ldg * 2, width, M}, {dup, (size_t)ldu * 2, width, M}};
+  const Span ins[] = {{dh, (size_t)ldd * 2, width, M}, flat(gq, codes), flat(gs, scales), flat(uq, codes), flat(us, scales)};
+  if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   // whole warps, up to four rounds a thread
   const int nv = F / 16, rounds = (nv + 255) / 256, threads = ((nv + rounds - 1) / rounds + 31) / 32 * 32;
   return launch_pdl(silu_mul_backward_kernel, dim3(M), dim3(threads), 0, static_cast<cudaStream_t>(stream), dh, ldd, gq,

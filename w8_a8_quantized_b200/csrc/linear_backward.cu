@@ -667,6 +667,11 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   if (add == dx && ldadd != lddx && M > 1) return AQ_ERR_ARG;  // in place is row by row
   if (!ws || ws_bytes < aq_linear_backward_workspace_bytes(M, w)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
+  // units end in any order: what one writes over dy, others would still read
+  const size_t elt = dxdtype == AQ_F32 ? 4 : 2, width = w->K * elt;
+  const Span outs[] = {{dx, lddx * elt, width, M}};
+  const Span ins[] = {{dy, (size_t)ldd * 2, (size_t)w->N * 2, M}, {add == dx ? nullptr : add, ldadd * elt, width, M}};
+  if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   const BwdPlan p = plan_bwd(M, w->N, w->C);
   BwdArgs a;
   memset(&a, 0, sizeof(a));

@@ -572,6 +572,9 @@ constexpr int kMaxTokens = 65535 * kTok;  // grid rows of the expand kernel
 bool bad_rows(const void* p, int ld, int width, int per16) { return !p || ((uintptr_t)p & 15) || ld < width || ld % per16; }
 // In place is row by row: the same pointer with another pitch would overwrite rows still to be read.
 bool skewed(const void* in, int ldi, const void* out, int ldo, int M) { return in == out && ldi != ldo && M > 1; }
+// Any other overlap of an output is refused too: kernels of a call run one after another and CTAs in any order, so
+// what was written over an input would be read as the input.
+Span rows_at(const void* p, int ld, int width, int elt, int M) { return {p, (size_t)ld * elt, (size_t)width * elt, M}; }
 
 }  // namespace
 }  // namespace aq
@@ -597,6 +600,13 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
     return AQ_ERR_ARG;
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 0)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
+  const int elt = ydtype == AQ_F32 ? 4 : 2;
+  const Span outs[] = {rows_at(out, ldo, ad->N, elt, M), flat(s, (size_t)M * ad->max_rank * 4)};
+  const Span ins[] = {rows_at(y == out ? nullptr : y, ldy, ad->N, elt, M), rows_at(x, ldx, ad->K, 2, M),
+                      flat(ids, (size_t)M * 4),
+                      flat(ad->a, (size_t)ad->R * ad->K * 2), flat(ad->bt, (size_t)ad->R * ad->N * 2),
+                      flat(ad->off, (size_t)(ad->L + 1) * 4), flat(ad->scale, (size_t)ad->L * 4)};
+  if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (lora_decode_fits(ad, M))
     return launch_lora_decode(ad, x, ldx, ids, M, y, ldy, out, ldo, ydtype == AQ_F32, s, st) == cudaSuccess ? AQ_OK
@@ -626,6 +636,15 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   }
   if (!ws || ws_bytes < aq_lora_workspace_bytes(ad, M, 1)) return AQ_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return AQ_ERR_ARG;
+  const int elt = dxdtype == AQ_F32 ? 4 : 2;
+  const Span outs[] = {flat(da, (size_t)ad->R * ad->K * 4), flat(dbt, (size_t)ad->R * ad->N * 4),
+                       rows_at(dx, lddx, ad->K, elt, M)};
+  const Span ins[] = {rows_at(add == dx ? nullptr : add, ldadd, ad->K, elt, M), rows_at(dy, ldd, ad->N, 2, M),
+                      rows_at(x, ldx, ad->K, sx ? 1 : 2, M), flat(ids, (size_t)M * 4), flat(sx, (size_t)M * 4),
+                      flat(s, (size_t)M * ad->max_rank * 4),
+                      flat(ad->a, (size_t)ad->R * ad->K * 2), flat(ad->bt, (size_t)ad->R * ad->N * 2),
+                      flat(ad->off, (size_t)(ad->L + 1) * 4), flat(ad->scale, (size_t)ad->L * 4)};
+  if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   const Products t = products(ad, M, true);
