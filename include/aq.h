@@ -51,6 +51,8 @@ typedef enum {
 } aq_status;
 
 typedef enum { AQ_F32 = 0, AQ_BF16 = 1 } aq_dtype;
+/* How aq_linear_backward takes the weights; added to its dxdtype, which decides without. */
+typedef enum { AQ_WEIGHTS_BF16 = 0x100, AQ_WEIGHTS_EXACT = 0x200 } aq_weights;
 typedef enum { AQ_PHASE_DECODE = 0, AQ_PHASE_PREFILL = 1 } aq_phase;
 
 /*
@@ -519,11 +521,17 @@ int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const fl
 /*
  * Input gradient of a packed projection (its weights are frozen):
  *   dx[m][k] = add[m][k] + sum_n dy[m][n] sw[n][k / 128] q[n][k]
+ * Products run on the bf16 tensor cores with fp32 sums.  For an fp32 dx a weight sw q
+ * enters exactly (as three bf16 terms) and the result is an fp32 product's; for a bf16
+ * dx it is rounded once to bf16 (2^-8 relative at most, independent from weight to weight,
+ * so an error like that of dx's own rounding: 2.35e-3 of the norm in all, 1.66e-3 with exact
+ * weights) at a third of the products.  dxdtype + AQ_WEIGHTS_BF16 or + AQ_WEIGHTS_EXACT
+ * takes the one or the other for either type.
  *  w     as for aq_linear_prefill
  *  dy    bf16 [M][ldd], 16-byte aligned, ldd % 8 == 0, ldd >= N
  *  add   [M][ldadd] of dxdtype or NULL (zero): e.g. the gradient through another
  *        projection of the same input
- *  dx    [M][lddx], fp32 or bf16 (dxdtype), 16-byte aligned rows; may be add itself (same pitch),
+ *  dx    [M][lddx], fp32 or bf16 (dxdtype, see above), 16-byte aligned rows; may be add itself (same pitch),
  *        and must not overlap dy, or add otherwise: AQ_ERR_ARG
  *  ws    >= aq_linear_backward_workspace_bytes(M, w) bytes, 16-byte aligned,
  *        zero-filled once as for the linear calls; errors by aq_workspace_status

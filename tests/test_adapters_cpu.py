@@ -205,3 +205,10 @@ def test_binding_refuses_host_tensors():
         aq.aq_silu_mul_quant([[1.0]], x)
     with pytest.raises(ValueError):
         aq.aq_silu_mul_backward(x, x, x, x, x)
+
+
+@pytest.mark.parametrize("dtype,status", [
+    (0x100, WORKSPACE), (0x101, WORKSPACE), (0x200, WORKSPACE), (0x201, WORKSPACE),  # the weights as asked for
+    (0x300, ARG), (0x102, ARG), (0x400, ARG), (-1, ARG)])
+def test_linear_backward_weights(dtype, status):
+    assert linear_back(dtype=dtype, ws=None) == status

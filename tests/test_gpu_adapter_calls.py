@@ -58,3 +58,51 @@ def test_outputs_over_inputs_are_refused():
         with pytest.raises(aq.AqError):
             call()
     assert torch.equal(dy, c.dy) and torch.equal(x, c.x)
+
+
+# ------------------------------------------------------------------ input gradient
+
+SUMS = [(1, 128, 256, 128), (33, 1088, 640, 64), (64, 4864, 384, 128), (77, 1088, 2560, 64), (129, 384, 512, 128),
+        (200, 14336, 256, 128), (257, 2560, 896, 64), (1030, 2560, 9728, 64), (2048, 9728, 1280, 128),
+        (700, 4096, 14336, 128)]
+
+
+@pytest.mark.parametrize("N,K,bN,frac8", [(256, 384, 128, 0.5), (192, 256, 64, 0.5), (128, 128, 64, 1.0)])
+def test_linear_backward_takes_the_weights_as_asked(N, K, bN, frac8):
+    """dy = the identity: dx is the weight matrix, exact or rounded once."""
+    w, w64 = packed(N, K, bN, frac8, N)
+    eye = torch.eye(N, device="cuda", dtype=torch.bfloat16)
+    rounded = w64.to(torch.bfloat16)
+    for out_dtype, weights, want in ((torch.float32, None, w64), (torch.float32, torch.float32, w64),
+                                     (torch.float32, torch.bfloat16, rounded.double()), (torch.bfloat16, None, rounded),
+                                     (torch.bfloat16, torch.bfloat16, rounded), (torch.bfloat16, torch.float32, rounded)):
+        got = aq.aq_linear_backward(w, eye, out_dtype=out_dtype, weights=weights)
+        assert got.dtype == out_dtype and torch.equal(got.to(want.dtype), want), (out_dtype, weights)
+    with pytest.raises(TypeError):
+        aq.aq_linear_backward(w, eye, weights=torch.float16)
+
+
+@pytest.mark.parametrize("M,N,K,bN", SUMS)
+def test_linear_backward_keeps_fp32(M, N, K, bN):
+    """A sum of 512 rows takes 96 additions in tensor memory, each off by 2^-23 of the partial
+    sum at most, whose norm grows with the root of its terms: 64 2^-23 of the norm, and one
+    rounding for each 512 rows and for `add` (weights rounded to bf16 are off by 1.6e-3)."""
+    w, w64 = packed(N, K, bN, 0.5, N + K + M)
+    dy = normal(rng(M), M, N, scale=0.01)
+    add = torch.randn(M, K, generator=rng(M + 1), device="cuda") * 0.01
+    ref = dy.double() @ w64
+    tol = (64 + N // 512 + 2) * U
+    got = aq.aq_linear_backward(w, dy, out_dtype=torch.float32)
+    assert (got.double() - ref).norm() <= tol * ref.norm()
+    assert torch.equal(aq.aq_linear_backward(w, dy, out_dtype=torch.float32), got)
+    both = aq.aq_linear_backward(w, dy, add=add)
+    assert (both.double() - ref - add.double()).norm() <= tol * (ref.norm() + add.double().norm())
+    z = add.clone()
+    assert aq.aq_linear_backward(w, dy, add=z, out=z) is z and torch.equal(z, both)
+    wide = torch.full((M + 2, K + 16), 7.0, device="cuda")
+    aq.aq_linear_backward(w, dy, out=wide)
+    assert torch.equal(wide[:M, :K], got) and bool((wide[M:] == 7).all()) and bool((wide[:, K:] == 7).all())
+    # exact weights and sums in tensor memory alone for a bf16 result: its own rounding, after 3N / 16 additions
+    got16 = aq.aq_linear_backward(w, dy, weights=torch.float32)
+    own = (ref.to(torch.bfloat16).double() - ref).norm()
+    assert (got16.double() - ref).norm() <= own * 1.01 + 3 * N / 16 * U * ref.norm()

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libaq.so")
 
 AQ_OK = 0
 AQ_F32, AQ_BF16 = 0, 1
+AQ_WEIGHTS_BF16, AQ_WEIGHTS_EXACT = 0x100, 0x200  # how aq_linear_backward takes the weights
 AQ_PHASE_DECODE, AQ_PHASE_PREFILL = 0, 1
 BUF_NAMES = ("bitmap", "row_off4", "row_off8", "tile_idx", "w4", "w8", "scales")
 EXPORTED = ("aq_status_str", "aq_packed_sizes", "aq_pack_metadata", "aq_pack", "aq_quant_act",
@@ -891,11 +892,19 @@ def aq_linear_backward_workspace_bytes(M: int, w: PackedWeights) -> int:
     return int(lib().aq_linear_backward_workspace_bytes(M, ctypes.byref(w.struct)))
 
 
+_WEIGHTS = {None: 0, _F32: AQ_WEIGHTS_EXACT, _BF16: AQ_WEIGHTS_BF16}
+
+
 def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = None, out: torch.Tensor = None,
-                       out_dtype=torch.bfloat16, ws: torch.Tensor = None) -> torch.Tensor:
+                       out_dtype=torch.bfloat16, ws: torch.Tensor = None, weights=None) -> torch.Tensor:
     """Input gradient of a packed projection: dx = add + dy W (W dequantized), dy bf16
-    [M][N] -> [M][K] in add's dtype (out_dtype without add).  out may be add."""
+    [M][N] -> [M][K] in add's dtype (out_dtype without add).  out may be add.  A float32
+    result takes the dequantized weights exactly, a bfloat16 one rounded to bfloat16 (a third
+    of the products, 1.4 times the rounding error); weights = torch.float32 or
+    torch.bfloat16 takes the one or the other for either."""
     dev, K = w.device, w.K
+    if weights not in _WEIGHTS:
+        raise TypeError("weights must be None, torch.float32 or torch.bfloat16")
     M, _, ldd, _ = _lead(dy, "dy", dev, w.N)
     ldadd = 0
     if add is not None:
@@ -916,7 +925,7 @@ def aq_linear_backward(w: PackedWeights, dy: torch.Tensor, add: torch.Tensor = N
         ws = _own_ws("backward", need, dev)
     _call(lib().aq_linear_backward, "aq_linear_backward", dev, ctypes.byref(w.struct), dy.data_ptr(), ldd, M,
           None if add is None else add.data_ptr(), ldadd, out.data_ptr(), ldo,
-          AQ_F32 if out.dtype == _F32 else AQ_BF16, ws.data_ptr(), ws.numel())
+          (AQ_F32 if out.dtype == _F32 else AQ_BF16) + _WEIGHTS[weights], ws.data_ptr(), ws.numel())
     return out
 
 

@@ -4,9 +4,17 @@
 // The contraction runs over the output features n, whose scales differ from row
 // to row, so a scale cannot be taken out of the sum: the packed codes are
 // dequantized on chip and the products run in bf16 with fp32 accumulation.
-// w is rounded to bf16 once (q is exact in bf16, sw q is not): 2^-8 relative per
-// product at most, independent from row to row, so about the error that the
-// rounding of a bf16 dx adds; dy is bf16 already.
+// dy is bf16 already.  w, 18 bits, enters as T bf16 terms:
+//   T = 1  rounded once, 2^-8 relative at most and independent from row to row, so about
+//          the error that the rounding of a bf16 dx adds (2.35e-3 of the norm for
+//          1.66e-3).  What a bf16 dx takes.
+//   T = 3  hi + mid + lo = w exactly, each term a step of its own over the same codes and
+//          dY, and sums of 512 rows n at a time are added to an fp32 dx in its own memory
+//          (tensor memory rounds every addition towards zero: 1.3e-6 of the norm with 512
+//          rows, 9.6e-6 with 4096; a bf16 dx is summed there throughout).  What an fp32 dx
+//          takes, at three times the products and more of the conversion (2048 tokens x
+//          9728 n x 1280 k: 325 us for 50).
+// The caller may choose either for either dx.
 //
 // A work unit is (128 columns k: one tile column; NT tokens; a range of n).  Per
 // step of 64 rows n:
@@ -60,6 +68,7 @@ constexpr int kRawBytes = kStep * kTileK + 256;  // INT8 codes, then 64 fp16 sca
 constexpr int kXfWarp0 = 4, kXfWarps = 4, kXfThreads = 32 * kXfWarps;  // groups of four warps
 constexpr int kEpiWarps = 4;
 constexpr int kMaxBwdSplits = 16;
+constexpr int kSumRows = 512;   // rows n summed in tensor memory for an exact fp32 dx
 
 template <int NT, int CG>
 struct BwdShape {
@@ -93,7 +102,8 @@ struct BwdArgs {
   const int32_t* tile_idx;
   const uint16_t* scales;
   int N, K, bN, C, T4, T8;
-  int M, ntb, steps;   // steps of a unit: N / 64
+  int M, ntb, steps;   // steps of a unit: T times N / 64
+  int chunk;           // steps summed in tensor memory (T = 3)
   int whole, S, units;  // units done whole, splits of the others, work items in all
   const void* add;
   void* dx;
@@ -173,24 +183,34 @@ __device__ __forceinline__ void mma_commit_all(uint64_t* bar) {
         : "memory");
 }
 
+// What the bf16 value of v leaves, exactly.
+__device__ __forceinline__ float2 bf16_rest(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&b) ^ 0x80008000u;  // - b
+  return __fadd2_rn(v, make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)));
+}
+
 // Four codes (two's-complement bytes) times sw, as two bf16 pairs.  The byte
 // b = q + 128 in the middle of a mantissa is 32768 + b, and 32896 sw is exact (9 + 11
-// bits), so one fused multiply-add gives sw q exactly, which is then rounded once.
-__device__ __forceinline__ uint2 codes4(uint32_t w, float2 sw, float2 off) {
+// bits), so one fused multiply-add gives sw q exactly.
+__device__ __forceinline__ void codes4(uint32_t w, float2 sw, float2 off, float2& p, float2& q) {
   const uint32_t x = w ^ 0x80808080u;
-  const float2 p = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7604)),
-                                          __uint_as_float(__byte_perm(x, 0x47000000u, 0x7614))), sw, off);
-  const float2 q = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7624)),
-                                          __uint_as_float(__byte_perm(x, 0x47000000u, 0x7634))), sw, off);
+  p = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7604)),
+                                    __uint_as_float(__byte_perm(x, 0x47000000u, 0x7614))), sw, off);
+  q = __ffma2_rn(make_float2(__uint_as_float(__byte_perm(x, 0x47000000u, 0x7624)),
+                                    __uint_as_float(__byte_perm(x, 0x47000000u, 0x7634))), sw, off);
+}
+__device__ __forceinline__ uint2 round4(float2 p, float2 q) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(p.x, p.y), b = __floats2bfloat162_rn(q.x, q.y);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-template <int NT, int CG>
+template <int NT, int CG, int T>
 __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
     linear_backward_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
   using Sh = BwdShape<NT, CG>;
   constexpr int SA = Sh::kSA, SB = Sh::kSB, RW = Sh::kRaw, H = Sh::kHalves;
+  static_assert(T == 1 || H == 1, "sums of part of a unit alternate between two accumulators");
   constexpr int kXfGroups = Sh::kXfGroups, kEpiWarp0 = Sh::kEpiWarp0;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -275,7 +295,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       kind = 2;
       row = sc = 0;
       if (u < a.units) {
-        const int n0 = (x.i0 + (int)(g - base)) * kStep, r = n0 / a.bN, in = n0 - r * a.bN;
+        const int n0 = (x.i0 + (int)(g - base)) / T * kStep, r = n0 / a.bN, in = n0 - r * a.bN;
         const int t = r * a.C + x.kb * CG + rank;
         kind = __ldg(a.bitmap + (t >> 3)) >> (t & 7) & 1;
         row = (uint32_t)__ldg(a.tile_idx + t) * a.bN + in;
@@ -322,7 +342,11 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       bool ok = true, any = false;
       for (int u = first_unit; ok && u < a.units; u += stride) {
         const BwdUnit x = bwd_unit(a, u);
+        int left = 0;  // steps of the sum that is being formed
         for (int i = x.i0; ok && i < x.i1; ++i) {
+          const bool first = T == 1 ? i == x.i0 : left == 0;
+          if (T > 1) left = (left == 0 ? min(a.chunk, x.i1 - i) : left) - 1;
+          const bool last = T == 1 ? i + 1 == x.i1 : left == 0;
           if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag) &&
                                            mbar_wait(&a_full[sr.i], sr.ph, abort_flag))) {
             fail(3);
@@ -332,7 +356,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             const int buf = H == 2 ? h : ar.i;
-            if (i == x.i0 && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
+            if (first && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
               fail(2);
               ok = false;
               break;
@@ -344,21 +368,21 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kStep / 16; ++k)  // 16 rows: two groups of A, 32 bytes of B
-                mma_bf16<CG>(d, ao + 128 * k, bo + 2 * k, Sh::kIdesc, i > x.i0 || k > 0);
+                mma_bf16<CG>(d, ao + 128 * k, bo + 2 * k, Sh::kIdesc, !first || k > 0);
               if (h == H - 1) {
                 mma_commit_all<CG>(&a_done[sr.i]);
                 mma_commit_all<CG>(&b_done[br.i]);
               }
-              if (i + 1 == x.i1) mma_commit_all<CG>(&acc_full[buf]);
+              if (last) mma_commit_all<CG>(&acc_full[buf]);
             }
             __syncwarp();
             any = true;
           }
           sr.template next<SA>();
           br.template next<SB>();
+          if (H == 1 && last) ar.template next<2>();
         }
         if (H == 2) ar.ph ^= 1u;
-        else ar.template next<2>();
       }
       if (any || CG == 2) {  // every MMA issued is complete before tensor memory is freed
         if (elect_one()) mma_commit_all<CG>(drain);
@@ -386,8 +410,8 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           for (int h = 0; h < H; ++h) {
             uint8_t* dst = stage_b(br.i) + h * (Sh::kB / H);
             const int m = x.tb * NT + h * Sh::kN + rank * (Sh::kN / CG);
-            if constexpr (CG == 1) tma_load_2d(dst, &maps.dy, i * kStep, m, &b_full[br.i]);
-            else tma_load_2d_lead(dst, &maps.dy, i * kStep, m, &b_full[br.i]);
+            if constexpr (CG == 1) tma_load_2d(dst, &maps.dy, i / T * kStep, m, &b_full[br.i]);
+            else tma_load_2d_lead(dst, &maps.dy, i / T * kStep, m, &b_full[br.i]);
           }
           br.template next<SB>();
         }
@@ -420,16 +444,29 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           const uint8_t* src = raw_slot(rr.i);
           const uint16_t* scl = reinterpret_cast<const uint16_t*>(src + kStep * kTileK);
           uint8_t* dst = stage_a(sr.i);
+          // (rotated, so that no group has the longest conversion throughout)
+          const int term = (i + i / T) % T;
           auto put = [&](int k, uint4 v, float s) {
             const float o = -32896.f * s;
             const float2 s2 = make_float2(s, s), o2 = make_float2(o, o);
-            const uint2 e0 = codes4(v.x, s2, o2), e1 = codes4(v.y, s2, o2), e2 = codes4(v.z, s2, o2), e3 = codes4(v.w, s2, o2);
+            float2 f[8];
+            codes4(v.x, s2, o2, f[0], f[1]);
+            codes4(v.y, s2, o2, f[2], f[3]);
+            codes4(v.z, s2, o2, f[4], f[5]);
+            codes4(v.w, s2, o2, f[6], f[7]);
+#pragma unroll 1
+            for (int t = 0; T > 1 && t < term; ++t)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = bf16_rest(f[j]);
+            const uint2 e0 = round4(f[0], f[1]), e1 = round4(f[2], f[3]), e2 = round4(f[4], f[5]), e3 = round4(f[6], f[7]);
             const uint4 lo = make_uint4(e0.x, e0.y, e1.x, e1.y), hi = make_uint4(e2.x, e2.y, e3.x, e3.y);
             *reinterpret_cast<uint4*>(dst + first + k * 2048) = late ? hi : lo;
             *reinterpret_cast<uint4*>(dst + second + k * 2048) = late ? lo : hi;
           };
+          // (compact with several terms: unrolled, and a copy of the code for each term, a step took twice as long)
+          constexpr int kUnrolled = T == 1 ? kStep / 16 : 1;
           if (raw_int4[rr.i]) {
-#pragma unroll
+#pragma unroll kUnrolled
             for (int k = 0; k < kStep / 16; ++k) {  // nibbles as 16 q: see tc_linear.cu
               const uint2 w = *reinterpret_cast<const uint2*>(src + (r0 + 16 * k) * (kTileK / 2) + c * 8);
               const uint32_t l0 = (w.x << 4) & 0xF0F0F0F0u, h0 = w.x & 0xF0F0F0F0u;
@@ -439,7 +476,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
                   __half2float(__ushort_as_half(scl[r0 + 16 * k])) * 0.0625f);
             }
           } else {
-#pragma unroll
+#pragma unroll kUnrolled
             for (int k = 0; k < kStep / 16; ++k)
               put(k, *reinterpret_cast<const uint4*>(src + (r0 + 16 * k) * kTileK + c * 16),
                   __half2float(__ushort_as_half(scl[r0 + 16 * k])));
@@ -462,56 +499,66 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
     const int quad = warp & 3, half = (warp - kEpiWarp0) / kEpiWarps;
     const size_t kcol = 32 * quad + lane;
     pdl_wait();
-    int ui = 0;
-    for (int u = first_unit; u < a.units; u += stride, ++ui) {
+    int ui = 0;  // sums taken over
+    bool ok = true;
+    for (int u = first_unit; ok && u < a.units; u += stride) {
       const BwdUnit x = bwd_unit(a, u);
-      const int buf = H == 2 ? half : ui & 1, phase = H == 2 ? ui & 1 : ui >> 1 & 1, m0 = x.tb * NT + half * Sh::kN;
-      const size_t k = (size_t)(x.kb * CG + rank) * kTileK + kcol;
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], phase, abort_flag))) {
-        fail(6);
-        break;
-      }
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * Sh::kN;
-      // a lane holds one column k of every token: a warp's stores cover 32 columns
-      float* fp = x.part >= 0 ? a.partial + ((size_t)(x.part * CG + rank) * NT + half * Sh::kN) * kTileK + kcol
-                              : static_cast<float*>(a.dx) + (size_t)m0 * a.lddx + k;
-      __nv_bfloat16* bp = static_cast<__nv_bfloat16*>(a.dx) + (size_t)m0 * a.lddx + k;
-      const size_t fld = x.part >= 0 ? kTileK : a.lddx;
-      const bool f32 = a.f32 || x.part >= 0, add = a.add && x.part < 0;
-      const int cols = min(Sh::kN, a.M - m0);  // (none: below 0)
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + c0, v);
-        float y[16];
-        if (add)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c0 + e < cols)
-              y[e] = a.f32 ? static_cast<const float*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]
-                           : bf16_bits_to_float(static_cast<const uint16_t*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          asm volatile("" : "+r"(v[e]));
-          if (add && c0 + e < cols) v[e] = __float_as_uint(__uint_as_float(v[e]) + y[e]);
+      for (int i = x.i0; i < x.i1; i = T == 1 ? x.i1 : i + a.chunk, ++ui) {
+        const int buf = H == 2 ? half : ui & 1, phase = H == 2 ? ui & 1 : ui >> 1 & 1, m0 = x.tb * NT + half * Sh::kN;
+        const size_t k = (size_t)(x.kb * CG + rank) * kTileK + kcol;
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], phase, abort_flag))) {
+          fail(6);
+          ok = false;
+          break;
         }
-        const int left = cols - c0;
-        if (f32) {
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(32 * quad) << 16) + buf * Sh::kN;
+        // a lane holds one column k of every token: a warp's stores cover 32 columns
+        float* fp = x.part >= 0 ? a.partial + ((size_t)(x.part * CG + rank) * NT + half * Sh::kN) * kTileK + kcol
+                                : static_cast<float*>(a.dx) + (size_t)m0 * a.lddx + k;
+        __nv_bfloat16* bp = static_cast<__nv_bfloat16*>(a.dx) + (size_t)m0 * a.lddx + k;
+        const size_t fld = x.part >= 0 ? kTileK : a.lddx;
+        // A unit's later sums (T = 3, fp32 throughout) are added to what the same thread has stored, at L2, in the
+        // order of its stores, so the result is the same on every run.  (A value below 2^-126 may become zero there.)
+        const bool f32 = a.f32 || x.part >= 0, more = T > 1 && i > x.i0, add = a.add && x.part < 0 && !more;
+        const int cols = min(Sh::kN, a.M - m0);  // (none: below 0)
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(taddr + c0, v);
+          const int left = cols - c0;
+          float y[16];
+          if (add)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < left) fp[(size_t)e * fld] = __uint_as_float(v[e]);
-        } else {
+            for (int e = 0; e < 16; ++e)
+              if (e < left)
+                y[e] = a.f32 ? static_cast<const float*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]
+                             : bf16_bits_to_float(static_cast<const uint16_t*>(a.add)[(size_t)(m0 + c0 + e) * a.ldadd + k]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < left) bp[(size_t)e * a.lddx] = __float2bfloat16_rn(__uint_as_float(v[e]));
+          for (int e = 0; e < 16; ++e) {
+            asm volatile("" : "+r"(v[e]));
+            if (add && e < left) v[e] = __float_as_uint(__uint_as_float(v[e]) + y[e]);
+          }
+          if (more) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < left) atomicAdd(fp + (size_t)e * fld, __uint_as_float(v[e]));
+          } else if (f32) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < left) fp[(size_t)e * fld] = __uint_as_float(v[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < left) bp[(size_t)e * a.lddx] = __float2bfloat16_rn(__uint_as_float(v[e]));
+          }
+          fp += 16 * fld;
+          bp += (size_t)16 * a.lddx;
         }
-        fp += 16 * fld;
-        bp += (size_t)16 * a.lddx;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_lead<CG>(&acc_empty[buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_lead<CG>(&acc_empty[buf]);
     }
   }
 
@@ -590,12 +637,12 @@ constexpr BwdForm kBwdForms[] = {{1, 32, 40, 30},   {1, 64, 40, 40},   {1, 128, 
 
 // The form and the splits of least time: the steps of the CTA that has most, its units'
 // ends, and for a split the second launch with its 4 bytes written and read per sum.
-BwdPlan plan_bwd(int M, int N, int C) {
-  const int steps = N / kStep;
+BwdPlan plan_bwd(int M, int N, int C, int terms) {
+  const int steps = N / kStep * terms;
   BwdPlan best{0, 0, 0, 0, 0, 1};
   long long best_cost = 0;
   for (const BwdForm& f : kBwdForms) {
-    if (C % f.cg) continue;
+    if (C % f.cg || (terms > 1 && f.nt > 256)) continue;
     const int ntb = (M + f.nt - 1) / f.nt, slots = num_sms() / f.cg;
     const long long units = (long long)C / f.cg * ntb, rounds = units / slots;
     const int rest = (int)(units % slots), most = rest ? std::max(1, std::min({slots / rest, steps / 4, kMaxBwdSplits})) : 1;
@@ -612,10 +659,10 @@ BwdPlan plan_bwd(int M, int N, int C) {
   return best;
 }
 
-template <int NT, int CG>
+template <int NT, int CG, int T>
 cudaError_t launch_bwd(const aq_packed* w, const uint16_t* dy, int ldd, const BwdArgs& a, cudaStream_t st) {
   using Sh = BwdShape<NT, CG>;
-  cudaError_t e = ensure_smem_attr<linear_backward_kernel<NT, CG>>(Sh::kSmem);
+  cudaError_t e = ensure_smem_attr<linear_backward_kernel<NT, CG, T>>(Sh::kSmem);
   if (e != cudaSuccess) return e;
   BwdMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -639,7 +686,32 @@ cudaError_t launch_bwd(const aq_packed* w, const uint16_t* dy, int ldd, const Bw
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, linear_backward_kernel<NT, CG>, maps, a);
+  return cudaLaunchKernelEx(&cfg, linear_backward_kernel<NT, CG, T>, maps, a);
+}
+
+template <int T>
+cudaError_t launch_form(const BwdPlan& p, const aq_packed* w, const uint16_t* dy, int ldd, const BwdArgs& a,
+                        cudaStream_t st) {
+  switch (p.cg * 1000 + p.nt) {
+    case 1032: return launch_bwd<32, 1, T>(w, dy, ldd, a, st);
+    case 1064: return launch_bwd<64, 1, T>(w, dy, ldd, a, st);
+    case 1128: return launch_bwd<128, 1, T>(w, dy, ldd, a, st);
+    case 1256: return launch_bwd<256, 1, T>(w, dy, ldd, a, st);
+    case 2256: return launch_bwd<256, 2, T>(w, dy, ldd, a, st);
+  }
+  if constexpr (T == 1) {
+    if (p.cg * 1000 + p.nt == 2384) return launch_bwd<384, 2, 1>(w, dy, ldd, a, st);
+    if (p.cg * 1000 + p.nt == 2512) return launch_bwd<512, 2, 1>(w, dy, ldd, a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// Terms of the weights for dxdtype (see aq_linear_backward); 0: not a valid one.
+int bwd_terms(int dxdtype) {
+  const int type = dxdtype & 0xFF, weights = dxdtype - type;
+  if (type != AQ_F32 && type != AQ_BF16) return 0;
+  if (weights == 0) return type == AQ_F32 ? 3 : 1;
+  return weights == AQ_WEIGHTS_EXACT ? 3 : weights == AQ_WEIGHTS_BF16 ? 1 : 0;
 }
 
 constexpr int kMaxBwdTokens = 1 << 21;
@@ -651,8 +723,12 @@ using namespace aq;
 
 extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) {
   if (validate_packed(w) != AQ_OK || M < 1 || M > kMaxBwdTokens) return 0;
-  const BwdPlan p = plan_bwd(M, w->N, w->C);
-  return kWsHeader + (size_t)p.rest * p.S * p.cg * p.nt * kTileK * sizeof(float);
+  size_t most = 0;
+  for (int terms : {1, 3}) {
+    const BwdPlan p = plan_bwd(M, w->N, w->C, terms);
+    most = std::max(most, (size_t)p.rest * p.S * p.cg * p.nt * kTileK * sizeof(float));
+  }
+  return kWsHeader + most;
 }
 
 extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
@@ -660,7 +736,9 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   int rc = validate_packed(w);
   if (rc != AQ_OK) return rc;
   if (!dy || !dx || M < 1 || M > kMaxBwdTokens || ldd < w->N || ldd % 8 || ((uintptr_t)dy & 15)) return AQ_ERR_ARG;
-  if (dxdtype != AQ_F32 && dxdtype != AQ_BF16) return AQ_ERR_ARG;
+  const int terms = bwd_terms(dxdtype);
+  if (terms == 0) return AQ_ERR_ARG;
+  dxdtype &= 0xFF;
   const int per16 = dxdtype == AQ_F32 ? 4 : 8;
   if (lddx < w->K || lddx % per16 || ((uintptr_t)dx & 15)) return AQ_ERR_ARG;
   if (add && (ldadd < w->K || ldadd % per16 || ((uintptr_t)add & 15))) return AQ_ERR_ARG;
@@ -672,12 +750,13 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   const Span outs[] = {{dx, lddx * elt, width, M}};
   const Span ins[] = {{dy, (size_t)ldd * 2, (size_t)w->N * 2, M}, {add == dx ? nullptr : add, ldadd * elt, width, M}};
   if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
-  const BwdPlan p = plan_bwd(M, w->N, w->C);
+  const BwdPlan p = plan_bwd(M, w->N, w->C, terms);
   BwdArgs a;
   memset(&a, 0, sizeof(a));
   a.bitmap = w->bitmap; a.tile_idx = w->tile_idx; a.scales = w->scales;
   a.N = w->N; a.K = w->K; a.bN = w->bN; a.C = w->C; a.T4 = w->T4; a.T8 = w->T8;
-  a.M = M; a.ntb = p.ntb; a.S = p.S; a.steps = w->N / kStep;
+  a.M = M; a.ntb = p.ntb; a.S = p.S; a.steps = w->N / kStep * terms;
+  a.chunk = dxdtype == AQ_F32 ? kSumRows / kStep * terms : 1 << 30;
   if (p.whole > 0x7FFF0000ll) return AQ_ERR_ARG;
   a.whole = (int)p.whole;
   a.units = a.whole + p.rest * p.S;
@@ -685,16 +764,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   a.ws = ws;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (p.cg * 1000 + p.nt) {
-    case 1032: e = launch_bwd<32, 1>(w, dy, ldd, a, st); break;
-    case 1064: e = launch_bwd<64, 1>(w, dy, ldd, a, st); break;
-    case 1128: e = launch_bwd<128, 1>(w, dy, ldd, a, st); break;
-    case 1256: e = launch_bwd<256, 1>(w, dy, ldd, a, st); break;
-    case 2256: e = launch_bwd<256, 2>(w, dy, ldd, a, st); break;
-    case 2384: e = launch_bwd<384, 2>(w, dy, ldd, a, st); break;
-    case 2512: e = launch_bwd<512, 2>(w, dy, ldd, a, st); break;
-  }
+  cudaError_t e = terms == 3 ? launch_form<3>(p, w, dy, ldd, a, st) : launch_form<1>(p, w, dy, ldd, a, st);
   if (e == cudaSuccess && p.rest > 0)
     e = launch_pdl(linear_backward_sum_kernel, dim3((p.nt * (kTileK / 4) + 255) / 256, p.rest * p.cg), dim3(256), 0, st, a,
                    p.nt, p.cg);
