@@ -106,3 +106,35 @@ def test_linear_backward_keeps_fp32(M, N, K, bN):
     got16 = aq.aq_linear_backward(w, dy, weights=torch.float32)
     own = (ref.to(torch.bfloat16).double() - ref).norm()
     assert (got16.double() - ref).norm() <= own * 1.01 + 3 * N / 16 * U * ref.norm()
+
+
+def whole_numbers(N, K, bN, frac8, seed):
+    """Packed weights that are whole multiples of 2^-4, 8 bits wide at most, and their values."""
+    g = rng(seed)
+    R, C = N // bN, K // 128
+    pmap = torch.ones(R * C, dtype=torch.uint8, device="cuda")
+    pmap[torch.randperm(R * C, generator=g, device="cuda")[: round(frac8 * R * C)]] = 0
+    pmap = pmap.view(R, C)
+    codes = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int16)
+    int4 = pmap.bool().repeat_interleave(bN, 0).repeat_interleave(128, 1)
+    codes = torch.where(int4, (codes & 15) - 8, codes).to(torch.int8)
+    scales = 2.0 ** torch.randint(-4, -2, (N, C), generator=g, device="cuda")
+    w = (codes.double().view(N, C, 128) * scales.double()[:, :, None]).view(N, K)
+    return aq.aq_pack(codes, scales.to(torch.float16), pmap, bN, 128), w
+
+
+@pytest.mark.parametrize("M,N,K,bN", SUMS + [(2, 14336, 256, 128), (16, 4864, 256, 128), (900, 2048, 2176, 128),
+                                             (513, 4864, 2560, 128), (1500, 2560, 4096, 128), (2048, 2560, 9728, 128),
+                                             (6000, 512, 640, 64), (4096, 14336, 512, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("weights", [torch.bfloat16, torch.float32])
+def test_linear_backward_sums_every_row(M, N, K, bN, dtype, weights):
+    """Weights of 8 bits times dy in -2 .. 2: every sum is a whole multiple of 2^-4 below 2^24
+    of them (2 x 256 x 14336 < 2^23), so fp32 holds it in any order and the result is exact: a
+    step, a row or an entry that is left out or taken twice shows."""
+    w, w64 = whole_numbers(N, K, bN, 0.5, N + K + M)
+    dy = torch.randint(-2, 3, (M, N), generator=rng(M), device="cuda").to(torch.bfloat16)
+    add = torch.randint(-64, 65, (M, K), generator=rng(M + 1), device="cuda").to(dtype)
+    ref = dy.double() @ w64
+    assert torch.equal(aq.aq_linear_backward(w, dy, out_dtype=dtype, weights=weights), ref.to(dtype))
+    assert torch.equal(aq.aq_linear_backward(w, dy, add=add, weights=weights), (ref + add.double()).to(dtype))
