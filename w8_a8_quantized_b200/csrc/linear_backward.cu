@@ -160,15 +160,46 @@ __device__ __forceinline__ void tma_load_2d_lead(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(lead_addr(bar))
       : "memory");
 }
-// Arrive at the leader's barrier.  (The products read each CTA's tiles in that CTA's own
-// memory: what it wrote has to be complete there, by the fence before the arrival.  A
-// release at cluster scope made the transform's step twice as long.)
+// Arrive at the leader's barrier.  Its products read tiles that this CTA wrote into its own
+// memory, so what came before is released at cluster scope; only for shared memory, which is all
+// that the leader reads.  (With a release of all memory each step waited for the copies and stores
+// under way: 8192 x 14336 x 4096 took 820 us for 677.)
 template <int CG>
 __device__ __forceinline__ void arrive_lead(uint64_t* bar) {
   if constexpr (CG == 1)
     mbar_arrive(bar);
   else
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(lead_addr(bar)) : "memory");
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(lead_addr(bar))
+        : "memory");
+}
+// The leader's mbar_wait on what the other CTA of the pair arrives at or its copies complete:
+// acquires at cluster scope.
+template <int CG>
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if constexpr (CG == 1) return mbar_wait(bar, parity, abort);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (ok) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+  }
 }
 // Arrive at the barriers of both CTAs when every MMA issued so far is done.
 template <int CG>
@@ -347,8 +378,8 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           const bool first = T == 1 ? i == x.i0 : left == 0;
           if (T > 1) left = (left == 0 ? min(a.chunk, x.i1 - i) : left) - 1;
           const bool last = T == 1 ? i + 1 == x.i1 : left == 0;
-          if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag) &&
-                                           mbar_wait(&a_full[sr.i], sr.ph, abort_flag))) {
+          if (!__all_sync(0xffffffffu, pair_wait<CG>(&b_full[br.i], br.ph, abort_flag) &&
+                                           pair_wait<CG>(&a_full[sr.i], sr.ph, abort_flag))) {
             fail(3);
             ok = false;
             break;
@@ -356,7 +387,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             const int buf = H == 2 ? h : ar.i;
-            if (first && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
+            if (first && !__all_sync(0xffffffffu, pair_wait<CG>(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
               fail(2);
               ok = false;
               break;
@@ -484,7 +515,8 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            arrive_lead<CG>(&a_full[sr.i]);
+            if (CG == 1 || rank == 0) mbar_arrive(&a_full[sr.i]);
+            else arrive_lead<CG>(&a_full[sr.i]);
             mbar_arrive(&raw_empty[rr.i]);
           }
         }
