@@ -597,9 +597,11 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (CG == 2) {
-    if (warp == 1) mbar_wait(drain, 0, never_flag);  // the leader's last arrival has come to this CTA too
-    __syncwarp();
     cluster_sync();  // the other's products may read this CTA's memory until here
+    // The leader's last arrival has come to this CTA too.  (After the barrier: the leader, should it have
+    // given up later than this CTA, has issued it by then, and this wait cannot run out before it.)
+    if (warp == 1) mbar_wait(drain, 0, never_flag);
+    __syncwarp();
   }
   if (warp == 1) {
     tc_fence_after();
