@@ -545,6 +545,21 @@ int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, c
 size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w);
 
 /*
+ * aq_debug_linear_stalled for the kernels of aq_lora_backward (kernel 0: the contraction, 1: the expansion, both
+ * of more than 64 tokens with ranks up to 64; 2: the weight gradients) and of aq_linear_backward:
+ * the producer of the activations, of y or of the weights stops after `stop_after` copies of each CTA (in a
+ * pair of CTAs the second's).  Outputs are unspecified; aq_workspace_status() reports AQ_ERR_TIMEOUT and
+ * the workspace serves ordinary calls again.  Errors: as for the calls.
+ */
+int aq_debug_lora_backward_stalled(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M,
+                                   const float* s, const void* x, int ldx, const float* sx, float* da, float* dbt,
+                                   void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes, int kernel,
+                                   unsigned long long wait_ns, int stop_after, void* stream);
+int aq_debug_linear_backward_stalled(const aq_packed* w, const uint16_t* dy, int ldd, int M, void* dx, int lddx,
+                                     int dxdtype, void* ws, size_t ws_bytes, unsigned long long wait_ns,
+                                     int stop_after, void* stream);
+
+/*
  * Decode-phase linear layer for callers that cannot allocate device memory
  * (code running inside an allocator or memory-pool callback, runtimes that
  * forbid allocation after start-up to keep a fixed footprint, plug-ins handed

@@ -212,3 +212,18 @@ def test_binding_refuses_host_tensors():
     (0x300, ARG), (0x102, ARG), (0x400, ARG), (-1, ARG)])
 def test_linear_backward_weights(dtype, status):
     assert linear_back(dtype=dtype, ws=None) == status
+
+
+@pytest.mark.parametrize("kw", [dict(wait=1000), dict(wait=20_000_000_000), dict(after=-1), dict(kernel=3), dict(kernel=-1),
+                                dict(kernel=0, M=64), dict(kernel=1, ad=lora(max_rank=65, R=80)), dict(dx=None)])
+def test_stalled_lora_refusals(kw):
+    v = dict(ad=lora(), M=70, dx=16, kernel=2, wait=20_000_000, after=0)
+    v.update(kw)
+    assert aq.lib().aq_debug_lora_backward_stalled(v["ad"], 16, 128, 16, v["M"], 16, 16, 256, 16, 16, 16, v["dx"], 256, 0,
+                                                   None, 0, v["kernel"], v["wait"], v["after"], None) == ARG
+
+
+@pytest.mark.parametrize("wait,after,status", [(1000, 0, ARG), (20_000_000_000, 0, ARG), (20_000_000, -1, ARG),
+                                               (20_000_000, 0, WORKSPACE)])
+def test_stalled_linear_backward_refusals(wait, after, status):
+    assert aq.lib().aq_debug_linear_backward_stalled(packed(), 16, 128, 4, 16, 256, 0, None, 0, wait, after, None) == status

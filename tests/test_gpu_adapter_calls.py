@@ -1,6 +1,8 @@
 """Calls of the adapter, gated-activation and input-gradient entries at the edges of what
 they document: buffers beside and over one another, captured calls and their workspaces,
 waits that give up, long sums."""
+import time
+
 import pytest
 import torch
 
@@ -138,3 +140,64 @@ def test_linear_backward_sums_every_row(M, N, K, bN, dtype, weights):
     ref = dy.double() @ w64
     assert torch.equal(aq.aq_linear_backward(w, dy, out_dtype=dtype, weights=weights), ref.to(dtype))
     assert torch.equal(aq.aq_linear_backward(w, dy, add=add, weights=weights), (ref + add.double()).to(dtype))
+
+
+# ------------------------------------------------------------------ waits that give up
+
+WAIT_NS = 20_000_000
+
+
+def gave_up(ws, codes, t0):
+    rc, info = aq.aq_workspace_status(ws)  # synchronizes
+    assert rc == -7 and info in codes, (rc, info)
+    assert time.monotonic() - t0 < 5.0
+    assert not ws[:256].any()
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [
+    (64, 1024, 256, torch.bfloat16), (300, 1024, 384, torch.bfloat16), (300, 1024, 384, torch.float32),  # single CTAs
+    (1030, 512, 5120, torch.bfloat16), (2048, 512, 2560, torch.bfloat16), (2048, 1024, 2560, torch.float32)])  # pairs
+@pytest.mark.parametrize("stop_after", [0, 3])
+def test_stalled_input_gradient(M, N, K, dtype, stop_after):
+    """A weight producer that stops (in a pair the second CTA's): every role gives up, the error is
+    reported, and the same workspace serves ordinary calls."""
+    w, _ = packed(N, K, 128, 0.5, 7)
+    dy = normal(rng(M), M, N, scale=0.01)
+    want = aq.aq_linear_backward(w, dy, out_dtype=dtype)
+    ws = torch.zeros(aq.aq_linear_backward_workspace_bytes(M, w), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    aq.aq_debug_linear_backward_stalled(w, dy, ws, out_dtype=dtype, wait_ns=WAIT_NS, stop_after=stop_after)
+    gave_up(ws, range(1, 8), t0)
+    assert torch.equal(aq.aq_linear_backward(w, dy, out_dtype=dtype, ws=ws), want)
+    assert aq.aq_workspace_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("kernel,codes", [(0, range(31, 37)), (1, range(41, 47)), (2, range(21, 27))])
+@pytest.mark.parametrize("ranks", [[8, 24], [16, 40], [64]])
+@pytest.mark.parametrize("checkpoint", [True, False])
+@pytest.mark.parametrize("stop_after", [0, 2])
+def test_stalled_adapters(kernel, codes, ranks, checkpoint, stop_after):
+    M, N, K = 6000 if stop_after else 333, 1024, 1536
+    c = LoraCase(M, N, K, ranks, mixed_ids(M, len(ranks), 3), seed=3)
+    s = torch.empty(M, max(ranks), device="cuda")
+    aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    x, sx = aq.aq_quant_act(c.x) if checkpoint else (c.x, None)
+    want = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, x, sx=sx)
+    ws = torch.zeros(aq.aq_lora_workspace_bytes(c.ad, M, True), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    aq.aq_debug_lora_backward_stalled(c.ad, c.dy, c.ids, s, x, sx, kernel, ws, wait_ns=WAIT_NS, stop_after=stop_after)
+    gave_up(ws, codes, t0)
+    got = aq.aq_lora_backward(c.ad, c.dy, c.ids, s, x, sx=sx, ws=ws)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert aq.aq_workspace_status(ws) == (0, 0)
+
+
+def test_stalled_weight_gradients_of_few_tokens():
+    c = LoraCase(30, 256, 512, [4, 7, 130], mixed_ids(30, 3, 3), seed=3)
+    s = torch.zeros(30, 130, device="cuda")
+    ws = torch.zeros(aq.aq_lora_workspace_bytes(c.ad, 30, True), dtype=torch.uint8, device="cuda")
+    t0 = time.monotonic()
+    aq.aq_debug_lora_backward_stalled(c.ad, c.dy, c.ids, s, c.x, None, 2, ws, wait_ns=WAIT_NS, stop_after=0)
+    gave_up(ws, range(21, 27), t0)

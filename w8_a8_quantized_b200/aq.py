@@ -29,7 +29,8 @@ EXPORTED = ("aq_status_str", "aq_packed_sizes", "aq_pack_metadata", "aq_pack", "
             "aq_linear_prefill_expanded", "aq_act_group_rows", "aq_quant_act_groups", "aq_measure_i8_peak",
             "aq_debug_linear_stalled", "aq_pack_tiles", "aq_paper_quant_act", "aq_paper_linear",
             "aq_debug_paper_partials", "aq_lora_apply", "aq_lora_backward", "aq_lora_workspace_bytes",
-            "aq_silu_mul_quant", "aq_silu_mul_backward", "aq_linear_backward", "aq_linear_backward_workspace_bytes")
+            "aq_silu_mul_quant", "aq_silu_mul_backward", "aq_linear_backward", "aq_linear_backward_workspace_bytes",
+            "aq_debug_lora_backward_stalled", "aq_debug_linear_backward_stalled")
 
 
 class AqError(RuntimeError):
@@ -142,6 +143,13 @@ def lib():
                                      c_size_t, c_void_p]
     L.aq_linear_backward_workspace_bytes.restype = c_size_t
     L.aq_linear_backward_workspace_bytes.argtypes = [c_int, P]
+    L.aq_debug_lora_backward_stalled.restype = c_int
+    L.aq_debug_lora_backward_stalled.argtypes = [A, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p,
+                                                 c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_size_t, c_int,
+                                                 ctypes.c_ulonglong, c_int, c_void_p]
+    L.aq_debug_linear_backward_stalled.restype = c_int
+    L.aq_debug_linear_backward_stalled.argtypes = [P, c_void_p, c_int, c_int, c_void_p, c_int, c_int, c_void_p, c_size_t,
+                                                   ctypes.c_ulonglong, c_int, c_void_p]
     _lib = L
     return L
 
@@ -953,6 +961,39 @@ def aq_debug_linear_stalled(w: PackedWeights, xq, sx, phase: int, ws: torch.Tens
         _check(lib().aq_debug_linear_stalled(ctypes.byref(w.struct), xq.data_ptr(), sx.data_ptr(), M, phase,
                                              out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel(), wait_ns,
                                              stop_after, _stream(w.device)), "aq_debug_linear_stalled")
+    return out
+
+
+def aq_debug_lora_backward_stalled(ad: Adapters, dy, ids, s, x, sx, kernel: int, ws: torch.Tensor,
+                                   wait_ns: int = 20_000_000, stop_after: int = 1):
+    """aq_lora_backward with a stage of one of its kernels (0 contraction, 1 expansion, 2
+    weight gradients) that never fills: returns the (unspecified) gradients; the error
+    lands in `ws`.  Contiguous tensors, as aq_lora_backward checks them."""
+    M = dy.shape[0]
+    da, dbt = _new(ad.R, ad.K, _F32, ad.device), _new(ad.R, ad.N, _F32, ad.device)
+    dx = _new(M, ad.K, _BF16, ad.device)
+    for t, name, dtype, shape in ((dy, "dy", _BF16, (M, ad.N)), (ids, "ids", torch.int32, (M,)),
+                                  (s, "s", _F32, (M, ad.max_rank)),
+                                  (x, "x", _BF16 if sx is None else torch.int8, (M, ad.K))):
+        _exact(t, name, dtype, ad.device, shape)
+    if sx is not None:
+        _exact(sx, "sx", _F32, ad.device, (M,))
+    _call(lib().aq_debug_lora_backward_stalled, "aq_debug_lora_backward_stalled", ad.device, ad.ref, dy.data_ptr(), ad.N,
+          ids.data_ptr(), M, s.data_ptr(), x.data_ptr(), ad.K, None if sx is None else sx.data_ptr(), da.data_ptr(),
+          dbt.data_ptr(), dx.data_ptr(), ad.K, AQ_BF16, ws.data_ptr(), ws.numel(), kernel, wait_ns, stop_after)
+    return da, dbt, dx
+
+
+def aq_debug_linear_backward_stalled(w: PackedWeights, dy, ws: torch.Tensor, out_dtype=torch.bfloat16,
+                                     wait_ns: int = 20_000_000, stop_after: int = 1) -> torch.Tensor:
+    """aq_linear_backward with a weight producer that stops: returns the (unspecified)
+    result; the error lands in `ws`."""
+    M = dy.shape[0]
+    _exact(dy, "dy", _BF16, w.device, (M, w.N))
+    out = _new(M, w.K, out_dtype, w.device)
+    _call(lib().aq_debug_linear_backward_stalled, "aq_debug_linear_backward_stalled", w.device, ctypes.byref(w.struct),
+          dy.data_ptr(), w.N, M, out.data_ptr(), w.K, AQ_F32 if out_dtype == _F32 else AQ_BF16, ws.data_ptr(),
+          ws.numel(), wait_ns, stop_after)
     return out
 
 

@@ -308,7 +308,7 @@ extern "C" int aq_debug_linear_stalled(const aq_packed* w, const int8_t* xq, con
   if (rc != AQ_OK) return rc;
   if (phase != AQ_PHASE_DECODE && phase != AQ_PHASE_PREFILL) return AQ_ERR_ARG;
   if (phase == AQ_PHASE_DECODE && (M > kMaxDecodeM || plan_decode(M, w).kernel != 1)) return AQ_ERR_ARG;
-  if (wait_ns < 100000ull || wait_ns > 10000000000ull || stop_after < 0) return AQ_ERR_ARG;
+  if (!stall_ok(wait_ns, stop_after)) return AQ_ERR_ARG;
   const size_t need = phase == AQ_PHASE_DECODE ? decode_ws_bytes(M, w) : prefill_ws_bytes(M, w);
   if ((rc = check_ws(ws, ws_bytes, need)) != AQ_OK) return rc;
   return launch_tc_stalled(w, xq, sx, M, y, ldy, ws, phase, wait_ns, stop_after, static_cast<cudaStream_t>(stream)) ==

@@ -39,6 +39,16 @@ struct WsHeader {
 // AQ_ERR_TIMEOUT in the workspace and lets the kernel wind down.
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s
 
+// The limit of a launch's bounded waits and, in the tests of the waits, the steps after which a
+// producer stops, so that later stages never fill (-1: never).
+struct Stall {
+  unsigned long long wait_ns = kWaitTimeoutNs;
+  int stop_after = -1;
+};
+inline bool stall_ok(unsigned long long wait_ns, int stop_after) {
+  return wait_ns >= 100000ull && wait_ns <= 10000000000ull && stop_after >= 0;
+}
+
 inline bool geometry_ok(int N, int K, int bN, int bK) {
   return N > 0 && K > 0 && (bN == 64 || bN == 128) && bK == kTileK && N % bN == 0 && K % bK == 0 &&
          (long long)N * K < (1ll << 40);

@@ -110,6 +110,7 @@ struct BwdArgs {
   int ldadd, lddx, f32;
   void* ws;
   float* partial;  // [split work item][NT][128]
+  Stall stall;     // (of a pair, the second CTA's weight producer stops)
 };
 
 struct BwdUnit {
@@ -177,8 +178,8 @@ __device__ __forceinline__ void arrive_lead(uint64_t* bar) {
 // The leader's mbar_wait on what the other CTA of the pair arrives at or its copies complete:
 // acquires at cluster scope.
 template <int CG>
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if constexpr (CG == 1) return mbar_wait(bar, parity, abort);
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
+  if constexpr (CG == 1) return mbar_wait(bar, parity, abort, limit_ns);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -198,7 +199,7 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volati
         : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitSuspendNs)
         : "memory");
     if (ok) return true;
-    if (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+    if (*abort || globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
 // Arrive at the barriers of both CTAs when every MMA issued so far is done.
@@ -338,6 +339,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
     fetch(row[0], sc[0], kind[0]);
     Ring rr{0, 0};
     bool more = true, ok = true;
+    int steps = 0;
     while (more && ok) {
       fetch(row[1], sc[1], kind[1]);
       for (int i = 0; i < 32 && ok; ++i) {
@@ -347,7 +349,12 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           more = false;
           break;
         }
-        if (!__all_sync(0xffffffffu, lane != 0 || mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag))) {
+        if (a.stall.stop_after >= 0 && rank == CG - 1 && steps++ == a.stall.stop_after) {
+          stalled(abort_flag, a.stall.wait_ns);
+          ok = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, lane != 0 || mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
           fail(1);
           ok = false;
         } else if (lane == 0) {
@@ -378,8 +385,8 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
           const bool first = T == 1 ? i == x.i0 : left == 0;
           if (T > 1) left = (left == 0 ? min(a.chunk, x.i1 - i) : left) - 1;
           const bool last = T == 1 ? i + 1 == x.i1 : left == 0;
-          if (!__all_sync(0xffffffffu, pair_wait<CG>(&b_full[br.i], br.ph, abort_flag) &&
-                                           pair_wait<CG>(&a_full[sr.i], sr.ph, abort_flag))) {
+          if (!__all_sync(0xffffffffu, pair_wait<CG>(&b_full[br.i], br.ph, abort_flag, a.stall.wait_ns) &&
+                                           pair_wait<CG>(&a_full[sr.i], sr.ph, abort_flag, a.stall.wait_ns))) {
             fail(3);
             ok = false;
             break;
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
 #pragma unroll
           for (int h = 0; h < H; ++h) {
             const int buf = H == 2 ? h : ar.i;
-            if (first && !__all_sync(0xffffffffu, pair_wait<CG>(&acc_empty[buf], ar.ph ^ 1u, abort_flag))) {
+            if (first && !__all_sync(0xffffffffu, pair_wait<CG>(&acc_empty[buf], ar.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
               fail(2);
               ok = false;
               break;
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       if (any || CG == 2) {  // every MMA issued is complete before tensor memory is freed
         if (elect_one()) mma_commit_all<CG>(drain);
         __syncwarp();
-        mbar_wait(drain, 0, never_flag);
+        mbar_wait(drain, 0, never_flag, a.stall.wait_ns);
       }
     }
   } else if (warp == 3) {
@@ -430,7 +437,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       for (int u = first_unit; ok && u < a.units; u += stride) {
         const BwdUnit x = bwd_unit(a, u);
         for (int i = x.i0; i < x.i1; ++i) {
-          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag)) {
+          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag, a.stall.wait_ns)) {
             fail(4);
             ok = false;
             break;
@@ -466,8 +473,8 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       const BwdUnit x = bwd_unit(a, u);
       for (int i = x.i0; i < x.i1; ++i) {
         if (turn == group) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag) &&
-                                           mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rr.i], rr.ph, abort_flag, a.stall.wait_ns) &&
+                                           mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
             fail(5);
             ok = false;
             break;
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
       for (int i = x.i0; i < x.i1; i = T == 1 ? x.i1 : i + a.chunk, ++ui) {
         const int buf = H == 2 ? half : ui & 1, phase = H == 2 ? ui & 1 : ui >> 1 & 1, m0 = x.tb * NT + half * Sh::kN;
         const size_t k = (size_t)(x.kb * CG + rank) * kTileK + kcol;
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], phase, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], phase, abort_flag, a.stall.wait_ns))) {
           fail(6);
           ok = false;
           break;
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(BwdShape<NT, CG>::kThreads, 1)
     cluster_sync();  // the other's products may read this CTA's memory until here
     // The leader's last arrival has come to this CTA too.  (After the barrier: the leader, should it have
     // given up later than this CTA, has issued it by then, and this wait cannot run out before it.)
-    if (warp == 1) mbar_wait(drain, 0, never_flag);
+    if (warp == 1) mbar_wait(drain, 0, never_flag, a.stall.wait_ns);
     __syncwarp();
   }
   if (warp == 1) {
@@ -765,8 +772,8 @@ extern "C" size_t aq_linear_backward_workspace_bytes(int M, const aq_packed* w) 
   return kWsHeader + most;
 }
 
-extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
-                                  void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes, void* stream) {
+static int linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd, void* dx,
+                           int lddx, int dxdtype, void* ws, size_t ws_bytes, const Stall& stall, void* stream) {
   int rc = validate_packed(w);
   if (rc != AQ_OK) return rc;
   if (!dy || !dx || M < 1 || M > kMaxBwdTokens || ldd < w->N || ldd % 8 || ((uintptr_t)dy & 15)) return AQ_ERR_ARG;
@@ -796,6 +803,7 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
   a.units = a.whole + p.rest * p.S;
   a.add = add; a.dx = dx; a.ldadd = ldadd; a.lddx = lddx; a.f32 = dxdtype == AQ_F32;
   a.ws = ws;
+  a.stall = stall;
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = terms == 3 ? launch_form<3>(p, w, dy, ldd, a, st) : launch_form<1>(p, w, dy, ldd, a, st);
@@ -803,4 +811,16 @@ extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ld
     e = launch_pdl(linear_backward_sum_kernel, dim3((p.nt * (kTileK / 4) + 255) / 256, p.rest * p.cg), dim3(256), 0, st, a,
                    p.nt, p.cg);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+extern "C" int aq_linear_backward(const aq_packed* w, const uint16_t* dy, int ldd, int M, const void* add, int ldadd,
+                                  void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes, void* stream) {
+  return linear_backward(w, dy, ldd, M, add, ldadd, dx, lddx, dxdtype, ws, ws_bytes, Stall{}, stream);
+}
+
+extern "C" int aq_debug_linear_backward_stalled(const aq_packed* w, const uint16_t* dy, int ldd, int M, void* dx, int lddx,
+                                                int dxdtype, void* ws, size_t ws_bytes, unsigned long long wait_ns,
+                                                int stop_after, void* stream) {
+  if (!stall_ok(wait_ns, stop_after)) return AQ_ERR_ARG;
+  return linear_backward(w, dy, ldd, M, nullptr, 0, dx, lddx, dxdtype, ws, ws_bytes, Stall{wait_ns, stop_after}, stream);
 }

@@ -541,18 +541,19 @@ cudaError_t expand(const Table& t, const int32_t* ids, int M, const float* p, in
 
 // p = the products of x with the a (or b) side; out = y + p's sums times the other side.
 cudaError_t shrink_any(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M, float* p,
-                       void* header, cudaStream_t st) {
+                       void* header, const Stall& stall, cudaStream_t st) {
   int32_t* counts = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(p) + sum_bytes(ad, M, b_side));
-  return lora_tc_fits(ad, M) ? launch_lora_shrink_tc(ad, b_side, x, ldx, ids, M, p, counts, header, st)
+  return lora_tc_fits(ad, M) ? launch_lora_shrink_tc(ad, b_side, x, ldx, ids, M, p, counts, header, stall, st)
                              : shrink(b_side ? table_b(ad) : table_a(ad), x, ldx, ids, M, p, st);
 }
 cudaError_t expand_any(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, const void* y, int ldy,
-                       void* out, int ldo, int dtype, float* s, const TermsArgs* terms, void* header, cudaStream_t st) {
+                       void* out, int ldo, int dtype, float* s, const TermsArgs* terms, void* header,
+                       const Stall& stall, cudaStream_t st) {
   const int splits = products(ad, M, !b_side).splits;
   const int32_t* counts = reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(p) + sum_bytes(ad, M, !b_side));
   return lora_tc_fits(ad, M)
              ? launch_lora_expand_tc(ad, b_side, ids, M, p, splits, counts, y, ldy, out, ldo, dtype == AQ_F32, s, terms, header,
-                                                   st)
+                                     stall, st)
              : expand(b_side ? table_b(ad) : table_a(ad), ids, M, p, splits, y, ldy, out, ldo, dtype, s, st);
 }
 
@@ -612,15 +613,16 @@ extern "C" int aq_lora_apply(const aq_lora* ad, const uint16_t* x, int ldx, cons
     return launch_lora_decode(ad, x, ldx, ids, M, y, ldy, out, ldo, ydtype == AQ_F32, s, st) == cudaSuccess ? AQ_OK
                                                                                                             : AQ_ERR_CUDA;
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
-  cudaError_t e = shrink_any(ad, false, x, ldx, ids, M, p, ws, st);
-  if (e == cudaSuccess) e = expand_any(ad, true, ids, M, p, y, ldy, out, ldo, ydtype, s, nullptr, ws, st);
+  cudaError_t e = shrink_any(ad, false, x, ldx, ids, M, p, ws, Stall{}, st);
+  if (e == cudaSuccess) e = expand_any(ad, true, ids, M, p, y, ldy, out, ldo, ydtype, s, nullptr, ws, Stall{}, st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
 }
 
-extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M,
-                                const float* s, const void* x, int ldx, const float* sx, float* da, float* dbt,
-                                const void* add, int ldadd, void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes,
-                                void* stream) {
+// `stalls`: of the contraction, the expansion and the weight gradients.
+static int lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M, const float* s,
+                         const void* x, int ldx, const float* sx, float* da, float* dbt, const void* add, int ldadd,
+                         void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes, const Stall (&stalls)[3],
+                         void* stream) {
   int rc = check_lora(ad);
   if (rc != AQ_OK) return rc;
   if (M < 1 || M > kMaxTokens || !ids || !da || !dbt || !s) return AQ_ERR_ARG;
@@ -648,13 +650,37 @@ extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* p = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
   const Products t = products(ad, M, true);
-  cudaError_t e = shrink_any(ad, true, dy, ldd, ids, M, p, ws, st);
+  cudaError_t e = shrink_any(ad, true, dy, ldd, ids, M, p, ws, stalls[0], st);
   char* rest = reinterpret_cast<char*>(p) + p_bytes(ad, M, true);
   const bool beside = dx && lora_tc_fits(ad, M);
   const TermsArgs terms = lora_grad_terms(ad, ids, M, 0, p, t.splits, t.ld, sx, s, rest);
   if (e == cudaSuccess && dx)
-    e = expand_any(ad, false, ids, M, p, add, ldadd, dx, lddx, dxdtype, nullptr, beside ? &terms : nullptr, ws, st);
+    e = expand_any(ad, false, ids, M, p, add, ldadd, dx, lddx, dxdtype, nullptr, beside ? &terms : nullptr, ws, stalls[1],
+                   st);
   if (e == cudaSuccess)
-    e = launch_lora_grad(ad, ids, M, p, t.splits, t.ld, x, ldx, sx, da, s, dy, ldd, dbt, beside, ws, rest, st);
+    e = launch_lora_grad(ad, ids, M, p, t.splits, t.ld, x, ldx, sx, da, s, dy, ldd, dbt, beside, ws, rest, stalls[2],
+                         st);
   return e == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+extern "C" int aq_lora_backward(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M,
+                                const float* s, const void* x, int ldx, const float* sx, float* da, float* dbt,
+                                const void* add, int ldadd, void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes,
+                                void* stream) {
+  const Stall stalls[3];
+  return lora_backward(ad, dy, ldd, ids, M, s, x, ldx, sx, da, dbt, add, ldadd, dx, lddx, dxdtype, ws, ws_bytes, stalls,
+                       stream);
+}
+
+extern "C" int aq_debug_lora_backward_stalled(const aq_lora* ad, const uint16_t* dy, int ldd, const int32_t* ids, int M,
+                                              const float* s, const void* x, int ldx, const float* sx, float* da,
+                                              float* dbt, void* dx, int lddx, int dxdtype, void* ws, size_t ws_bytes,
+                                              int kernel, unsigned long long wait_ns, int stop_after, void* stream) {
+  if (check_lora(ad) != AQ_OK || !dx || kernel < 0 || kernel > 2 || (kernel < 2 && !lora_tc_fits(ad, M)) ||
+      !stall_ok(wait_ns, stop_after))
+    return AQ_ERR_ARG;
+  Stall stalls[3];
+  stalls[kernel] = Stall{wait_ns, stop_after};
+  return lora_backward(ad, dy, ldd, ids, M, s, x, ldx, sx, da, dbt, nullptr, 0, dx, lddx, dxdtype, ws, ws_bytes, stalls,
+                       stream);
 }

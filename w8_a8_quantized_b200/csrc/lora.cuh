@@ -34,10 +34,10 @@ bool lora_tc_fits(const aq_lora* ad, int M);
 int lora_tc_splits(int M, int D);
 size_t lora_tc_count_bytes(int M);
 cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M,
-                                  float* p, int32_t* counts, void* header, cudaStream_t st);
+                                  float* p, int32_t* counts, void* header, const Stall& stall, cudaStream_t st);
 cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
                                   const int32_t* counts, const void* y, int ldy, void* out, int ldo, bool f32, float* s,
-                                  const TermsArgs* terms, void* header, cudaStream_t st);
+                                  const TermsArgs* terms, void* header, const Stall& stall, cudaStream_t st);
 
 // Weight gradients (lora_grad.cu): t [tsplits][M][ldt] partial sums of the
 // output's gradient times B, s [M][max_rank] the forward products.  `header`: the
@@ -46,7 +46,7 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
 size_t lora_grad_ws_bytes(const aq_lora* ad, int M);
 cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
                              int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
-                             float* dbt, bool have_terms, void* header, void* ws, cudaStream_t st);
+                             float* dbt, bool have_terms, void* header, void* ws, const Stall& stall, cudaStream_t st);
 // What the terms of rank block rb are made of, and where they go in `ws`.
 TermsArgs lora_grad_terms(const aq_lora* ad, const int32_t* ids, int M, int rb, const float* t, int tsplits, int ldt,
                           const float* sx, const float* s, void* ws);

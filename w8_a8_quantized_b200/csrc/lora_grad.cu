@@ -122,6 +122,7 @@ struct GradArgs {
   int blocks, shares;  // CTAs along the columns, and those that share a range's adapters
   uint8_t* has;   // [L][splits]: whether the range has tokens of the adapter
   void* ws;
+  Stall stall;    // (the activations' producer stops)
 };
 
 // Eight codes (bytes) as bf16: 128 + the low seven bits, less 128 or 256 by the sign, exact.
@@ -245,6 +246,7 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
 
   Ring sr{0, 0}, br{0, 0}, rr{0, 0}, ar{0, 0};  // activations, terms, codes, accumulator
   bool ok = true, issued = false;
+  int loads = 0;
   float tot[Sh::kRanks];
 #pragma unroll
   for (int r = 0; r < Sh::kRanks; ++r) tot[r] = 0.f;
@@ -353,8 +355,13 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
       if (lane == 0) {
         for (int i = 0; ok && i < n; ++i) {
           const int m0 = (base + (int)(list[i] & 0x1FF)) * kTok;
-          if (!(CODES ? mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag)
-                      : mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag))) {
+          if (a.stall.stop_after >= 0 && loads++ == a.stall.stop_after) {
+            stalled(abort_flag, a.stall.wait_ns);
+            ok = false;
+            break;
+          }
+          if (!(CODES ? mbar_wait(&raw_empty[rr.i], rr.ph ^ 1u, abort_flag, a.stall.wait_ns)
+                      : mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
             fail(21);
             ok = false;
             break;
@@ -377,14 +384,14 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
       const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
       for (int i = 0; ok && i < n; ++i) {
         const uint32_t step = __shfl_sync(0xffffffffu, list[i], 0);
-        if ((step & kUnitStart) && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag))) {
+        if ((step & kUnitStart) && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
           fail(22);
           ok = false;
           break;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag) &&
-                                         mbar_wait(&a_full[sr.i], sr.ph, abort_flag) &&
-                                         (CODES || mbar_wait(&a_tma[sr.i], sr.ph, abort_flag)))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&b_full[br.i], br.ph, abort_flag, a.stall.wait_ns) &&
+                                         mbar_wait(&a_full[sr.i], sr.ph, abort_flag, a.stall.wait_ns) &&
+                                         (CODES || mbar_wait(&a_tma[sr.i], sr.ph, abort_flag, a.stall.wait_ns)))) {
           fail(23);
           ok = false;
           break;
@@ -409,7 +416,7 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
       // ------------------------------------------------------------ terms
       if (lane == 0) {
         for (int i = 0; ok && i < n; ++i) {
-          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag)) {
+          if (!mbar_wait(&b_done[br.i], br.ph ^ 1u, abort_flag, a.stall.wait_ns)) {
             fail(24);
             ok = false;
             break;
@@ -432,10 +439,10 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
       for (int i = 0; ok && i < n; ++i) {
         const bool mixed = list[i] & kMixed;
         const int m0 = (base + (int)(list[i] & 0x1FF)) * kTok;
-        bool got = mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag);
-        if (CODES) got = got && mbar_wait(&raw_full[rr.i], rr.ph, abort_flag);
-        if (mixed) got = got && mbar_wait(&b_full[br.i], br.ph, abort_flag);
-        if (mixed && !CODES) got = got && mbar_wait(&a_tma[sr.i], sr.ph, abort_flag);
+        bool got = mbar_wait(&a_done[sr.i], sr.ph ^ 1u, abort_flag, a.stall.wait_ns);
+        if (CODES) got = got && mbar_wait(&raw_full[rr.i], rr.ph, abort_flag, a.stall.wait_ns);
+        if (mixed) got = got && mbar_wait(&b_full[br.i], br.ph, abort_flag, a.stall.wait_ns);
+        if (mixed && !CODES) got = got && mbar_wait(&a_tma[sr.i], sr.ph, abort_flag, a.stall.wait_ns);
         if (!__all_sync(0xffffffffu, got)) {
           fail(25);
           ok = false;
@@ -481,7 +488,7 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
       for (int i = 0; ok && i < n; ++i) {
         const uint32_t step = list[i];
         if (!(step & kUnitEnd)) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag, a.stall.wait_ns))) {
           fail(26);
           ok = false;
           break;
@@ -538,7 +545,7 @@ __device__ __forceinline__ void grad_cta(const GradMaps& maps, const GradArgs& a
   if (warp == 1 && issued) {
     if (elect_one()) mma_commit(drain);
     __syncwarp();
-    mbar_wait(drain, 0, never_flag);
+    mbar_wait(drain, 0, never_flag, a.stall.wait_ns);
   }
   if ((warp == 0 || warp == 2) && lane == 0 && (!ok || *abort_flag)) {
     grace();
@@ -698,7 +705,7 @@ TermsArgs lora_grad_terms(const aq_lora* ad, const int32_t* ids, int M, int rb, 
 
 cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const float* t, int tsplits, int ldt, const void* x,
                              int ldx, const float* sx, float* da, const float* s, const uint16_t* dy, int ldd,
-                             float* dbt, bool have_terms, void* header, void* ws, cudaStream_t st) {
+                             float* dbt, bool have_terms, void* header, void* ws, const Stall& stall, cudaStream_t st) {
   char* at = static_cast<char*>(ws);
   int32_t* info = reinterpret_cast<int32_t*>(at);
   at += align256((size_t)ceil_div(M, kTok) * 4);
@@ -731,7 +738,7 @@ cudaError_t launch_lora_grad(const aq_lora* ad, const int32_t* ids, int M, const
                          : map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, D, M, (uint64_t)ldx * 2, 64, kTok, true));
       if (!ok) return cudaErrorInvalidValue;
       j.args[side] = {ids, ad->off, info, M, D, ad->L, ad->R, ad->max_rank, 64 * rb,
-                      splits > 1 ? reinterpret_cast<float*>(part) : out, splits, ceil_div(D, kD), shares, has, header};
+                      splits > 1 ? reinterpret_cast<float*>(part) : out, splits, ceil_div(D, kD), shares, has, header, stall};
       part += part_bytes(ad, M, D);
     }
     e = sx ? launch_ranks<true>(rc, j, st) : launch_ranks<false>(rc, j, st);

@@ -110,6 +110,7 @@ struct ShrinkTcArgs {
   float* p;
   int32_t* counts;  // [tiles]: adapters of a tile, for the expansion
   void* ws;
+  Stall stall;      // (the activations' producer stops)
 };
 
 template <int RC>
@@ -191,9 +192,15 @@ __global__ void __launch_bounds__(kSThreads, 2)
   if (warp == 0) {
     if (lane == 0) {
       Ring xr{0, 0};
+      int loads = 0;
       for (int p0 = 0; ok && p0 < na; p0 += Sh::kCap)
         for (int s = s0; s < s1; ++s) {
-          if (!mbar_wait(&x_free[xr.i], xr.ph ^ 1u, abort_flag)) {
+          if (a.stall.stop_after >= 0 && loads++ == a.stall.stop_after) {
+            stalled(abort_flag, a.stall.wait_ns);
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(&x_free[xr.i], xr.ph ^ 1u, abort_flag, a.stall.wait_ns)) {
             fail(31);
             ok = false;
             break;
@@ -211,7 +218,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
         const int p1 = min(p0 + Sh::kCap, na);
         for (int s = s0; ok && s < s1; ++s)
           for (int i = p0; i < p1; ++i) {
-            if (!mbar_wait(&w_free[wr.i], wr.ph ^ 1u, abort_flag)) {
+            if (!mbar_wait(&w_free[wr.i], wr.ph ^ 1u, abort_flag, a.stall.wait_ns)) {
               fail(32);
               ok = false;
               break;
@@ -233,18 +240,18 @@ __global__ void __launch_bounds__(kSThreads, 2)
       const int p1 = min(p0 + Sh::kCap, na);
       for (int s = s0; ok && s < s1; ++s) {
         const int in_unit = (s - s0) % kSUnit;
-        if (in_unit == 0 && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag))) {
+        if (in_unit == 0 && !__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
           fail(33);
           ok = false;
           break;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&x_full[xr.i], xr.ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&x_full[xr.i], xr.ph, abort_flag, a.stall.wait_ns))) {
           fail(34);
           ok = false;
           break;
         }
         for (int i = p0; i < p1; ++i) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&w_full[wr.i], wr.ph, abort_flag))) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&w_full[wr.i], wr.ph, abort_flag, a.stall.wait_ns))) {
             fail(35);
             ok = false;
             break;
@@ -275,7 +282,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
     if (issued) {
       if (elect_one()) mma_commit(drain);
       __syncwarp();
-      mbar_wait(drain, 0, never_flag);
+      mbar_wait(drain, 0, never_flag, a.stall.wait_ns);
     }
   } else if (warp >= 4) {
     const int w = warp & 3, row = 32 * w + lane, mine = q.slot[row];
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(kSThreads, 2)
     for (int p0 = 0; ok && p0 < na; p0 += Sh::kCap) {
       const int p1 = min(p0 + Sh::kCap, na);
       for (int s = s0; s < s1; s += kSUnit) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag, a.stall.wait_ns))) {
           fail(36);
           ok = false;
           break;
@@ -356,6 +363,7 @@ struct ExpandTcArgs {
   const float* p;  // [splits][M][rp]
   float* s;        // [M][max_rank] or null
   void* ws;
+  Stall stall;     // (y's producer stops)
 };
 
 // kEW: slots of table rows, as many as fit (3 for 64 ranks, 5 up to 32): with k slots
@@ -555,7 +563,12 @@ __global__ void __launch_bounds__(kEThreads, 1)
     if (lane == 0) {
       Ring yr{0, 0};
       for (int b = b0; b < b1; ++b) {
-        if (!mbar_wait(&y_free[yr.i], yr.ph ^ 1u, abort_flag)) {
+        if (a.stall.stop_after >= 0 && b - b0 == a.stall.stop_after) {
+          stalled(abort_flag, a.stall.wait_ns);
+          ok = false;
+          break;
+        }
+        if (!mbar_wait(&y_free[yr.i], yr.ph ^ 1u, abort_flag, a.stall.wait_ns)) {
           fail(41);
           ok = false;
           break;
@@ -582,8 +595,8 @@ __global__ void __launch_bounds__(kEThreads, 1)
     bool issued = false;
     for (int b = b0; ok && b < b1; ++b)
       for (int i = 0; i < na; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag) &&
-                                         mbar_wait(&w_full[wr.i], wr.ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[ar.i], ar.ph ^ 1u, abort_flag, a.stall.wait_ns) &&
+                                         mbar_wait(&w_full[wr.i], wr.ph, abort_flag, a.stall.wait_ns))) {
           fail(42);
           ok = false;
           break;
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     if (issued) {
       if (elect_one()) mma_commit(drain);
       __syncwarp();
-      mbar_wait(drain, 0, never_flag);
+      mbar_wait(drain, 0, never_flag, a.stall.wait_ns);
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ table rows
@@ -627,7 +640,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
           asm volatile("cp.async.wait_group %0;" ::"n"(kEW - 2) : "memory");
           publish();
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&w_free[wr.i], wr.ph ^ 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&w_free[wr.i], wr.ph ^ 1u, abort_flag, a.stall.wait_ns))) {
           fail(43);
           ok = false;
           break;
@@ -658,7 +671,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
     for (int b = b0; ok && b < b1; ++b) {
       uint8_t* ybase = ybuf(yr.i) + half * (kYBytes / 2);
       uint4* yrow = reinterpret_cast<uint4*>(ybase + row * 128);  // chunk c of the row at c ^ (row & 7)
-      if (!__all_sync(0xffffffffu, mbar_wait(&y_full[yr.i], yr.ph, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&y_full[yr.i], yr.ph, abort_flag, a.stall.wait_ns))) {
         fail(44);
         ok = false;
         break;
@@ -667,7 +680,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
 #pragma unroll
       for (int c = 0; c < 8; ++c) y[c] = a.has_y ? yrow[c ^ (row & 7)] : make_uint4(0, 0, 0, 0);
       for (int i = 0; i < na; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ar.i], ar.ph, abort_flag, a.stall.wait_ns))) {
           fail(45);
           ok = false;
           break;
@@ -717,7 +730,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
       // every warp waits: one that ran ahead would arrive for the next block in place of
       // one that has not finished this block
       if (lane == 0) mbar_arrive(&epi[half]);
-      if (!__all_sync(0xffffffffu, mbar_wait(&epi[half], phase, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&epi[half], phase, abort_flag, a.stall.wait_ns))) {
         fail(46);
         break;
       }
@@ -800,14 +813,14 @@ int lora_tc_splits(int M, int D) {
 size_t lora_tc_count_bytes(int M) { return (size_t)ceil_div(M, kTok) * 4; }
 
 cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t* x, int ldx, const int32_t* ids, int M,
-                                  float* p, int32_t* counts, void* header, cudaStream_t st) {
+                                  float* p, int32_t* counts, void* header, const Stall& stall, cudaStream_t st) {
   const TcTable t = table(ad, b_side);
   ShrinkMaps maps;
   memset(&maps, 0, sizeof(maps));
   if (!map_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, t.D, M, (uint64_t)ldx * 2, 64, kTok, true) ||
       !map_2d(&maps.w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, t.w, t.D, t.R, (uint64_t)t.D * 2, 64, t.rp, true))
     return cudaErrorInvalidValue;
-  const ShrinkTcArgs a{t, ids, M, lora_tc_splits(M, t.D), p, counts, header};
+  const ShrinkTcArgs a{t, ids, M, lora_tc_splits(M, t.D), p, counts, header, stall};
   switch (t.rp) {
     case 16: return launch_shrink<16>(maps, a, st);
     case 32: return launch_shrink<32>(maps, a, st);
@@ -819,7 +832,7 @@ cudaError_t launch_lora_shrink_tc(const aq_lora* ad, bool b_side, const uint16_t
 
 cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t* ids, int M, const float* p, int splits,
                                   const int32_t* counts, const void* y, int ldy, void* out, int ldo, bool f32, float* s,
-                                  const TermsArgs* terms, void* header, cudaStream_t st) {
+                                  const TermsArgs* terms, void* header, const Stall& stall, cudaStream_t st) {
   const TcTable t = table(ad, b_side);
   ExpandMaps maps;
   memset(&maps, 0, sizeof(maps));
@@ -828,7 +841,7 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
   if (!map_2d(&maps.out, type, out, t.D, M, (uint64_t)ldo * elt, 128 / elt, kTok, true) ||
       (y && !map_2d(&maps.y, type, y, t.D, M, (uint64_t)ldy * elt, 128 / elt, kTok, true)))
     return cudaErrorInvalidValue;
-  const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, terms ? *terms : TermsArgs{}, p, s, header};
+  const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, terms ? *terms : TermsArgs{}, p, s, header, stall};
   if (t.rp <= 32) return f32 ? launch_expand<true, 5>(maps, a, st) : launch_expand<false, 5>(maps, a, st);
   return f32 ? launch_expand<true, 3>(maps, a, st) : launch_expand<false, 3>(maps, a, st);
 }

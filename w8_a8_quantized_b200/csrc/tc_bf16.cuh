@@ -66,6 +66,12 @@ struct Ring {
   }
 };
 
+// A producer that has stopped (see Stall) stays until the other roles have given up.
+__device__ __forceinline__ void stalled(volatile int* abort, unsigned long long wait_ns) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!*abort && globaltimer_ns() - t0 < 2 * wait_ns) __nanosleep(1000);
+}
+
 // Copies in flight when a CTA gives up get this long to land.
 __device__ __forceinline__ void grace() {
   const unsigned long long t0 = globaltimer_ns();
