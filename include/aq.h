@@ -445,8 +445,8 @@ typedef struct aq_lora {
  *        aq_lora_backward takes
  *  out and s must not overlap an input (but y as said) or each other: AQ_ERR_ARG.  Rows of one
  *  pitch that lie side by side in one buffer do not overlap.
- *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned, zero-filled once
- *        when allocated; calls that share it must not run concurrently (one of 16
+ *  ws    >= aq_lora_workspace_bytes(ad, M, 0) bytes, 16-byte aligned, its first 256 bytes
+ *        zeroed once when allocated; calls that share it must not run concurrently (one of 16
  *        bytes is not touched: decode batches need none)
  * Rows are 16-byte aligned: x, y, out on 16 bytes, ld % 8 == 0 (bf16) or
  * ld % 4 == 0 (fp32).  1 <= M <= 4194240.  Asynchronous.
@@ -534,7 +534,7 @@ int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const fl
  *  dx    [M][lddx], fp32 or bf16 (dxdtype, see above), 16-byte aligned rows; may be add itself (same pitch),
  *        and must not overlap dy, or add otherwise: AQ_ERR_ARG
  *  ws    >= aq_linear_backward_workspace_bytes(M, w) bytes, 16-byte aligned,
- *        zero-filled once as for the linear calls; errors by aq_workspace_status
+ *        the first 256 of them zeroed once when allocated; errors by aq_workspace_status
  * 1 <= M <= 2097152.  Asynchronous.
  * Errors: AQ_ERR_ARG, AQ_ERR_SHAPE, AQ_ERR_WORKSPACE, AQ_ERR_CUDA.
  */
@@ -605,6 +605,10 @@ int aq_measure_i8_peak(int iters, double* tops, void* stream);
  * Synchronizes `stream`, then reads and clears the error word a kernel left in
  * the workspace `ws`.  Returns AQ_OK, AQ_ERR_TIMEOUT (a bounded wait inside a
  * kernel gave up; *info, nullable, receives where) or AQ_ERR_CUDA.
+ * The error word is in the first 256 bytes of the workspace, zero at first.  Bytes 16 .. 23 of
+ * them may hold the device address of another 256 bytes, zero at first, that receive the error
+ * as well and that this call takes in place of a workspace: for workspaces that are gone when
+ * the error is asked for, such as those of a captured graph's replays.
  */
 int aq_workspace_status(void* ws, void* stream, int* info);
 

@@ -201,3 +201,95 @@ def test_stalled_weight_gradients_of_few_tokens():
     t0 = time.monotonic()
     aq.aq_debug_lora_backward_stalled(c.ad, c.dy, c.ids, s, c.x, None, 2, ws, wait_ns=WAIT_NS, stop_after=0)
     gave_up(ws, range(21, 27), t0)
+
+
+# ------------------------------------------------------------------ workspaces
+
+def test_workspaces_need_a_clear_header_only():
+    """Whatever the rest of a workspace holds, the bits are the same."""
+    c = LoraCase(333, 640, 1536, [5, 40, 64], mixed_ids(333, 3, 2), seed=2)
+    few = LoraCase(40, 640, 1536, [5, 40, 200], mixed_ids(40, 3, 2), seed=2)
+    w, _ = packed(640, 1536, 128, 0.5, 4)
+
+    def filled(need, value):
+        ws = torch.full((need,), value, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        return ws
+
+    for case in (c, few):
+        s = torch.empty(case.M, max(case.ranks), device="cuda")
+        got = []
+        for value in (0, 255, 127):
+            out = aq.aq_lora_apply(case.ad, case.x, case.ids, s=s,
+                                   ws=filled(aq.aq_lora_workspace_bytes(case.ad, case.M, False), value))
+            got.append((out,) + aq.aq_lora_backward(case.ad, case.dy, case.ids, s, case.x,
+                                                    ws=filled(aq.aq_lora_workspace_bytes(case.ad, case.M, True), value)))
+            for dtype in (torch.bfloat16, torch.float32):
+                ws = filled(aq.aq_linear_backward_workspace_bytes(case.M, w), value)
+                got[-1] += (aq.aq_linear_backward(w, case.dy, ws=ws, out_dtype=dtype),)
+        for other in got[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(got[0], other))
+
+
+def test_a_replay_that_gives_up_is_reported():
+    w, _ = packed(512, 2560, 128, 0.5, 7)
+    dy = normal(rng(1), 300, 512, scale=0.01)
+    c = LoraCase(333, 512, 640, [8, 24], mixed_ids(333, 2, 3), seed=3)
+    s = torch.empty(333, 24, device="cuda")
+    aq.aq_lora_apply(c.ad, c.x, c.ids, s=s)
+    want = aq.aq_linear_backward(w, dy)
+    aq.check_all_workspaces()
+    for stall in (lambda: aq.aq_debug_linear_backward_stalled(w, dy, wait_ns=WAIT_NS),
+                  lambda: aq.aq_debug_lora_backward_stalled(c.ad, c.dy, c.ids, s, c.x, None, 0, wait_ns=WAIT_NS)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = aq.aq_linear_backward(w, dy)
+            stall()
+            again = aq.aq_linear_backward(w, dy)
+        torch.cuda.synchronize()
+        aq.check_all_workspaces()  # captured, not run
+        for _ in range(2):  # each replay anew
+            graph.replay()
+            with pytest.raises(aq.AqError):
+                aq.check_all_workspaces()
+            aq.check_all_workspaces()  # and once
+        assert torch.equal(got, want) and torch.equal(again, want)
+        stall()  # not captured: the same
+        with pytest.raises(aq.AqError):
+            aq.check_all_workspaces()
+
+
+def test_errors_outlive_a_grown_workspace_and_its_thread():
+    import threading
+    w, _ = packed(512, 2560, 128, 0.5, 7)
+    small, large = normal(rng(1), 40, 512), normal(rng(2), 3000, 512)
+    want = aq.aq_linear_backward(w, large, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    free, got = [], []
+
+    def run():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            aq.aq_debug_linear_backward_stalled(w, small, wait_ns=WAIT_NS, stop_after=0)
+            got.append(aq.aq_linear_backward(w, large, out_dtype=torch.float32))  # a larger workspace takes its place
+            free.append(torch.cuda.memory_allocated())
+            torch.cuda.current_stream().synchronize()
+
+    thread = threading.Thread(target=run)
+    thread.start()
+    thread.join()
+    assert torch.equal(got[0], want)
+    assert torch.cuda.memory_allocated() < free[0]  # the thread's workspaces went with it
+    with pytest.raises(aq.AqError):
+        aq.check_all_workspaces()
+    aq.check_all_workspaces()
+
+
+def test_a_captured_workspace_clears_its_header_only():
+    w, _ = packed(256, 256, 128, 0.5, 1)  # (a header to report to)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ws = aq._new_ws(1 << 20, w.device)
+    ws.fill_(9)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((ws[256:] == 9).all()) and not ws[:16].any() and not ws[24:256].any()

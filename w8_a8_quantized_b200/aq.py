@@ -195,6 +195,8 @@ class PackedWeights:
         self.device = torch.device(device)
         self.buffers = {n: torch.empty(max(s, 16), dtype=torch.uint8, device=self.device) for n, s in sizes.items()}
         self.sizes = sizes
+        if self.device.type == "cuda":
+            _report(self.buffers["w4"].device.index)
         self.struct = AqPackedStruct(N=N, K=K, bN=bN, bK=bK, R=N // bN, C=K // bK, T4=T4, T8=0)
         for n in BUF_NAMES:
             setattr(self.struct, n, self.buffers[n].data_ptr())
@@ -423,6 +425,28 @@ def aq_workspace_bytes(phase: int, M: int, w: PackedWeights) -> int:
 
 
 _ws_cache = {}
+
+# The adapter and gradient calls' own workspaces report their errors to a header of their device as well,
+# which outlives them: {device index: (that header, the header that such a workspace starts with)}.
+_WS_HEADER = 256
+_reports, _reports_lock = {}, threading.Lock()
+
+
+def _report(index: int):
+    r = _reports.get(index)
+    if r is None:
+        with _reports_lock, torch.cuda.device(index), torch.inference_mode(False):
+            r = _reports.get(index)
+            if r is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("make the Adapters or PackedWeights before the capture begins")
+                head = torch.zeros(_WS_HEADER, dtype=torch.uint8, device="cuda")
+                first = np.zeros(_WS_HEADER, np.uint8)
+                first[16:24] = np.frombuffer(head.data_ptr().to_bytes(8, "little"), np.uint8)
+                r = head, torch.from_numpy(first).to(head.device)
+                torch.cuda.current_stream().synchronize()  # both are there for every stream
+                _reports[index] = r
+    return r
 
 
 def workspace(phase: int, M: int, w: PackedWeights) -> torch.Tensor:
@@ -709,6 +733,7 @@ class Adapters:
         if max(self.ranks) > AQ_LORA_MAX_RANK:
             raise ValueError(f"ranks above {AQ_LORA_MAX_RANK} are not supported")
         self.a, self.bt, self.device = a, bt, a.device
+        _report(a.device.index)
         off = np.concatenate([[0], np.cumsum(self.ranks)]).astype(np.int32)
         self.off = torch.from_numpy(off).to(self.device)
         self.scale = torch.tensor(self.scales, dtype=torch.float32, device=self.device)
@@ -735,17 +760,31 @@ def aq_lora_workspace_bytes(ad: Adapters, M: int, backward: bool) -> int:
     return int(lib().aq_lora_workspace_bytes(ctypes.byref(ad.struct), M, int(bool(backward))))
 
 
+_thread = threading.local()  # .ws: a thread's workspaces, gone with it
+
+
+def _new_ws(need: int, device) -> torch.Tensor:
+    """A workspace whose header is ready; the rest of it needs no clearing."""
+    first = _report(device.index)[1]
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:_WS_HEADER].copy_(first)
+    return ws
+
+
 def _stream_ws(tag: str, need: int, device) -> torch.Tensor:
-    """A zero-filled workspace of the current stream and thread, cached and grown on
-    demand (threads may take turns on a stream between one call's launches: autograd
-    runs backward passes in a thread of its own); a call that is captured into a graph
-    gets its own, so that graphs share none."""
+    """A workspace of the current stream and thread, kept and grown on demand (threads
+    may take turns on a stream between one call's launches: autograd runs backward
+    passes in a thread of its own); a call that is captured into a graph gets its own,
+    so that graphs share none."""
     if _capturing():
-        return torch.zeros(need, dtype=torch.uint8, device=device)
-    key = device.index, tag, _raw_stream(device.index), threading.get_ident()
-    ws = _ws_cache.get(key)
+        return _new_ws(need, device)
+    kept = getattr(_thread, "ws", None)
+    if kept is None:
+        kept = _thread.ws = {}
+    key = device.index, tag, _raw_stream(device.index)
+    ws = kept.get(key)
     if ws is None or ws.numel() < need:
-        ws = _ws_cache[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = kept[key] = _new_ws(need, device)
     return ws
 
 
@@ -964,12 +1003,13 @@ def aq_debug_linear_stalled(w: PackedWeights, xq, sx, phase: int, ws: torch.Tens
     return out
 
 
-def aq_debug_lora_backward_stalled(ad: Adapters, dy, ids, s, x, sx, kernel: int, ws: torch.Tensor,
+def aq_debug_lora_backward_stalled(ad: Adapters, dy, ids, s, x, sx, kernel: int, ws: torch.Tensor = None,
                                    wait_ns: int = 20_000_000, stop_after: int = 1):
     """aq_lora_backward with a stage of one of its kernels (0 contraction, 1 expansion, 2
     weight gradients) that never fills: returns the (unspecified) gradients; the error
     lands in `ws`.  Contiguous tensors, as aq_lora_backward checks them."""
     M = dy.shape[0]
+    ws = _lora_ws(ad, M, 1, ws)
     da, dbt = _new(ad.R, ad.K, _F32, ad.device), _new(ad.R, ad.N, _F32, ad.device)
     dx = _new(M, ad.K, _BF16, ad.device)
     for t, name, dtype, shape in ((dy, "dy", _BF16, (M, ad.N)), (ids, "ids", torch.int32, (M,)),
@@ -984,12 +1024,14 @@ def aq_debug_lora_backward_stalled(ad: Adapters, dy, ids, s, x, sx, kernel: int,
     return da, dbt, dx
 
 
-def aq_debug_linear_backward_stalled(w: PackedWeights, dy, ws: torch.Tensor, out_dtype=torch.bfloat16,
+def aq_debug_linear_backward_stalled(w: PackedWeights, dy, ws: torch.Tensor = None, out_dtype=torch.bfloat16,
                                      wait_ns: int = 20_000_000, stop_after: int = 1) -> torch.Tensor:
     """aq_linear_backward with a weight producer that stops: returns the (unspecified)
     result; the error lands in `ws`."""
     M = dy.shape[0]
     _exact(dy, "dy", _BF16, w.device, (M, w.N))
+    if ws is None:
+        ws = _own_ws("backward", aq_linear_backward_workspace_bytes(M, w), w.device)
     out = _new(M, w.K, out_dtype, w.device)
     _call(lib().aq_debug_linear_backward_stalled, "aq_debug_linear_backward_stalled", w.device, ctypes.byref(w.struct),
           dy.data_ptr(), w.N, M, out.data_ptr(), w.K, AQ_F32 if out_dtype == _F32 else AQ_BF16, ws.data_ptr(),
@@ -1017,8 +1059,11 @@ def aq_measure_i8_peak(iters: int = 20000, device=None) -> float:
 
 
 def check_all_workspaces():
-    """Raise if any cached workspace recorded a kernel error."""
-    for ws in list(_ws_cache.values()):
+    """Raise if a call on a workspace that was left out recorded a kernel error: also
+    one of a thread that has ended, or of a replayed graph.  Waits for the devices."""
+    for index in list(_reports):
+        torch.cuda.synchronize(index)
+    for ws in list(_ws_cache.values()) + [head for head, _ in list(_reports.values())]:
         rc, info = aq_workspace_status(ws)
         if rc != AQ_OK:
             raise AqError(rc, f"kernel wait gave up (info {info})")

@@ -457,14 +457,17 @@ extern "C" int aq_linear_group(int phase, const aq_packed* const* w, int G, cons
 extern "C" int aq_workspace_status(void* ws, void* stream, int* info) {
   if (!ws) return AQ_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  WsHeader h{0, 0, 0};
+  WsHeader h{};
   if (cudaStreamSynchronize(st) != cudaSuccess) return AQ_ERR_CUDA;
   if (cudaMemcpy(&h, ws, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return AQ_ERR_CUDA;
   if (h.err_code != 0) {
     // a call that gave up may have left split-K arrival counters nonzero: the
     // kernel recorded how many bytes after the header to zero with the error
-    const size_t clear = kWsHeader + (size_t)std::max(h.err_clear, 0);
-    if (cudaMemset(ws, 0, clear) != cudaSuccess) return AQ_ERR_CUDA;
+    // (the address that the header reports to stays)
+    char* base = static_cast<char*>(ws);
+    if (cudaMemset(base, 0, offsetof(WsHeader, unused)) != cudaSuccess ||
+        (h.err_clear > 0 && cudaMemset(base + kWsHeader, 0, (size_t)h.err_clear) != cudaSuccess))
+      return AQ_ERR_CUDA;
   }
   if (info) *info = h.err_info;
   return h.err_code == 0 ? AQ_OK : AQ_ERR_TIMEOUT;

@@ -33,6 +33,8 @@ struct WsHeader {
   int err_code;   // 0 or AQ_ERR_TIMEOUT
   int err_info;   // which wait gave up (kernel-specific code)
   int err_clear;  // bytes after the header (split-K counters) to zero again after an error
+  int unused;
+  unsigned long long report;  // 0, or the address of a header that receives the error too (see aq_workspace_status)
 };
 
 // Bounded waits: any spin on an mbarrier gives up after this long, records
@@ -349,6 +351,8 @@ __device__ __forceinline__ void record_error(void* ws, int code, int info, int c
     atomicExch(&h->err_info, info);
     atomicExch(&h->err_clear, clear_bytes);
   }
+  WsHeader* r = reinterpret_cast<WsHeader*>(h->report);
+  if (r && atomicCAS(&r->err_code, 0, code) == 0) atomicExch(&r->err_info, info);
 }
 
 // Programmatic dependent launch controls (no-ops without the launch attribute).
