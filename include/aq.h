@@ -433,7 +433,9 @@ typedef struct aq_lora {
  * in fp32, out rounded once.  A token whose id is outside [0, L) (-1 by
  * convention) or whose adapter has rank 0 gets out = y.  Tokens may carry ids
  * in any order; tokens of one request next to one another are the fast case
- * (each run of 64 tokens costs one pass per adapter that occurs in it).  A
+ * (a tile of tokens costs a pass per adapter that occurs in it: tiles of 64 tokens with ranks above
+ * 64; of 128 otherwise, where x is read again for every 128 / r of a tile's adapters, r the largest
+ * rank rounded up to 16).  A
  * token's result depends on its own activations and adapter alone, also where
  * others hold infinities or NaN.
  *  x     bf16 [M][ldx], ldx % 8 == 0, ldx >= K
@@ -490,8 +492,11 @@ size_t aq_lora_workspace_bytes(const aq_lora* ad, int M, int backward);
  * down projection's input codes: h = gate / (1 + exp(-gate)) * up, and for every
  * token its codes and scale,
  *   s = max(max_f |h[m][f]| * R, 1e-12), R = fl64(1 / 127);  hq = clamp(rint(h / s), -127, 127);  sh[m] = (float)s
- * with h, s and the quotient in fp64 (h is not rounded to bf16 in between).  It is
- * aq_quant_act's rule up to the last fp64 bit of s.
+ * with h, s and the quotient in fp64 (h is not rounded to bf16 in between).  s is a
+ * product with R, as elementary operations on a GPU form it (a division by a constant is
+ * a product with its reciprocal there); aq_quant_act's s is the quotient max / 127, which differs in
+ * the last fp64 bit for some maxima.  That shows in a value of exactly half the largest alone: for 9
+ * of a bf16 maximum's 128 mantissas its code is 64 here and 63 by the quotient, each half a step off.
  * gq, gs, uq, us (all or none): 8-bit checkpoints of gate and up for the backward
  * pass, the same rule with one scale per 128 features of a row (the last group
  * may be shorter).
@@ -526,7 +531,8 @@ int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const fl
  * dx it is rounded once to bf16 (2^-8 relative at most, independent from weight to weight,
  * so an error like that of dx's own rounding: 2.35e-3 of the norm in all, 1.66e-3 with exact
  * weights) at a third of the products.  dxdtype + AQ_WEIGHTS_BF16 or + AQ_WEIGHTS_EXACT
- * takes the one or the other for either type.
+ * takes the one or the other for either type.  A row of dy that holds an infinity or NaN
+ * makes that row of dx infinite or NaN, and no other.
  *  w     as for aq_linear_prefill
  *  dy    bf16 [M][ldd], 16-byte aligned, ldd % 8 == 0, ldd >= N
  *  add   [M][ldadd] of dxdtype or NULL (zero): e.g. the gradient through another

@@ -142,6 +142,18 @@ def test_linear_backward_sums_every_row(M, N, K, bN, dtype, weights):
     assert torch.equal(aq.aq_linear_backward(w, dy, add=add, weights=weights), (ref + add.double()).to(dtype))
 
 
+@pytest.mark.parametrize("M", [150, 1100])
+def test_exact_weights_keep_infinite_rows_apart(M):
+    w, _ = packed(1024, 2560, 128, 0.5, 3)
+    dy = normal(rng(3), M, 1024)
+    want = aq.aq_linear_backward(w, dy, out_dtype=torch.float32)
+    dy[7], dy[M - 1, 3] = float("inf"), float("nan")
+    got = aq.aq_linear_backward(w, dy, out_dtype=torch.float32)
+    ok = [m for m in range(M) if m not in (7, M - 1)]
+    assert torch.equal(got[ok], want[ok])
+    assert not torch.isfinite(got[[7, M - 1]]).any()
+
+
 # ------------------------------------------------------------------ waits that give up
 
 WAIT_NS = 20_000_000

@@ -629,6 +629,9 @@ class Group:
 
 
 # ------------------------------------------------------------------ adapters, gated activation, gradients
+#
+# These calls stand outside autograd, as the linear calls do: results carry no graph, whatever the
+# inputs require; a training step calls the backward entries itself.
 
 AQ_LORA_MAX_RANK = 256
 

@@ -10,9 +10,9 @@
 //   p = 1 / (1 + exp(-g~));  dg = dh u~ p (1 + g~ (1 - p));  du = dh g~ p.
 //
 // Both are bound by HBM on paper (4 bytes read and 1, with checkpoints 3, written
-// per element forward; 4 and 4 backward).  Backward gets there: 4096 x 14336 in 79 us, 81% of
-// the copy rate.  Forward is bound by its instructions, 33 an element with three codes (46
-// when the checkpoints' codes were tested and redone): 81 us, 75% of the copy rate.
+// per element forward; 4 and 4 backward).  Backward gets there: 4096 x 14336 in 79 us in a graph, 91%
+// of the copy rate by the call's bytes.  Forward is bound by its instructions, 33 an element with three codes (46
+// when the checkpoints' codes were tested and redone): 83 us in a graph, 76%.
 // Hence float2 arithmetic, two multifunction operations per sigmoid, no clamps (a
 // quotient cannot pass 127 by more than its rounding), and one comparison per
 // eight codes; what that cannot decide is redone one element at a time.
@@ -380,6 +380,18 @@ cudaError_t launch_row(const uint16_t* gate, int ldg, const uint16_t* up, int ld
 template <bool KEEP>
 cudaError_t launch_fwd(const uint16_t* gate, int ldg, const uint16_t* up, int ldu, int M, int F, int8_t* hq, float* sh,
                        int8_t* gq, float* gs, int8_t* uq, float* us, cudaStream_t st) {
+  // Vectors a thread, threads of a CTA, CTAs per SM.  With few tokens as few vectors as the row allows, since a thread's
+  // work is a chain; with many as many as leave registers for two CTAs per SM, as far as that goes (14336 features).
+  // us in graphs, without and with checkpoints, here and with another variant:
+  //      1 token    2048:   1.9   2.2  (two vectors    2.0   2.4)
+  //                14336:   3.0   3.7  (four vectors   3.4   4.4)
+  //                17408:   5.0   6.6  (1024 threads   6.7   8.9)
+  //   4096 tokens   2048:  13.0  17.3  (two vectors    9.5  13.0: the one bound that many tokens would move)
+  //                 4096:  18.3  27.7  (four vectors  21.6  30.7)
+  //                 9728:    51    69  (two, 75 and 93; eight, 71 and 97)
+  //                14336:    60    83  (two, 89 and 112; eight, 92 and 132)
+  //                17408:   145   211  (1024 threads, 133 and 202): one CTA per SM either way, at 116 to 126 registers
+  // Above 32768 features the last variant spills 388 bytes (1 token of 65536: 12.9 and 16.9).
   const int nvec = F / 8;
 #define AQ_GATED(CV, T, B) return launch_row<CV, T, B, KEEP>(gate, ldg, up, ldu, M, F, hq, sh, gq, gs, uq, us, st)
   if (nvec <= 256) AQ_GATED(1, 256, 4);
@@ -430,7 +442,7 @@ extern "C" int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* g
   const Span outs[] = {{dgate, (size_t)ldg * 2, width, M}, {dup, (size_t)ldu * 2, width, M}};
   const Span ins[] = {{dh, (size_t)ldd * 2, width, M}, flat(gq, codes), flat(gs, scales), flat(uq, codes), flat(us, scales)};
   if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
-  // whole warps, up to four rounds a thread
+  // whole warps, ceil(F / 4096) rounds a thread
   const int nv = F / 16, rounds = (nv + 255) / 256, threads = ((nv + rounds - 1) / rounds + 31) / 32 * 32;
   return launch_pdl(silu_mul_backward_kernel, dim3(M), dim3(threads), 0, static_cast<cudaStream_t>(stream), dh, ldd, gq,
                     gs, uq, us, F, dgate, ldg, dup, ldu) == cudaSuccess

@@ -13,7 +13,7 @@
 //          (tensor memory rounds every addition towards zero: 1.3e-6 of the norm with 512
 //          rows, 9.6e-6 with 4096; a bf16 dx is summed there throughout).  What an fp32 dx
 //          takes, at three times the products and more of the conversion (2048 tokens x
-//          9728 n x 1280 k: 325 us for 50).
+//          1280 k x 9728 n: 325 us for 50).
 // The caller may choose either for either dx.
 //
 // A work unit is (128 columns k: one tile column; NT tokens; a range of n).  Per
@@ -43,9 +43,10 @@
 //
 // What bounds it: the transform with 256 tokens a unit (step 810 cycles), the tensor pipe
 // with 512 (step 1100 of 1024 cycles; each dequantized tile serves twice the products), and
-// for long calls the power: 8192 tokens x 14336 n x 4096 k take 1010 us in single CTAs, 910
-// in pairs with 256 tokens and 740 with 512 (1.3 PFLOP/s; a library product sustains 1.38);
-// 2048 x 2560 x 9728 101, 95 and 84; 2048 x 9728 x 2560 102, 92 and 98, and 87 with 384.
+// for long calls the power.  The kernels' own times, in graphs with the form forced (calls take
+// 780 and 100 us): 8192 tokens x 14336 k x 4096 n 1010 us in single CTAs, 910 in pairs with 256
+// tokens and 740 with 512 (1.3 PFLOP/s; a library product sustains 1.38); 2048 x 2560 x 9728 101,
+// 95 and 84; 2048 x 9728 x 2560 102, 92 and 98, and 87 with 384.
 //
 // Whole units go to the CTAs as long as every CTA gets one; the units that are left
 // (all of them for short sequences) may be split over n so that they fill the GPU once
