@@ -515,8 +515,9 @@ int aq_silu_mul_quant(const uint16_t* gate, int ldg, const uint16_t* up, int ldu
  * u = us uq, p = 1 / (1 + exp(-g)),
  *   dgate = dh u p (1 + g (1 - p)),   dup = dh g p        (fp32, rounded once to bf16)
  *  dh  bf16 [M][ldd];  dgate, dup bf16 [M][ldg], [M][ldu]; 16-byte aligned, ld % 8 == 0
- * The rounding of h to its codes is passed through.  dgate and dup must not overlap an
- * input or each other (side by side in one buffer they do not).  Limits and errors as for
+ * The rounding of h to its codes is passed through.  dgate or dup may be dh
+ * itself (same pitch); otherwise they must not overlap an input or each other (side by side in
+ * one buffer they do not).  Limits and errors as for
  * aq_silu_mul_quant.
  */
 int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* gq, const float* gs, const int8_t* uq,

@@ -146,13 +146,16 @@ def test_gated_refuses_overlaps(kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(dg="dh"), dict(du="dh"), dict(du="dh+512"), dict(dg="gq"), dict(du="uq+16"), dict(dg="us"), dict(du="gs"),
+    dict(dg="dh+16"), dict(du="dh+16"), dict(du="dh+512"), dict(dg="dh", ldg=264), dict(du="dh", ldu=264),
+    dict(dg="dh", du="dh+16"), dict(dg="dh", du="dh"), dict(dg="dh", du="gq"), dict(dg="gq"), dict(du="uq+16"), dict(dg="us"), dict(du="gs"),
     dict(dg="du"), dict(du="dg+16"), dict(dh="dg+35328")])
 def test_gated_backward_refuses_overlaps(kw):
+    kw = dict(kw)
     at = {n: (i + 1) * MIB for i, n in enumerate(("dh", "gq", "gs", "uq", "us", "dg", "du"))}
-    for n, where in kw.items():
-        at[n] = at[where.split("+")[0]] + int((where.split("+") + ["0"])[1])
-    assert gated_back(M=70, **at) == ARG
+    for n in [n for n in kw if n in at]:
+        base, _, plus = kw.pop(n).partition("+")
+        at[n] = at[base] + int(plus or 0)
+    assert gated_back(M=70, **at, **kw) == ARG
 
 
 def packed(**kw):

@@ -44,6 +44,17 @@ def test_rows_side_by_side_in_one_buffer(M):
     assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
+@pytest.mark.parametrize("M,F", [(1, 16), (77, 9728), (300, 1104), (33, 40000)])
+def test_gated_backward_in_place(M, F):
+    gate, up, dh = (normal(rng(i), M, F) for i in range(3))
+    kept = aq.aq_silu_mul_quant(gate, up, keep=True)[2:]
+    want = aq.aq_silu_mul_backward(dh, *kept)
+    for i, name in enumerate(("dgate", "dup")):
+        d = dh.clone()
+        got = aq.aq_silu_mul_backward(d, *kept, **{name: d})
+        assert got[i] is d and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_outputs_over_inputs_are_refused():
     M, N = 130, 256
     c = LoraCase(M, N, N, [8], segment_ids(M, 1, 1), seed=5)

@@ -918,7 +918,7 @@ def aq_silu_mul_quant(gate: torch.Tensor, up: torch.Tensor, keep: bool = False, 
 def aq_silu_mul_backward(dh: torch.Tensor, gq: torch.Tensor, gs: torch.Tensor, uq: torch.Tensor, us: torch.Tensor,
                          dgate: torch.Tensor = None, dup: torch.Tensor = None):
     """Gradients of silu(gate) * up from its 8-bit checkpoints: dh bf16 [M][F] ->
-    (dgate, dup) bf16 [M][F]."""
+    (dgate, dup) bf16 [M][F].  dgate or dup may be dh."""
     M, F, ldd, dev = _lead(dh, "dh")
     groups = -(-F // AQ_GATED_GROUP)
     _exact(gq, "gq", torch.int8, dev, (M, F))

@@ -331,6 +331,14 @@ __device__ __forceinline__ void back2(float2 g, float2 u, float2 d, float2& dg, 
   du = __fmul2_rn(d, __fmul2_rn(g, p));
 }
 
+// A load of what the same thread may overwrite afterwards (dgate or dup in place of dh): not by way of the read-only
+// cache.
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // One CTA per row, 16 features per thread and round.
 __global__ void __launch_bounds__(256)
     silu_mul_backward_kernel(const uint16_t* __restrict__ dh, int ldd, const int8_t* __restrict__ gq,
@@ -346,7 +354,7 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
 #pragma unroll 2
   for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v), d0 = __ldg(drow + 2 * v), d1 = __ldg(drow + 2 * v + 1);
+    const uint4 gv = __ldg(grow + v), uv = __ldg(urow + v), d0 = load16(drow + 2 * v), d1 = load16(drow + 2 * v + 1);
     const float sg = __ldg(gs + (size_t)m * groups + v / 8), su = __ldg(us + (size_t)m * groups + v / 8);
     const float2 sg2 = make_float2(sg, sg), su2 = make_float2(su, su);
     uint32_t og[8], ou[8];
@@ -440,7 +448,9 @@ extern "C" int aq_silu_mul_backward(const uint16_t* dh, int ldd, const int8_t* g
   if (((uintptr_t)gs | (uintptr_t)us) & 3) return AQ_ERR_ARG;
   const size_t codes = (size_t)M * F, scales = (size_t)M * ((F + kGroup - 1) / kGroup) * 4, width = (size_t)F * 2;
   const Span outs[] = {{dgate, (size_t)ldg * 2, width, M}, {dup, (size_t)ldu * 2, width, M}};
-  const Span ins[] = {{dh, (size_t)ldd * 2, width, M}, flat(gq, codes), flat(gs, scales), flat(uq, codes), flat(us, scales)};
+  // in place of dh: a thread stores what it has made of its own loads, so rows of one pitch are as good as apart
+  const bool in_place = (dgate == dh && (ldg == ldd || M == 1)) || (dup == dh && (ldu == ldd || M == 1));
+  const Span ins[] = {{in_place ? nullptr : dh, (size_t)ldd * 2, width, M}, flat(gq, codes), flat(gs, scales), flat(uq, codes), flat(us, scales)};
   if (outputs_overlap(outs, ins)) return AQ_ERR_ARG;
   // whole warps, ceil(F / 4096) rounds a thread
   const int nv = F / 16, rounds = (nv + 255) / 256, threads = ((nv + rounds - 1) / rounds + 31) / 32 * 32;
