@@ -316,3 +316,45 @@ def test_a_captured_workspace_clears_its_header_only():
     graph.replay()
     torch.cuda.synchronize()
     assert bool((ws[256:] == 9).all()) and not ws[:16].any() and not ws[24:256].any()
+
+
+# ------------------------------------------------------------------ products of adapters
+
+@pytest.mark.parametrize("M", [8, 60, 150])
+@pytest.mark.parametrize("rank", [2, 31, 48, 70])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products_keep_24_bits_whatever_the_output(M, rank, dtype):
+    """S = (n, -p) with n a whole number of 24 bits and p its leading 16: the output n - p is what the last
+    8 bits hold, in whole numbers, so every sum is exact."""
+    L, K, N = 5, 128, 256
+    g = torch.Generator().manual_seed(M + rank)
+    n = torch.randint(2 ** 23, 2 ** 24, (L,), generator=g).double()
+    hi = n.to(torch.bfloat16).double()
+    p = hi + (n - hi).to(torch.bfloat16).double()
+    assert (n != p).any()
+
+    def row(v):  # 256 a + 16 b + c = v with 8-bit multiples of powers of two
+        v, out = v.clone(), torch.zeros(L, K, dtype=torch.float64)
+        for i, (x, step) in enumerate(((256, 65536), (16, 256), (1, 1))):
+            digit = torch.trunc(v / step)
+            out[:, i] = digit * step / x
+            v -= digit * step
+        assert not v.any()
+        return out
+
+    a = torch.zeros(L, rank, K, dtype=torch.float64)
+    a[:, 0], a[:, 1] = row(n), -row(p)
+    assert torch.equal(a.to(torch.bfloat16).double(), a)
+    b = torch.zeros(L * rank, N, dtype=torch.bfloat16, device="cuda")
+    b[0::rank], b[1::rank] = 1, 1
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = 256, 16, 1
+    ids = torch.arange(M, dtype=torch.int32, device="cuda") % L
+    want = (n - p).to(device="cuda")[ids.long()][:, None].expand(M, N).to(dtype)
+    ad = aq.Adapters(a.reshape(L * rank, K).to(torch.bfloat16).cuda(), b, [rank] * L, [1.0] * L)
+    assert torch.equal(aq.aq_lora_apply(ad, x, ids, out_dtype=dtype), want)
+    # the same through the gradient of x, the tables' sides exchanged
+    back = aq.Adapters(b, a.reshape(L * rank, K).to(torch.bfloat16).cuda(), [rank] * L, [1.0] * L)
+    z = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dx = aq.aq_lora_backward(back, x, ids, torch.zeros(M, rank, device="cuda"), z, dx_dtype=dtype)[2]
+    assert torch.equal(dx, want)

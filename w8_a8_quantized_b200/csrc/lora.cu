@@ -14,7 +14,7 @@
 //
 // Products run on mma.sync (bf16 in, fp32 out): the tables and x, dy are bf16
 // (8-bit codes are exact in bf16), and S and T, fp32, enter as three bf16 terms
-// (24 significant bits; two where the result is rounded to bf16).  Sums are fp32.
+// (24 significant bits).  Sums are fp32.
 //
 // A tile is 64 consecutive tokens.  A kernel lists the adapters that occur in
 // its tile and runs them one after another on the same activations: requests
@@ -292,11 +292,11 @@ struct ExpandArgs {
 // adapters and the products' bf16 terms are made once, then the blocks stream
 // through two buffers of table rows and two of y (16-byte copies, one item
 // ahead); sums go into the y buffer and leave it as 16-byte stores.
-// F32: fp32 y and out, 64 columns a block and three terms of S; otherwise bf16,
-// 128 columns and two terms: 2^-17 of a product, far below the rounding of out.
+// F32: fp32 y and out, 64 columns a block; otherwise bf16, 128 columns.  Three terms
+// of S, 24 bits.
 template <bool F32>
 struct ExpandShape {
-  static constexpr int kBN = F32 ? 64 : 128, kTerms = F32 ? 3 : 2;
+  static constexpr int kBN = F32 ? 64 : 128, kTerms = 3;
   static constexpr int kLdW = kBN + 8;                // bf16 elements
   static constexpr int kElt = F32 ? 4 : 2, kPer16 = 16 / kElt;
   static constexpr int kLdY = kBN + kPer16;           // elements of y: rows of 272 bytes
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const ExpandAr
       uint16_t* d = terms + r * lds + c;
       d[0] = hi;
       d[plane] = mid;
-      if (Sh::kTerms > 2) d[2 * plane] = lo;
+      d[2 * plane] = lo;
     }
   }
 

@@ -340,8 +340,10 @@ __global__ void __launch_bounds__(kSThreads, 2)
 
 // ---------------------------------------------------------------- expand
 // out = y + S B^T:  D[128 tokens][block of columns] = S_terms[128][ranks] B^T[ranks][block],
-// S (fp32) as bf16 terms in shared memory for the whole CTA (three, 24 bits; two,
-// 2^-17 of a product, where out is rounded to bf16), table rows by asynchronous
+// S (fp32) as three bf16 terms, 24 bits, in shared memory for the whole CTA (two, 2^-17 of a
+// product, where out is rounded to bf16 and ranks above 48 leave the third no room: it would
+// take a slot of y, 4001 x 4096 -> 14336 73 us for 65, and bring nothing that shows beside
+// out's rounding, 1.7e-3 of the norm), table rows by asynchronous
 // copies that clear the rows behind the adapter's rank, y and out by TMA through
 // the same buffer.  Blocks of 128 bf16 or 64 fp32 columns: 32 KiB of y.
 // Eight epilogue warps: four per half block, each half with its own stores, so that
@@ -368,13 +370,13 @@ struct ExpandTcArgs {
 
 // kEW: slots of table rows, as many as fit (3 for 64 ranks, 5 up to 32): with k slots
 // k - 1 loads are on their way.
-template <bool F32, int EW>
+template <bool F32, int EW, int T>
 struct ExpandTcShape {
   static constexpr int kEW = EW;
-  static constexpr int kBN = F32 ? 64 : 128, kTerms = F32 ? 3 : 2, kPer16 = F32 ? 4 : 8;
+  static constexpr int kBN = F32 ? 64 : 128, kTerms = T, kPer16 = F32 ? 4 : 8;
   static constexpr int kHalf = 8 * kPer16;  // columns of 128 bytes
   static constexpr int kCtrl = 512;
-  static int smem(int rp) {
+  static constexpr int smem(int rp) {
     return 1024 + kEY * kYBytes + kTerms * kTok * 128 + kEW * rp * kBN * 2 + kCtrl + (int)sizeof(TcList);
   }
 };
@@ -397,10 +399,10 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
                : "memory");
 }
 
-template <bool F32, int kEW>
+template <bool F32, int kEW, int T>
 __global__ void __launch_bounds__(kEThreads, 1)
     lora_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const __grid_constant__ ExpandTcArgs a) {
-  using Sh = ExpandTcShape<F32, kEW>;
+  using Sh = ExpandTcShape<F32, kEW, T>;
   constexpr int BN = Sh::kBN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -775,10 +777,12 @@ cudaError_t launch_shrink(const ShrinkMaps& maps, const ShrinkTcArgs& a, cudaStr
                     maps, a);
 }
 
-template <bool F32, int EW>
+template <bool F32, int EW, int T>
 cudaError_t launch_expand(const ExpandMaps& maps, ExpandTcArgs a, cudaStream_t st) {
-  using Sh = ExpandTcShape<F32, EW>;
-  cudaError_t e = ensure_smem_attr<lora_expand_tc_kernel<F32, EW>>(Sh::smem(EW == 3 ? kMaxTcRank : 32));
+  using Sh = ExpandTcShape<F32, EW, T>;
+  constexpr int most = EW == 5 ? 32 : F32 || T == 2 ? kMaxTcRank : 48;  // ranks
+  static_assert(Sh::smem(most) + 512 <= 227 * 1024, "shared memory");
+  cudaError_t e = ensure_smem_attr<lora_expand_tc_kernel<F32, EW, T>>(Sh::smem(most));
   if (e != cudaSuccess) return e;
   // column ranges per tile: the fewest blocks on the longest path, counting the
   // start of a CTA (list, terms, first copies) as four blocks
@@ -796,7 +800,7 @@ cudaError_t launch_expand(const ExpandMaps& maps, ExpandTcArgs a, cudaStream_t s
   }
   // the rest of the last wave (a thread of the kernel looks after each tile)
   a.extra = a.t.L > 1 && tiles <= kEThreads && a.g < blocks ? ceil_div((long long)tiles * a.g, sms) * sms - tiles * a.g : 0;
-  return launch_pdl(lora_expand_tc_kernel<F32, EW>, dim3(tiles * a.g + a.extra), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st,
+  return launch_pdl(lora_expand_tc_kernel<F32, EW, T>, dim3(tiles * a.g + a.extra), dim3(kEThreads), (size_t)Sh::smem(a.t.rp), st,
                     maps, a);
 }
 
@@ -842,8 +846,9 @@ cudaError_t launch_lora_expand_tc(const aq_lora* ad, bool b_side, const int32_t*
       (y && !map_2d(&maps.y, type, y, t.D, M, (uint64_t)ldy * elt, 128 / elt, kTok, true)))
     return cudaErrorInvalidValue;
   const ExpandTcArgs a{t, ids, counts, M, splits, y != nullptr, y == out, 0, 0, 0, terms ? *terms : TermsArgs{}, p, s, header, stall};
-  if (t.rp <= 32) return f32 ? launch_expand<true, 5>(maps, a, st) : launch_expand<false, 5>(maps, a, st);
-  return f32 ? launch_expand<true, 3>(maps, a, st) : launch_expand<false, 3>(maps, a, st);
+  if (t.rp <= 32) return f32 ? launch_expand<true, 5, 3>(maps, a, st) : launch_expand<false, 5, 3>(maps, a, st);
+  if (f32) return launch_expand<true, 3, 3>(maps, a, st);
+  return t.rp <= 48 ? launch_expand<false, 3, 3>(maps, a, st) : launch_expand<false, 3, 2>(maps, a, st);
 }
 
 }  // namespace aq
