@@ -358,3 +358,33 @@ def test_products_keep_24_bits_whatever_the_output(M, rank, dtype):
     z = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
     dx = aq.aq_lora_backward(back, x, ids, torch.zeros(M, rank, device="cuda"), z, dx_dtype=dtype)[2]
     assert torch.equal(dx, want)
+
+
+def test_exact_input_gradient_past_32_bit_offsets():
+    """Several sums of 512 rows, each added where the last row lies more than 2^31 elements on."""
+    M, N, K = 70, 1600, 256
+    pitch = (1 << 31) // (M - 1) // 16 * 16 + 64
+    w, _ = packed(N, K, 64, 0.5, 7)
+    dy = normal(rng(8), M, N)
+    want = aq.aq_linear_backward(w, dy, out_dtype=torch.float32)
+    out = torch.empty(pitch * (M - 1) + K, device="cuda").as_strided((M, K), (pitch, 1))
+    assert torch.equal(aq.aq_linear_backward(w, dy, out=out), want)
+
+
+def test_exact_input_gradients_of_two_streams_and_a_graph():
+    w, _ = packed(2560, 1280, 128, 0.5, 1)
+    dy = [normal(rng(i), 700, 2560) for i in range(3)]
+    want = [aq.aq_linear_backward(w, d, out_dtype=torch.float32) for d in dy]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = aq.aq_linear_backward(w, dy[0], out_dtype=torch.float32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        graph.replay()
+        outs = []
+        for s, d in zip(streams, dy[1:]):
+            with torch.cuda.stream(s):
+                outs.append(aq.aq_linear_backward(w, d, out_dtype=torch.float32))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip([got] + outs, want))
