@@ -430,7 +430,8 @@ typedef struct aq_lora {
  * Adapters of many requests at once.  With l = ids[m], the adapter of token m:
  *   S[m][i]   = scale[l] * sum_k x[m][k] A_l[i][k]
  *   out[m][n] = y[m][n] + sum_i S[m][i] B_l[n][i]
- * in fp32, out rounded once.  A token whose id is outside [0, L) (-1 by
+ * in fp32, out rounded once (a bf16 out of more than 64 tokens with ranks above 48 takes S to 17
+ * bits, 2^-17 of a product).  A token whose id is outside [0, L) (-1 by
  * convention) or whose adapter has rank 0 gets out = y.  Tokens may carry ids
  * in any order; tokens of one request next to one another are the fast case
  * (a tile of tokens costs a pass per adapter that occurs in it: tiles of 64 tokens with ranks above
